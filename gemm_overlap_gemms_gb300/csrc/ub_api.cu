@@ -23,6 +23,7 @@
 #include <new>
 #include <vector>
 
+#include "ub_attn.h"
 #include "ub_internal.h"
 
 using ubk::GemmParams;
@@ -169,14 +170,17 @@ namespace {
 
 // Control block, in 32-bit words: the readiness flags [0, UB_MAX_TP), the partial-tile
 // flags [UB_MAX_TP, UB_MAX_TP + W) with W = ws_slots * EPI_WARPS, then the abort word, the
-// status word and the gather's per-chunk counters (zero between calls). The words a
-// captured call clears (flags and partial-tile flags) are one contiguous run.
+// status word, the gather's per-chunk counters and the decode attention's join counters
+// (both zero between calls). The words a captured call clears (flags and partial-tile
+// flags) are one contiguous run.
 size_t ws_flag_words(const ub_handle *h) { return static_cast<size_t>(h->ws_slots) * ubk::EPI_WARPS; }
 uint32_t *flags_of(ub_handle *h) { return h->ctrl; }
 uint32_t *ws_flags_of(ub_handle *h) { return h->ctrl + UB_MAX_TP; }
 uint32_t *abort_of(ub_handle *h) { return h->ctrl + UB_MAX_TP + ws_flag_words(h); }
 int32_t *status_of(ub_handle *h) { return reinterpret_cast<int32_t *>(abort_of(h) + 1); }
 uint32_t *gather_counters_of(ub_handle *h) { return abort_of(h) + 8; }  // UB_MAX_TP words
+int join_words(const ub_handle *h) { return ubk::DECODE_COUNTERS * ubk::DECODE_CTAS_PER_SM * h->sm_count; }
+uint32_t *join_counters_of(ub_handle *h) { return gather_counters_of(h) + UB_MAX_TP; }
 
 // Makes the handle's device current for the duration of a call.
 struct DeviceGuard {
@@ -713,6 +717,86 @@ int check_handle(ub_handle *h)
 
 void ubk::set_last_error(const char *msg) { snprintf(g_err, sizeof g_err, "%s", msg); }
 
+// What the attention operators (ub_attn_api.cu) take from a handle.
+int ubk::handle_call(ub_handle_t h, cudaStream_t s, HandleCall *out)
+{
+    uint32_t epoch = 0;
+    if (int rc = begin_call(h, s, epoch, false, false)) return rc;
+    const int sms = h->sm_count - static_cast<int>(h->sm_margin);
+    out->device = h->device;
+    out->sms = sms < 1 ? 1 : sms;
+    out->pdl = static_cast<int>(h->pdl);
+    out->T = h->T;
+    out->abort_word = abort_of(h);
+    out->status = status_of(h);
+    out->timeout_ns = static_cast<uint64_t>(h->timeout_ns);
+    out->epoch = epoch;
+    out->ws = h->ws;
+    out->ws_floats = static_cast<size_t>(h->ws_slots) * PARTIAL_FLOATS;
+    out->join_counters = join_counters_of(h);
+    out->join_words = join_words(h);
+    h->counters.last_T = h->T;
+    return UB_OK;
+}
+
+int ubk::handle_device(ub_handle_t h) { return h->device; }
+int64_t ubk::handle_tokens(ub_handle_t h) { return h->T; }
+
+int ubk::handle_prof_start(ub_handle_t h, int op, cudaStream_t s, bool *timed)
+{
+    ProfileRing &ring = h->prof[op];
+    *timed = h->profile != 0 && ring.count < kMaxProfiled;
+    if (!*timed) return UB_OK;
+    if (static_cast<int>(ring.start.size()) <= ring.count) {
+        cudaEvent_t a, b;
+        UB_CUDA(cudaEventCreate(&a));
+        UB_CUDA(cudaEventCreate(&b));
+        ring.start.push_back(a);
+        ring.stop.push_back(b);
+    }
+    UB_CUDA(cudaEventRecord(ring.start[ring.count], s));
+    return UB_OK;
+}
+
+int ubk::handle_prof_stop(ub_handle_t h, int op, cudaStream_t s, bool timed)
+{
+    if (!timed) return UB_OK;
+    ProfileRing &ring = h->prof[op];
+    UB_CUDA(cudaEventRecord(ring.stop[ring.count], s));
+    ++ring.count;
+    return UB_OK;
+}
+
+void ubk::handle_count_maps(ub_handle_t h, int n) { h->counters.tensor_map_encodes += n; }
+
+int ubk::fail_call(int code, const char *fmt, ...)
+{
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_err, sizeof g_err, fmt, ap);
+    va_end(ap);
+    return code;
+}
+
+int ubk::encode_nd(CUtensorMap *map, const void *ptr, int rank, const uint64_t *dims, const uint64_t *strides,
+                   const uint32_t *box)
+{
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    cuuint64_t d[5], st[5];
+    cuuint32_t b[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        if (i > 0) st[i - 1] = strides[i];
+    }
+    CUresult r = driver().encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank),
+                                 const_cast<void *>(ptr), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(UB_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for a rank-%d tensor", (int)r, rank);
+    return UB_OK;
+}
+
 extern "C" {
 
 const char *ub_last_error(void) { return g_err; }
@@ -771,7 +855,7 @@ int ub_create(int64_t max_tokens, int64_t hidden, int tp, ub_dtype_t dtype, ub_h
     ++h->counters.device_allocations;
     h->max_pairs = h->sm_count / 2 > 0 ? h->sm_count / 2 : 1;
     h->ws_slots = 2 * (h->sm_count > 0 ? h->sm_count : 1);
-    h->ctrl_bytes = (UB_MAX_TP + ws_flag_words(h) + 8 + UB_MAX_TP) * sizeof(uint32_t);
+    h->ctrl_bytes = (UB_MAX_TP + ws_flag_words(h) + 8 + UB_MAX_TP + join_words(h)) * sizeof(uint32_t);
     e = cudaMalloc(reinterpret_cast<void **>(&h->ctrl), h->ctrl_bytes);
     if (e != cudaSuccess) return cleanup(cuda_fail(e, "cudaMalloc(control block)"));
     ++h->counters.device_allocations;

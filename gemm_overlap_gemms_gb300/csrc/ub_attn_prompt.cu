@@ -1,0 +1,712 @@
+// Causal attention of packed prompts, or of chunks of prompts over the paged cache.
+//
+//   O_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale * q_i . k_j - m_i),  j <= pos_i
+//
+// in one pass over the keys: a running maximum m and sum l per row, and O rescaled by
+// exp(m_old - m_new) when the maximum grows. The rescaling is put off while the maximum
+// has grown by less than 2^8: the weights then stay below 2^8, which neither BF16 nor the
+// fp32 sums mind, and the division by l at the end cancels the choice of m.
+//
+// A work item is 256 rows, two q tiles of 128: consecutive tokens of one sequence, and,
+// where query heads share a key/value head, a power of two of those heads per token (row =
+// token * pack + head). Per 128 keys and q tile the tensor core computes S = Q K^T (128 x
+// 128, both operands from shared memory) and O += P V (P from TMEM, V read MN-major); the
+// softmax in between is per TMEM lane, one thread per row, without shuffles.
+//
+// Roles (16 warps, one CTA per SM, persistent over items):
+//   warps 0-3, 4-7   softmax of q tile 0 and 1: S from TMEM, P back into the columns of S
+//   warps 8-11       correction: rescale O in TMEM when a row's maximum grew; epilogue
+//   warp 12          loads (TMA): Q, then K and V tiles in a ring
+//   warp 13          MMA issue: S_0, S_1, then per key tile O_0, S_0', O_1, S_1'
+//   warp 14          zeroes the rows of V past a sequence's end in its last tile (their
+//                    weights are zero, their values may be anything)
+//   warp 15          schedule: the CTA's items, longest first over the whole call
+// The two q tiles alternate, so that the tensor core works on one while the softmax of
+// the other runs. TMEM: S_0, S_1 (128 columns each), O_0, O_1.
+//
+// Only the keys that a q tile needs are multiplied: the last key tile of a q tile is cut
+// to 16 keys (N of the first product, K of the second).
+#include <cuda_bf16.h>
+
+#include "ub_attn.h"
+#include "ub_device.cuh"
+#include "ub_internal.h"
+
+namespace ubk {
+namespace {
+
+constexpr int PR_THREADS = 512;
+constexpr int ITEMS = 4;                 // schedule ring
+constexpr int TM_S = 0, TM_O = 256;      // TMEM columns: S_i at 128 i, O_i at 256 + 128 i
+constexpr float RESCALE_LOG2 = 8.f;      // growth of the maximum (log2) that is put off
+
+template <int D>
+struct PromptShape {
+    static constexpr int TILE_BYTES = PROMPT_KEYS * D * 2;
+    static constexpr int HALF_BYTES = PROMPT_KEYS * 128;  // 64 columns of a tile
+    static constexpr int STAGES = D == 128 ? 5 : 10;
+    static constexpr int SMEM = 1024 + 2 * TILE_BYTES + STAGES * TILE_BYTES + 1024 + 768;
+    static_assert(SMEM <= 232448, "shared memory");
+};
+
+// One work item as the schedule warp publishes it.
+struct Item {
+    int row0;    // first token (row of q); -1: no more items
+    int ntok;    // tokens
+    int off;     // position of the first token
+    int len;     // keys of the sequence
+    int src;     // first key row (packed) or sequence (paged)
+    int unit;
+};
+
+struct Range2 {
+    int lim[2];  // keys that q tile i reaches
+    int n[2];    // its key tiles
+    int tok[2];  // its tokens
+    int nmax;
+    int limmax;
+};
+__device__ __forceinline__ Range2 ranges(const Item &it, int tpt)
+{
+    Range2 r;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        int tok = it.ntok - i * tpt;
+        tok = tok < 0 ? 0 : (tok > tpt ? tpt : tok);
+        int lim = tok > 0 ? it.off + i * tpt + tok : 0;
+        lim = lim < 0 ? 0 : (lim > it.len ? it.len : lim);
+        r.tok[i] = tok;
+        r.lim[i] = lim;
+        r.n[i] = (lim + PROMPT_KEYS - 1) / PROMPT_KEYS;
+    }
+    r.nmax = r.n[0] > r.n[1] ? r.n[0] : r.n[1];
+    r.limmax = r.lim[0] > r.lim[1] ? r.lim[0] : r.lim[1];
+    return r;
+}
+// Keys of tile j that are multiplied, for a q tile that reaches `lim` keys: a multiple of 16.
+__device__ __forceinline__ int extent(int lim, int j)
+{
+    const int left = lim - j * PROMPT_KEYS;
+    return left >= PROMPT_KEYS ? PROMPT_KEYS : (left + 15) & ~15;
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z, int w)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// A from TMEM: 128 lanes x 8 columns, two bf16 of K per column.
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *v)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(v[0]),
+        "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]),
+        "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
+        "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// kind::f16, fp32 accumulator, bf16 operands, M = 128.
+__device__ __forceinline__ constexpr uint32_t prompt_idesc(int n, bool b_mn)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? (1u << 16) : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
+           (static_cast<uint32_t>(128 >> 4) << 24);
+}
+
+// V tile, MN-major (the head dimension contiguous): atoms of 8 keys x 64 columns, 1024
+// bytes apart along the keys, the second 64 columns `half` bytes further.
+__device__ __forceinline__ uint64_t smem_desc_v(uint32_t saddr, uint32_t half)
+{
+    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(half >> 4) << 16) |
+           (static_cast<uint64_t>(1024u >> 4) << 32) | (static_cast<uint64_t>(1u) << 46) | (static_cast<uint64_t>(2u) << 61);
+}
+
+// ---------------------------------------------------------------- schedule
+
+struct SeqInfo {
+    int start, n, len, off;
+};
+__device__ __forceinline__ SeqInfo seq_info(const PromptParams &p, int s)
+{
+    SeqInfo q;
+    int a = p.b.seq_starts[s], z = p.b.seq_starts[s + 1];
+    a = a < 0 ? 0 : (a > p.T ? p.T : a);
+    z = z < a ? a : (z > p.T ? p.T : z);
+    q.start = a;
+    q.n = z - a;
+    if (p.paged) {
+        const int64_t most = static_cast<int64_t>(p.b.table_width) << p.b.page_shift;
+        const int len = p.b.kv_lens[s];
+        q.len = len < 0 ? 0 : (len > most ? static_cast<int>(most) : len);
+    } else {
+        q.len = q.n;
+    }
+    q.off = q.len - q.n;
+    return q;
+}
+// Items (token tiles) of the sequence that reach at least `c` key tiles.
+__device__ __forceinline__ int items_from(const SeqInfo &q, int c, int tokens)
+{
+    const int nt = (q.n + tokens - 1) / tokens;
+    if (c <= 0) return nt;
+    const int64_t x = static_cast<int64_t>(c - 1) * PROMPT_KEYS;
+    if (q.len <= x) return 0;
+    const int64_t t = x < q.off ? 0 : (x - q.off) / tokens;
+    return nt - (t < nt ? static_cast<int>(t) : nt);
+}
+__device__ __forceinline__ int warp_sum(int v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+__device__ int count_from(const PromptParams &p, int c, int tokens, int lane)
+{
+    int sum = 0;
+    for (int i = lane; i < p.b.n_seqs; i += 32) sum += items_from(seq_info(p, i), c, tokens);
+    return warp_sum(sum);
+}
+
+// Item of rank g in the order "most key tiles first" (ties: by sequence, then by tile).
+__device__ Item item_at(const PromptParams &p, int g, int cmax, int tokens, int lane)
+{
+    int lo = 0, hi = cmax;  // count(lo) > g; find the largest such level
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (count_from(p, mid, tokens, lane) > g) lo = mid;
+        else hi = mid - 1;
+    }
+    int r = g - count_from(p, lo + 1, tokens, lane);
+    Item it{-1, 0, 0, 0, 0, 0};
+    for (int i0 = 0; i0 < p.b.n_seqs; i0 += 32) {
+        SeqInfo q{0, 0, 0, 0};
+        int mine = 0, from = 0;
+        if (i0 + lane < p.b.n_seqs) {
+            q = seq_info(p, i0 + lane);
+            from = items_from(q, lo, tokens);
+            mine = from - items_from(q, lo + 1, tokens);
+        }
+        int upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += x;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, upto > r);
+        if (past != 0u) {
+            const int l = __ffs(static_cast<int>(past)) - 1;
+            const int nt = (q.n + tokens - 1) / tokens;
+            const int tile = nt - from + (r - (upto - mine));
+            it.row0 = q.start + tile * tokens;
+            it.ntok = q.n - tile * tokens < tokens ? q.n - tile * tokens : tokens;
+            it.off = q.off + tile * tokens;
+            it.len = q.len;
+            it.src = p.paged ? i0 + lane : q.start;
+            it.row0 = __shfl_sync(0xffffffffu, it.row0, l);
+            it.ntok = __shfl_sync(0xffffffffu, it.ntok, l);
+            it.off = __shfl_sync(0xffffffffu, it.off, l);
+            it.len = __shfl_sync(0xffffffffu, it.len, l);
+            it.src = __shfl_sync(0xffffffffu, it.src, l);
+            return it;
+        }
+        r -= __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return it;
+}
+
+// ---------------------------------------------------------------- kernel
+
+template <int D>
+__global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __grid_constant__ PromptParams p)
+{
+    using Sh = PromptShape<D>;
+    constexpr int NST = Sh::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sm_q = smem_u32(base), sm_kv = sm_q + 2 * Sh::TILE_BYTES;
+    float *sm_scale = reinterpret_cast<float *>(base + (2 + NST) * Sh::TILE_BYTES);  // [2][128]
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm_scale + 256);
+    const uint32_t b0 = smem_u32(bars);
+    const uint32_t kv_full = b0, kv_empty = b0 + 8 * NST, v_raw = b0 + 16 * NST;
+    const uint32_t misc = b0 + 24 * NST;
+    const uint32_t q_full = misc, q_empty = misc + 16, s_full = misc + 32, p_full = misc + 48, corr = misc + 64,
+                   sc_full = misc + 80, sc_empty = misc + 96, o_full = misc + 112, drain = misc + 128,
+                   it_full = misc + 136, it_empty = it_full + 8 * ITEMS;
+    Item *items = reinterpret_cast<Item *>(reinterpret_cast<uint8_t *>(bars) + 24 * NST + 136 + 16 * ITEMS);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(items + ITEMS);
+    static_assert(24 * NST + 136 + 16 * ITEMS + sizeof(Item) * ITEMS + 4 <= 768, "barrier area");
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NST; ++i) {
+            mbar_init(kv_full + 8 * i, 1);
+            mbar_init(kv_empty + 8 * i, 1);
+            mbar_init(v_raw + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(q_full + 8 * i, 1);
+            mbar_init(q_empty + 8 * i, 1);
+            mbar_init(s_full + 8 * i, 1);
+            mbar_init(p_full + 8 * i, 4);
+            mbar_init(corr + 8 * i, 4);
+            mbar_init(sc_full + 8 * i, 4);
+            mbar_init(sc_empty + 8 * i, 4);
+            mbar_init(o_full + 8 * i, 1);
+        }
+        mbar_init(drain, 1);
+        for (int i = 0; i < ITEMS; ++i) {
+            mbar_init(it_full + 8 * i, 1);
+            mbar_init(it_empty + 8 * i, 15);
+        }
+        fence_mbar_init();
+        prefetch_tmap(&p.tmQ);
+        prefetch_tmap(&p.tmK);
+        prefetch_tmap(&p.tmV);
+    }
+    if (warp == 13) tmem_alloc(smem_u32(tmem_slot), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();
+    pdl_trigger();
+
+    const WaitCtx wc{p.abort_word, p.b.status, p.timeout_ns, p.epoch};
+    const int pack = 1 << p.pack_shift;
+    const int tpt = PROMPT_ROWS >> p.pack_shift;  // tokens per q tile
+    bool alive = true;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        alive = __all_sync(0xffffffffu, mbar_wait(bar, parity, wc)) != 0;
+        return alive;
+    };
+    auto arrive = [&](uint32_t bar) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+    };
+    // The k-th item of this CTA; false at the end (or when a wait ran out).
+    auto next_item = [&](uint32_t k, Item &it) {
+        const uint32_t slot = k % ITEMS;
+        if (!wait(it_full + 8 * slot, (k / ITEMS) & 1)) return false;
+        it = items[slot];
+        arrive(it_empty + 8 * slot);
+        return it.row0 >= 0;
+    };
+
+    if (warp < 8) {
+        // ------------------------------------------------------------ softmax
+        const int i = warp >> 2;                       // q tile
+        const int row = (warp & 3) * 32 + lane;
+        const uint32_t ts = tmem + TM_S + i * 128 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const float sl = p.scale * 1.4426950408889634f;
+        uint32_t n_s = 0, n_sc = 0;                    // phases used
+        Item it;
+        for (uint32_t k = 0; next_item(k, it); ++k) {
+            const Range2 r = ranges(it, tpt);
+            if (r.n[i] == 0) continue;
+            const int token = i * tpt + (row >> p.pack_shift);
+            int reach = it.off + token + 1;            // keys this row sees
+            reach = reach > it.len ? it.len : reach;
+            float m = -INFINITY, l = 0.f;
+            for (int j = 0; j < r.n[i]; ++j) {
+                if (!wait(s_full + 8 * i, n_s & 1)) break;
+                ++n_s;
+                tc_fence_after();
+                float s[128];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, reinterpret_cast<uint32_t *>(s) + c * 32);
+                tmem_wait_ld();
+                const int cols = reach - j * PROMPT_KEYS;
+                if (cols < PROMPT_KEYS) {
+#pragma unroll
+                    for (int c = 0; c < 128; ++c)
+                        if (c >= cols) s[c] = -INFINITY;
+                }
+                float mx[4] = {m, m, m, m};
+#pragma unroll
+                for (int c = 0; c < 128; c += 4)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], s[c + u]);
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                float f = 1.f;
+                if (j == 0) {
+                    m = top;
+                } else if ((top - m) * sl > RESCALE_LOG2) {  // also from m = -inf
+                    f = ex2((m - top) * sl);
+                    m = top;
+                }
+                if (j > 0) {
+                    if (!wait(sc_empty + 8 * i, (n_sc & 1) ^ 1)) break;
+                    sm_scale[i * 128 + row] = f;
+                    arrive(sc_full + 8 * i);
+                    ++n_sc;
+                }
+                const float ref = m == -INFINITY ? 0.f : m * sl;  // no key yet: every weight is zero
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                uint32_t pk[64];
+#pragma unroll
+                for (int c = 0; c < 128; c += 4) {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        s[c + u] = ex2(fmaf(s[c + u], sl, -ref));
+                        sum[u] += s[c + u];
+                    }
+                    pk[c / 2] = pack_bf16x2(__float_as_uint(s[c]), __float_as_uint(s[c + 1]));
+                    pk[c / 2 + 1] = pack_bf16x2(__float_as_uint(s[c + 2]), __float_as_uint(s[c + 3]));
+                }
+                tmem_st32(ts, pk);
+                tmem_st32(ts + 32, pk + 32);
+                tmem_wait_st();
+                tc_fence_before();
+                arrive(p_full + 8 * i);
+                l = l * f + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+            }
+            if (!alive) break;
+            if (!wait(sc_empty + 8 * i, (n_sc & 1) ^ 1)) break;
+            sm_scale[i * 128 + row] = l;
+            arrive(sc_full + 8 * i);
+            ++n_sc;
+            if (p.lse && token < it.ntok) {
+                const int h = (it.unit << p.pack_shift) + (row & (pack - 1));
+                p.lse[static_cast<int64_t>(it.row0 + token) * p.heads + h] = l > 0.f ? m * p.scale + logf(l) : (l == 0.f ? -INFINITY : l);
+            }
+        }
+    } else if (warp < 12) {
+        // ------------------------------------------------------------ correction, epilogue
+        const int row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        uint32_t n_sc[2] = {0, 0}, n_o[2] = {0, 0};
+        Item it;
+        for (uint32_t k = 0; next_item(k, it); ++k) {
+            const Range2 r = ranges(it, tpt);
+            for (int j = 0; j < r.nmax && alive; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (j >= r.n[i] || !alive) continue;
+                    if (j > 0) {
+                        if (!wait(sc_full + 8 * i, n_sc[i] & 1)) continue;
+                        ++n_sc[i];
+                        const float f = sm_scale[i * 128 + row];
+                        arrive(sc_empty + 8 * i);
+                        if (__any_sync(0xffffffffu, f != 1.f)) {
+                            tc_fence_after();  // the softmax saw S of this tile: O of the last one is complete
+                            const uint32_t to = tmem + TM_O + i * 128 + lanes;
+#pragma unroll
+                            for (int c = 0; c < D; c += 32) {
+                                uint32_t v[32];
+                                tmem_ld32(to + c, v);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int u = 0; u < 32; ++u) v[u] = __float_as_uint(__uint_as_float(v[u]) * f);
+                                tmem_st32(to + c, v);
+                            }
+                            tmem_wait_st();
+                            tc_fence_before();
+                        }
+                    }
+                    arrive(corr + 8 * i);
+                }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (r.tok[i] == 0 || !alive) continue;
+                const int token = i * tpt + (row >> p.pack_shift);
+                const int h = (it.unit << p.pack_shift) + (row & (pack - 1));
+                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + (it.row0 + token) * p.o_row + h * p.o_head;
+                float inv = 0.f;
+                bool none = true;                      // no key: zeros
+                if (r.n[i] > 0) {
+                    if (!wait(sc_full + 8 * i, n_sc[i] & 1)) continue;
+                    ++n_sc[i];
+                    const float l = sm_scale[i * 128 + row];
+                    arrive(sc_empty + 8 * i);
+                    none = l == 0.f;
+                    inv = 1.f / l;
+                    if (!wait(o_full + 8 * i, n_o[i] & 1)) continue;
+                    ++n_o[i];
+                    tc_fence_after();
+                } else if (p.lse && token < it.ntok) {
+                    p.lse[static_cast<int64_t>(it.row0 + token) * p.heads + h] = -INFINITY;
+                }
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t v[32];
+                    if (r.n[i] > 0) {
+                        tmem_ld32(tmem + TM_O + i * 128 + lanes + c, v);
+                        tmem_wait_ld();
+                    }
+                    if (token < it.ntok) {
+#pragma unroll
+                        for (int u = 0; u < 32; u += 8) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                w[e] = none ? 0u
+                                            : pack_bf16x2(__float_as_uint(__uint_as_float(v[u + 2 * e]) * inv),
+                                                          __float_as_uint(__uint_as_float(v[u + 2 * e + 1]) * inv));
+                            *reinterpret_cast<uint4 *>(dst + c + u) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                }
+                tc_fence_before();
+            }
+            if (!alive) break;
+        }
+    } else if (warp == 12) {
+        // ------------------------------------------------------------ loads
+        uint32_t c = 0, n_q[2] = {0, 0};               // ring position, Q loads so far
+        Item it;
+        const int box = PROMPT_KEYS < (1 << p.b.page_shift) ? PROMPT_KEYS : (1 << p.b.page_shift);
+        constexpr int HALVES = D / 64;
+        for (uint32_t k = 0; next_item(k, it); ++k) {
+            const Range2 r = ranges(it, tpt);
+            const int kvh = (it.unit << p.pack_shift) / p.group;
+            const int32_t *table = p.paged ? p.b.page_table + it.src * p.b.table_row : nullptr;
+            const int pages = p.paged ? (it.len + (1 << p.b.page_shift) - 1) >> p.b.page_shift : 0;
+            int cached0 = 0, cached_n = 0, ids = -1;   // page ids, one per lane
+            auto load_q = [&](int i) {
+                if (r.n[i] == 0) return;
+                if (n_q[i] > 0 && !wait(q_empty + 8 * i, (n_q[i] - 1) & 1)) return;
+                ++n_q[i];
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(q_full + 8 * i, Sh::TILE_BYTES);
+                    for (int hf = 0; hf < HALVES; ++hf)
+                        tma_load_3d(sm_q + i * Sh::TILE_BYTES + hf * Sh::HALF_BYTES, &p.tmQ, q_full + 8 * i, hf * 64,
+                                    it.unit << p.pack_shift, it.row0 + i * tpt);
+                }
+                __syncwarp();
+            };
+            load_q(0);
+            for (int j = 0; j < r.nmax && alive; ++j) {
+                const int key0 = j * PROMPT_KEYS;
+                // every key that is multiplied is loaded (pages past the length as zeros)
+                const int n_box = p.paged ? (extent(r.limmax, j) + box - 1) / box : 1;
+                const int page0 = key0 >> p.b.page_shift;
+                const int boxes = PROMPT_KEYS / box;
+                if (p.paged && page0 + boxes > cached0 + cached_n) {
+                    cached0 = page0;
+                    cached_n = 32;
+                    ids = cached0 + lane < pages ? table[cached0 + lane] : -1;
+                    if (cached0 + lane < pages && (ids < 0 || ids >= p.b.num_pages)) {
+                        atomicCAS(p.b.status, 0, UB_ERR_ARG);
+                        ids = -1;                      // outside the tensor: filled with zeros
+                    }
+                }
+#pragma unroll
+                for (int kind = 0; kind < 2 && alive; ++kind, ++c) {
+                    const uint32_t st = c % NST;
+                    if (c >= NST && !wait(kv_empty + 8 * st, (c / NST - 1) & 1)) break;
+                    // The last tile of V goes through the zeroing warp when it ends inside 16 keys.
+                    const bool fix = kind == 1 && j == r.nmax - 1 && extent(r.limmax, j) > it.len - key0;
+                    const uint32_t bar = (fix ? v_raw : kv_full) + 8 * st;
+                    const CUtensorMap *map = kind == 0 ? &p.tmK : &p.tmV;
+                    const uint32_t dst = sm_kv + st * Sh::TILE_BYTES;
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(bar, p.paged ? n_box * HALVES * box * 128 : Sh::TILE_BYTES);
+                    __syncwarp();
+                    if (p.paged) {
+                        const int bx = lane / HALVES, hf = lane - bx * HALVES;
+                        const int page = __shfl_sync(0xffffffffu, ids, (page0 - cached0 + bx) & 31);
+                        if (bx < n_box)
+                            tma_load_4d(dst + hf * Sh::HALF_BYTES + bx * box * 128, map, bar, hf * 64,
+                                        boxes > 1 ? 0 : key0 & ((1 << p.b.page_shift) - 1), kvh, page);
+                    } else if (lane < HALVES) {
+                        tma_load_3d(dst + lane * Sh::HALF_BYTES, map, bar, lane * 64, kvh, it.src + key0);
+                    }
+                    __syncwarp();
+                }
+                if (j == 0 && alive) load_q(1);
+            }
+            if (!alive) break;
+        }
+    } else if (warp == 13) {
+        // ------------------------------------------------------------ MMA issue
+        uint32_t c = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
+        Item it;
+        // S_i = Q_i K^T of the tile in ring slot cs
+        auto issue_s = [&](int i, uint32_t cs, int ext, bool last) {
+            if (lane == 0) {
+                const uint32_t q = sm_q + i * Sh::TILE_BYTES, kk = sm_kv + (cs % NST) * Sh::TILE_BYTES;
+                const uint32_t idesc = prompt_idesc(ext, false);
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s) {
+                    const uint32_t o = (s / 4) * Sh::HALF_BYTES + (s % 4) * 32;
+                    umma_ss(tmem + TM_S + i * 128, smem_desc_sw128(q + o), smem_desc_sw128(kk + o), idesc, s > 0);
+                }
+                umma_commit(s_full + 8 * i);
+                if (last) umma_commit(q_empty + 8 * i);
+            }
+            __syncwarp();
+        };
+        for (uint32_t k = 0; next_item(k, it); ++k) {
+            const Range2 r = ranges(it, tpt);
+            if (r.nmax == 0) continue;
+            if (!wait(kv_full + 8 * (c % NST), (c / NST) & 1)) break;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (r.n[i] == 0 || !alive) continue;
+                if (!wait(q_full + 8 * i, n_q[i] & 1)) continue;
+                ++n_q[i];
+                tc_fence_after();
+                issue_s(i, c, extent(r.lim[i], 0), r.n[i] == 1);
+            }
+            if (!alive) break;
+            if (lane == 0) umma_commit(kv_empty + 8 * (c % NST));
+            __syncwarp();
+            for (int j = 0; j < r.nmax && alive; ++j) {
+                const uint32_t cv = c + 2 * j + 1, ck = cv + 1;
+                const bool more = j + 1 < r.nmax;
+                if (!wait(kv_full + 8 * (cv % NST), (cv / NST) & 1)) break;
+                if (more && !wait(kv_full + 8 * (ck % NST), (ck / NST) & 1)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (j >= r.n[i] || !alive) continue;
+                    if (!wait(corr + 8 * i, n_p[i] & 1) || !wait(p_full + 8 * i, n_p[i] & 1)) continue;
+                    ++n_p[i];
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint32_t v = sm_kv + (cv % NST) * Sh::TILE_BYTES;
+                        const int steps = extent(r.lim[i], j) / 16;
+                        constexpr uint32_t idesc = prompt_idesc(D, true);
+                        for (int s = 0; s < steps; ++s)
+                            umma_ts(tmem + TM_O + i * 128, tmem + TM_S + i * 128 + s * 8,
+                                    smem_desc_v(v + s * 2048, Sh::HALF_BYTES), idesc, j > 0 || s > 0);
+                        if (j == r.n[i] - 1) umma_commit(o_full + 8 * i);
+                    }
+                    __syncwarp();
+                    if (j + 1 < r.n[i]) issue_s(i, ck, extent(r.lim[i], j + 1), j + 2 == r.n[i]);
+                }
+                if (!alive) break;
+                if (lane == 0) {
+                    umma_commit(kv_empty + 8 * (cv % NST));
+                    if (more) umma_commit(kv_empty + 8 * (ck % NST));
+                }
+                __syncwarp();
+            }
+            if (!alive) break;
+            c += 2 * r.nmax;
+        }
+        // everything issued has completed before TMEM goes back
+        if (lane == 0) {
+            umma_commit(drain);
+            mbar_wait_drain(drain, 0, p.timeout_ns);
+        }
+        __syncwarp();
+    } else if (warp == 14) {
+        // ------------------------------------------------------------ V past the end
+        uint32_t c = 0, used = 0;                      // ring position; phase bit per stage of v_raw
+        Item it;
+        for (uint32_t k = 0; next_item(k, it); ++k) {
+            const Range2 r = ranges(it, tpt);
+            if (r.nmax == 0) continue;
+            const int j = r.nmax - 1, valid = it.len - j * PROMPT_KEYS, ext = extent(r.limmax, j);
+            if (ext > valid) {
+                const uint32_t st = (c + 2 * j + 1) % NST;
+                if (!wait(v_raw + 8 * st, (used >> st) & 1)) break;
+                used ^= 1u << st;
+                const uint32_t v = sm_kv + st * Sh::TILE_BYTES;
+                for (int u = lane; u < (ext - valid) * (D / 8); u += 32) {
+                    const int rr = valid + u / (D / 8), ch = u % (D / 8);
+                    st_shared_v4(v + (ch / 8) * Sh::HALF_BYTES + rr * 128 + (ch % 8) * 16, 0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_shared();
+                arrive(kv_full + 8 * st);
+            }
+            c += 2 * r.nmax;
+        }
+    } else {
+        // ------------------------------------------------------------ schedule
+        const int tokens = 2 * tpt;
+        int cmax = 0, tiles = 0;
+        for (int i = lane; i < p.b.n_seqs; i += 32) {
+            const SeqInfo q = seq_info(p, i);
+            const int n = (q.len + PROMPT_KEYS - 1) / PROMPT_KEYS;
+            if (q.n > 0 && n > cmax) cmax = n;
+            tiles += (q.n + tokens - 1) / tokens;
+        }
+        tiles = warp_sum(tiles);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) cmax = max(cmax, __shfl_xor_sync(0xffffffffu, cmax, o));
+        const int64_t total = static_cast<int64_t>(tiles) * p.units;
+        // Longest first, dealt forth and back over the CTAs.
+        uint32_t k = 0;
+        for (;; ++k) {
+            const int64_t round = static_cast<int64_t>(k) * gridDim.x;
+            const int64_t g = round + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            Item it{-1, 0, 0, 0, 0, 0};
+            if (g < total) {
+                it = item_at(p, static_cast<int>(g / p.units), cmax, tokens, lane);
+                it.unit = static_cast<int>(g % p.units);
+            }
+            const uint32_t slot = k % ITEMS;
+            if (k >= ITEMS && !wait(it_empty + 8 * slot, (k / ITEMS - 1) & 1)) break;
+            if (lane == 0) items[slot] = it;
+            arrive(it_full + 8 * slot);
+            if (it.row0 < 0) break;
+        }
+    }
+
+    if (!alive) settle(200000);  // a wait ran out: copies already issued land first
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 13) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+cudaError_t launch_prompt(const PromptParams &p, int grid, cudaStream_t s)
+{
+    const cudaError_t e = raise_smem_limit(reinterpret_cast<const void *>(ub_attn_prompt_kernel<D>), PromptShape<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_ex(ub_attn_prompt_kernel<D>, p, grid, PR_THREADS, PromptShape<D>::SMEM, 1, p.pdl != 0, s);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_prompt(const PromptParams &p, int grid, cudaStream_t s)
+{
+    return p.head_dim == 128 ? launch_prompt<128>(p, grid, s) : launch_prompt<64>(p, grid, s);
+}
+
+}  // namespace ubk

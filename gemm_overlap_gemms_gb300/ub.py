@@ -13,7 +13,9 @@ hidden], tp_size, dtype=torch.bfloat16)`` registers a buffer at capacity, and
 from __future__ import annotations
 
 import ctypes
+import math
 import os
+import struct
 
 import torch
 
@@ -30,7 +32,8 @@ CODES = {v: k for k, v in ERRORS.items()}
 OPTIONS = {"sm_margin": 1, "timeout_ns": 2, "self_rank": 3, "drop_flag": 4, "profile": 5,
            "cta_pair": 6, "streamk": 7, "copy_streams": 8, "gather_kernel": 9, "skinny": 10, "pdl": 11,
            "bulk_beside": 12, "gather_chain": 13}
-OPS = {"ag": 0, "rs": 1, "ag_swiglu": 2, "ag_kn": 3, "rs_kn": 4, "wgrad": 5, "reduce_scatter": 6}
+OPS = {"ag": 0, "rs": 1, "ag_swiglu": 2, "ag_kn": 3, "rs_kn": 4, "wgrad": 5, "reduce_scatter": 6, "kv_append": 7,
+       "attn_prompt": 8, "attn_decode": 9}
 MAX_TP = 8
 EXPORTS = [
     "ub_create", "ub_destroy", "ub_set_active_shape", "ub_set_active_shape_nd",
@@ -40,7 +43,7 @@ EXPORTS = [
     "ag_gemm_noalloc", "ag_gemm_swiglu", "ag_gemm_kn", "gemm_rs_kn", "ub_wgrad",
     "ub_allgather", "ub_reduce_scatter", "ub_plan_tail_split", "ub_plan_path",
     "ub_plan_ag_self_head", "ag_gemm_from_buffer", "ub_plan_gather_parts", "ub_stream_read",
-    "ub_plan_ag_group_m",
+    "ub_plan_ag_group_m", "ub_kv_append", "ub_attn_prompt", "ub_attn_decode",
 ]
 NOALLOC_MAX_ELEMS = 16 * 1024 * 1024
 
@@ -110,6 +113,9 @@ def load():
         "ub_plan_path": [I64, I64, I64, I64, I64, I, I, I, ctypes.POINTER(I), ctypes.POINTER(I)],
         "ub_plan_ag_self_head": [I64, I, I, I64, I64],
         "ub_plan_ag_group_m": [I64, I, I, I64, I64],
+        "ub_kv_append": [P, ctypes.c_char_p, P],
+        "ub_attn_prompt": [P, ctypes.c_char_p, P],
+        "ub_attn_decode": [P, ctypes.c_char_p, P],
         "ub_plan_gather_parts": [I, I, I64, I64, ctypes.POINTER(I), ctypes.POINTER(I64), ctypes.POINTER(I64),
                                  ctypes.POINTER(I)],
     }
@@ -210,6 +216,55 @@ def _bf16_cuda(t: torch.Tensor, name: str, shape=None, device=None):
         raise ValueError("%s must be contiguous" % name)
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+
+
+# ub_attn_t of include/ub.h, packed by one struct call instead of a ctypes structure (a
+# decoding step's call takes microseconds): 8 ints, scale, reserved, 4 sizes, four
+# [data, row, head], two [data, page, head, row], six pointers.
+_ATTN = struct.Struct("=I7ifI4q" + "Q2q" * 4 + "Q3q" * 2 + "6Q")
+_NO_HEADS = (0, 0, 0)
+_NO_PAGES = (0, 0, 0, 0)
+
+
+def _attn_error(t, name: str, dtype, device, what: str):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype != dtype or not t.is_cuda:
+        raise TypeError("%s must be a CUDA %s tensor, got %s on %s" % (name, dtype, t.dtype, t.device))
+    if t.device != device:
+        raise ValueError("%s is on %s, the user buffer on %s" % (name, t.device, device))
+    raise ValueError("%s must be %s, got %s with strides %s" % (name, what, tuple(t.shape), t.stride()))
+
+
+def _heads_view(t: torch.Tensor, name: str, T: int, D: int | None, device):
+    """([data, row, head], heads, head_dim) of a [T, heads, D] bf16 view with a contiguous head dimension."""
+    if (not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.device != device or t.dim() != 3
+            or t.shape[0] != T or (D is not None and t.shape[2] != D) or t.stride(2) != 1):
+        _attn_error(t, name, torch.bfloat16, device, "[%d, heads, %s] with a contiguous last dimension" % (T, D or "head_dim"))
+    row, head, _ = t.stride()
+    return (t.data_ptr(), row, head), t.shape[1], t.shape[2]
+
+
+def _pages_view(t: torch.Tensor, name: str, D: int, device, like=None):
+    if (not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.device != device or t.dim() != 4
+            or t.shape[3] != D or t.stride(3) != 1 or (like is not None and t.shape != like)):
+        _attn_error(t, name, torch.bfloat16, device, "[pages, kv_heads, page_size, %d] with a contiguous last dimension%s"
+                    % (D, "" if like is None else ", as k_cache"))
+    return (t.data_ptr(),) + t.stride()[:3]
+
+
+def _ints(t: torch.Tensor, name: str, shape, device) -> int:
+    if (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device or tuple(t.shape) != shape
+            or not t.is_contiguous()):
+        _attn_error(t, name, torch.int32, device, "%s and contiguous" % (shape,))
+    return t.data_ptr()
+
+
+def _table(t: torch.Tensor, n: int, device):
+    if (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device or t.dim() != 2
+            or t.shape[0] != n or t.stride(1) != 1):
+        _attn_error(t, "page_table", torch.int32, device, "[%d, entries] with a contiguous last dimension" % n)
+    return t.data_ptr(), t.shape[1], t.stride(0)
 
 
 class _DeviceArray:
@@ -508,6 +563,138 @@ class UserBuffer:
         _check(load().gemm_rs(self._h, _ptrs(A), _ptrs(Bt), K, _ptrs(Y_shards),
                               _stream_ptr(stream)))
         return Y_shards
+
+
+    # -- attention between the QKV and the attention-out projections
+    def _stream(self, stream):
+        return torch.cuda.current_stream(self.device) if stream is None else stream
+
+    def _new(self, shape, dtype, stream):
+        """A new tensor of the stream that the call runs on, so that its memory is not reused too early."""
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def _attn_outputs(self, q, out, lse, T, H, D, stream):
+        """(out, its view, lse, its pointer); lse=True allocates it."""
+        if out is None:
+            out = self._new((T, H, D), torch.bfloat16, stream)
+        o, oh, _ = _heads_view(out, "out", T, D, self.device)
+        if oh != H:
+            raise ValueError("out has %d heads, q has %d" % (oh, H))
+        if lse is True:
+            lse = self._new((T, H), torch.float32, stream)
+        if lse is None or lse is False:
+            return out, o, None, 0
+        if (not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32 or lse.device != self.device
+                or tuple(lse.shape) != (T, H) or not lse.is_contiguous()):
+            _attn_error(lse, "lse", torch.float32, self.device, "(%d, %d) and contiguous" % (T, H))
+        return out, o, lse, lse.data_ptr()
+
+    def kv_append(self, q, k, v, cos, sin, seq_starts, kv_lens, page_table, k_cache, v_cache, q_out=None,
+                  interleaved: bool = False, stream=None):
+        """Rotate q and k of the active tokens by their positions and store k and v in the paged
+        cache (ub_kv_append). Returns the rotated queries.
+
+        q [T, heads, D], k and v [T, kv_heads, D]: views of the QKV output, any token and head
+        strides that are multiples of 8; D 64 or 128. cos, sin: fp32 [positions, rot / 2], rot a
+        multiple of 16 up to D (None: no rotation). seq_starts int32 [n + 1], kv_lens int32 [n]
+        (the tokens of this call included), page_table int32 [n, entries], on the device.
+        k_cache, v_cache [pages, kv_heads, page_size, D]. q_out: like q, q itself allowed."""
+        dev = self.device
+        T = self.active_shape[0]
+        qv, H, D = _heads_view(q, "q", T, None, dev)
+        kv, G, _ = _heads_view(k, "k", T, D, dev)
+        vv, Gv, _ = _heads_view(v, "v", T, D, dev)
+        kc = _pages_view(k_cache, "k_cache", D, dev)
+        vc = _pages_view(v_cache, "v_cache", D, dev, k_cache.shape)
+        pages, Gc, page, _ = k_cache.shape
+        if Gv != G or Gc != G:
+            raise ValueError("k has %d heads, v %d, the caches %d" % (G, Gv, Gc))
+        n = kv_lens.shape[0] if kv_lens.dim() else 0
+        table, width, table_row = _table(page_table, n, dev)
+        rot, positions, cp, sp = 0, 0, 0, 0
+        if cos is not None or sin is not None:
+            for name, t in (("cos", cos), ("sin", sin)):
+                if (not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.device != dev or t.dim() != 2
+                        or not t.is_contiguous() or t.shape != cos.shape):
+                    _attn_error(t, name, torch.float32, dev, "[positions, rot / 2] and contiguous, cos like sin")
+            positions, rot = cos.shape[0], 2 * cos.shape[1]
+            cp, sp = cos.data_ptr(), sin.data_ptr()
+        s = self._stream(stream)
+        if q_out is None:
+            q_out = self._new((T, H, D), torch.bfloat16, s)
+        ov, Ho, _ = _heads_view(q_out, "q_out", T, D, dev)
+        if Ho != H:
+            raise ValueError("q_out has %d heads, q has %d" % (Ho, H))
+        a = _ATTN.pack(_ATTN.size, n, H, G, D, page, rot, 1 if interleaved else 0, 1.0, 0, pages, width, table_row,
+                       positions, *qv, *kv, *vv, *ov, *kc, *vc, _ints(seq_starts, "seq_starts", (n + 1,), dev),
+                       _ints(kv_lens, "kv_lens", (n,), dev), table, cp, sp, 0)
+        _check(load().ub_kv_append(self._h, a, s.cuda_stream))
+        return q_out
+
+    def attn_prompt(self, q, k, v, seq_starts, out=None, lse=None, scale: float | None = None, stream=None):
+        """Causal attention of whole packed prompts (ub_attn_prompt): sequence s is rows
+        [seq_starts[s], seq_starts[s + 1]) of q [T, heads, D] and of k, v [T, kv_heads, D].
+        scale: 1 / sqrt(D) if None. lse: an fp32 [T, heads] tensor, or True for a new one.
+        Returns out, or (out, lse) where lse is asked for. Rows of no sequence stay as they are."""
+        dev = self.device
+        T = self.active_shape[0]
+        qv, H, D = _heads_view(q, "q", T, None, dev)
+        kv, G, _ = _heads_view(k, "k", T, D, dev)
+        vv, Gv, _ = _heads_view(v, "v", T, D, dev)
+        if Gv != G:
+            raise ValueError("k has %d heads, v %d" % (G, Gv))
+        n = seq_starts.shape[0] - 1 if seq_starts.dim() else 0
+        s = self._stream(stream)
+        out, ov, lse, lp = self._attn_outputs(q, out, lse, T, H, D, s)
+        a = _ATTN.pack(_ATTN.size, n, H, G, D, 0, 0, 0, 1.0 / math.sqrt(D) if scale is None else scale, 0, 0, 0, 0, 0,
+                       *qv, *kv, *vv, *ov, *_NO_PAGES, *_NO_PAGES, _ints(seq_starts, "seq_starts", (n + 1,), dev),
+                       0, 0, 0, 0, lp)
+        _check(load().ub_attn_prompt(self._h, a, s.cuda_stream))
+        return out if lse is None else (out, lse)
+
+    def attn_prompt_paged(self, q, k_cache, v_cache, seq_starts, kv_lens, page_table, out=None, lse=None,
+                          scale: float | None = None, stream=None):
+        """Causal attention of prompts, or of chunks of prompts, over the paged cache that holds
+        their keys and values (after kv_append); arguments as there and in attn_prompt."""
+        dev = self.device
+        T = self.active_shape[0]
+        qv, H, D = _heads_view(q, "q", T, None, dev)
+        kc = _pages_view(k_cache, "k_cache", D, dev)
+        vc = _pages_view(v_cache, "v_cache", D, dev, k_cache.shape)
+        pages, G, page, _ = k_cache.shape
+        n = kv_lens.shape[0] if kv_lens.dim() else 0
+        table, width, table_row = _table(page_table, n, dev)
+        s = self._stream(stream)
+        out, ov, lse, lp = self._attn_outputs(q, out, lse, T, H, D, s)
+        if page == 0:
+            raise ValueError("pages of no rows")
+        a = _ATTN.pack(_ATTN.size, n, H, G, D, page, 0, 0, 1.0 / math.sqrt(D) if scale is None else scale, 0, pages,
+                       width, table_row, 0, *qv, *_NO_HEADS, *_NO_HEADS, *ov, *kc, *vc,
+                       _ints(seq_starts, "seq_starts", (n + 1,), dev), _ints(kv_lens, "kv_lens", (n,), dev), table, 0, 0, lp)
+        _check(load().ub_attn_prompt(self._h, a, s.cuda_stream))
+        return out if lse is None else (out, lse)
+
+    def attn_decode(self, q, k_cache, v_cache, kv_lens, page_table, out=None, lse=None, scale: float | None = None,
+                    stream=None):
+        """Attention of one new token per sequence over the paged cache (ub_attn_decode): row s of
+        q [T, heads, D] is sequence s, n = kv_lens.shape[0] <= T; arguments as in kv_append and
+        attn_prompt. Rows from n on stay as they are."""
+        dev = self.device
+        T = self.active_shape[0]
+        qv, H, D = _heads_view(q, "q", T, None, dev)
+        kc = _pages_view(k_cache, "k_cache", D, dev)
+        vc = _pages_view(v_cache, "v_cache", D, dev, k_cache.shape)
+        pages, G, page, _ = k_cache.shape
+        n = kv_lens.shape[0] if kv_lens.dim() else 0
+        table, width, table_row = _table(page_table, n, dev)
+        s = self._stream(stream)
+        out, ov, lse, lp = self._attn_outputs(q, out, lse, T, H, D, s)
+        a = _ATTN.pack(_ATTN.size, n, H, G, D, page, 0, 0, 1.0 / math.sqrt(D) if scale is None else scale, 0, pages,
+                       width, table_row, 0, *qv, *_NO_HEADS, *_NO_HEADS, *ov, *kc, *vc, 0,
+                       _ints(kv_lens, "kv_lens", (n,), dev), table, 0, 0, lp)
+        _check(load().ub_attn_decode(self._h, a, s.cuda_stream))
+        return out if lse is None else (out, lse)
 
 
 def ag_gemm_noalloc(shards, Wt: torch.Tensor, Y: torch.Tensor | None = None, stream=None):

@@ -134,7 +134,10 @@ enum {
     UB_OP_RS_KN = 4,
     UB_OP_WGRAD = 5,
     UB_OP_REDUCE_SCATTER = 6,
-    UB_NUM_OPS = 7
+    UB_OP_KV_APPEND = 7,
+    UB_OP_ATTN_PROMPT = 8,
+    UB_OP_ATTN_DECODE = 9,
+    UB_NUM_OPS = 10
 };
 
 /*
@@ -352,6 +355,98 @@ int ag_gemm_from_buffer(ub_handle_t h, const void *Wt, int64_t N, int64_t glu_f,
  *    wait that runs out is reported by ub_query_status (UB_ERR_TIMEOUT).
  */
 int ub_stream_read(ub_handle_t h, const void *src, int64_t bytes, void *stream);
+
+/*
+ * Additions of this library: the attention between the two projections of [P1]'s attention
+ * diagram (QKV = ag_gemm, attention out = gemm_rs), on one shard's heads of the packed
+ * active tokens, for serving: prompts, chunks of prompts and single new tokens over a
+ * paged key/value cache. The pages draw the box and define no call.
+ *
+ * The tokens of a call are the handle's active T rows. seq_starts[n_seqs + 1] cuts their
+ * prefix into sequences: sequence s is rows [seq_starts[s], seq_starts[s + 1]), n_s of them
+ * (zero is allowed); rows from seq_starts[n_seqs] on (padding to a multiple of tp) belong
+ * to no sequence and are neither read for a result nor written. kv_lens[s] counts the keys
+ * of sequence s in the cache, its n_s new tokens included: token i of the sequence has
+ * position kv_lens[s] - n_s + i. The cache is a pool of pages of page_size rows for every
+ * key/value head; page page_table[s][p] holds positions [p * page_size, (p + 1) * page_size)
+ * of sequence s. These arrays live on the device and are read there: nothing is copied to
+ * the host, and a captured call sees their new contents at every replay.
+ *
+ * What the device finds wrong with them faults nothing and is recorded in the sticky status
+ * (ub_query_status: UB_ERR_ARG): a table entry outside [0, num_pages) or beyond the table's
+ * width (its keys read as zeros, an append to it is dropped), a position below zero or
+ * outside the rotation tables (the token is dropped). A kv_lens entry below zero counts as
+ * zero, one beyond the table as the table's capacity; starts that run backwards or past T
+ * are cut to [0, T]. What is past a sequence's length in its last page may hold anything,
+ * NaN too; the keys and values of a sequence itself must be finite (a value that is not
+ * may reach earlier rows of the same sequence, never another sequence).
+ *
+ * Views: strides in elements, the head dimension contiguous (stride 1); pointers 16-byte
+ * aligned, every stride of a dimension longer than 1 a positive multiple of 8. So q, k, v
+ * may be slices of one QKV output row.
+ */
+typedef struct {
+    void *data;   /* [tokens, heads, head_dim] bf16 */
+    int64_t row;  /* elements between tokens */
+    int64_t head; /* elements between heads */
+} ub_heads_t;
+typedef struct {
+    void *data;   /* [num_pages, kv_heads, page_size, head_dim] bf16 */
+    int64_t page, head, row;
+} ub_pages_t;
+typedef struct {
+    uint32_t size;        /* sizeof(ub_attn_t) */
+    int32_t n_seqs;
+    int32_t heads;        /* query heads; a multiple of kv_heads */
+    int32_t kv_heads;
+    int32_t head_dim;     /* 64 or 128 */
+    int32_t page_size;    /* a power of two, 8..256 (0: no cache, ub_attn_prompt) */
+    int32_t rot_dim;      /* ub_kv_append: elements of a head that are rotated, a multiple of
+                             16 up to head_dim; 0: none */
+    int32_t interleaved;  /* rotated pairs: 0: (j, j + rot_dim / 2), 1: (2 j, 2 j + 1) */
+    float scale;          /* attention: factor of q . k, finite and > 0 */
+    uint32_t reserved;    /* 0 */
+    int64_t num_pages;
+    int64_t table_width;  /* entries per sequence of page_table */
+    int64_t table_row;    /* elements between its rows */
+    int64_t max_pos;      /* rows of cos and sin */
+    ub_heads_t q, k, v;   /* k, v: ub_kv_append, ub_attn_prompt without a cache */
+    ub_heads_t out;       /* attention output, or the rotated queries of ub_kv_append */
+    ub_pages_t k_cache, v_cache;
+    const int32_t *seq_starts; /* [n_seqs + 1]; not read by ub_attn_decode */
+    const int32_t *kv_lens;    /* [n_seqs]; not read without a cache */
+    const int32_t *page_table; /* [n_seqs, table_width] */
+    const float *cos, *sin;    /* [max_pos, rot_dim / 2], contiguous */
+    float *lse;           /* NULL, or [tokens, heads]: natural log of the sum of exp(scores) */
+} ub_attn_t;
+
+/*
+ * ub_kv_append: rotate the queries and keys of the new tokens by their positions, and store
+ * keys and values in the cache:
+ *     (a, b) -> (a cos - b sin, b cos + a sin),  cos, sin = row `position` of the tables,
+ * fp32 arithmetic, one BF16 rounding. Queries go to `out` (q itself is allowed), rotated
+ * keys and unrotated values to the cache. One kernel.
+ *
+ * ub_attn_prompt: causal attention of the new tokens, fp32 scores and sums:
+ *     out[t][h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q[t][h] . k_j[h / g] - max),
+ * g = heads / kv_heads, over the keys j of t's sequence up to and including t's position.
+ *  - page_size = 0: whole prompts; the keys and values are the packed rows k, v themselves.
+ *  - page_size > 0: keys and values come from the cache (after ub_kv_append): whole prompts,
+ *    or chunks of prompts whose beginnings are cached already.
+ * A row without any key (kv_lens[s] < n_s) gives 0 and lse -inf.
+ *
+ * ub_attn_decode: the same for one new token per sequence: row s of q and out is sequence s
+ * (n_seqs <= T), over all kv_lens[s] cached keys; 0 and lse -inf where there is none. The
+ * cache's length is split over the whole GPU and joined in a fixed order; uses the handle's
+ * workspace.
+ *
+ * Errors: UB_ERR_ARG (null pointers, size, heads not a multiple of kv_heads, head_dim,
+ * page_size, rot_dim, scale), UB_ERR_ZERO (n_seqs, heads, kv_heads, num_pages or table_width
+ * <= 0), UB_ERR_CAPACITY (ub_attn_decode: n_seqs > T), UB_ERR_ALIGN, UB_ERR_CUDA.
+ */
+int ub_kv_append(ub_handle_t h, const ub_attn_t *a, void *stream);
+int ub_attn_prompt(ub_handle_t h, const ub_attn_t *a, void *stream);
+int ub_attn_decode(ub_handle_t h, const ub_attn_t *a, void *stream);
 
 /* Options (UB_OPT_*). UB_ERR_ARG for an unknown key or an out-of-range value. */
 int ub_set_option(ub_handle_t h, int key, int64_t val);
