@@ -37,6 +37,9 @@ namespace {
 
 constexpr int PR_THREADS = 512;
 constexpr int ITEMS = 4;                 // schedule ring
+// Registers per thread by role; their sum is what the block is launched with (512 x 128).
+constexpr int SOFTMAX_REGS = 192, CORRECT_REGS = 72, SINGLE_REGS = 56;
+static_assert(2 * SOFTMAX_REGS + CORRECT_REGS + SINGLE_REGS == 4 * 128, "register split");
 constexpr int TM_S = 0, TM_O = 256;      // TMEM columns: S_i at 128 i, O_i at 256 + 128 i
 constexpr float RESCALE_LOG2 = 8.f;      // growth of the maximum (log2) that is put off
 
@@ -89,6 +92,49 @@ __device__ __forceinline__ int extent(int lim, int j)
     const int left = lim - j * PROMPT_KEYS;
     return left >= PROMPT_KEYS ? PROMPT_KEYS : (left + 15) & ~15;
 }
+
+template <int N>
+__device__ __forceinline__ void more_registers()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// Two fp32 operations in one instruction, on a register pair.
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi)
+{
+    return static_cast<uint64_t>(__float_as_uint(lo)) | (static_cast<uint64_t>(__float_as_uint(hi)) << 32);
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float low(uint64_t a) { return __uint_as_float(static_cast<uint32_t>(a)); }
+__device__ __forceinline__ float high(uint64_t a) { return __uint_as_float(static_cast<uint32_t>(a >> 32)); }
 
 __device__ __forceinline__ float ex2(float x)
 {
@@ -144,6 +190,15 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *v)
         "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]),
         "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
         "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *v)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(v[0]),
+        "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(taddr)
         : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -336,6 +391,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
 
     if (warp < 8) {
         // ------------------------------------------------------------ softmax
+        more_registers<SOFTMAX_REGS>();
         const int i = warp >> 2;                       // q tile
         const int row = (warp & 3) * 32 + lane;
         const uint32_t ts = tmem + TM_S + i * 128 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
@@ -365,10 +421,10 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                 }
                 float mx[4] = {m, m, m, m};
 #pragma unroll
-                for (int c = 0; c < 128; c += 4)
+                for (int c = 0; c < 128; c += 8)
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], s[c + u]);
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], s[c + 2 * u], s[c + 2 * u + 1]);
+                const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
                 float f = 1.f;
                 if (j == 0) {
                     m = top;
@@ -383,24 +439,25 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                     ++n_sc;
                 }
                 const float ref = m == -INFINITY ? 0.f : m * sl;  // no key yet: every weight is zero
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                uint32_t pk[64];
+                const uint64_t sl2 = pair_of(sl, sl), ref2 = pair_of(-ref, -ref);
+                uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
-                for (int c = 0; c < 128; c += 4) {
+                for (int c0 = 0; c0 < 128; c0 += 32) {
+                    uint32_t pk[16];
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        s[c + u] = ex2(fmaf(s[c + u], sl, -ref));
-                        sum[u] += s[c + u];
+                    for (int c = 0; c < 32; c += 2) {
+                        const uint64_t x = fma2(pair_of(s[c0 + c], s[c0 + c + 1]), sl2, ref2);
+                        const float e0 = ex2(low(x)), e1 = ex2(high(x));
+                        sum[(c / 2) & 1] = add2(sum[(c / 2) & 1], pair_of(e0, e1));
+                        pk[c / 2] = pack_bf16x2(__float_as_uint(e0), __float_as_uint(e1));
                     }
-                    pk[c / 2] = pack_bf16x2(__float_as_uint(s[c]), __float_as_uint(s[c + 1]));
-                    pk[c / 2 + 1] = pack_bf16x2(__float_as_uint(s[c + 2]), __float_as_uint(s[c + 3]));
+                    tmem_st16(ts + c0 / 2, pk);
                 }
-                tmem_st32(ts, pk);
-                tmem_st32(ts + 32, pk + 32);
                 tmem_wait_st();
                 tc_fence_before();
                 arrive(p_full + 8 * i);
-                l = l * f + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+                const uint64_t both = add2(sum[0], sum[1]);
+                l = l * f + (low(both) + high(both));
             }
             if (!alive) break;
             if (!wait(sc_empty + 8 * i, (n_sc & 1) ^ 1)) break;
@@ -414,6 +471,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
         }
     } else if (warp < 12) {
         // ------------------------------------------------------------ correction, epilogue
+        fewer_registers<CORRECT_REGS>();
         const int row = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         uint32_t n_sc[2] = {0, 0}, n_o[2] = {0, 0};
@@ -492,7 +550,10 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
             }
             if (!alive) break;
         }
-    } else if (warp == 12) {
+    } else {
+      // the four single warps
+      fewer_registers<SINGLE_REGS>();
+      if (warp == 12) {
         // ------------------------------------------------------------ loads
         uint32_t c = 0, n_q[2] = {0, 0};               // ring position, Q loads so far
         Item it;
@@ -685,6 +746,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
             arrive(it_full + 8 * slot);
             if (it.row0 < 0) break;
         }
+      }
     }
 
     if (!alive) settle(200000);  // a wait ran out: copies already issued land first
