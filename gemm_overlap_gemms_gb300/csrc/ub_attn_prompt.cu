@@ -48,7 +48,7 @@ struct PromptShape {
     static constexpr int TILE_BYTES = PROMPT_KEYS * D * 2;
     static constexpr int HALF_BYTES = PROMPT_KEYS * 128;  // 64 columns of a tile
     static constexpr int STAGES = D == 128 ? 5 : 10;
-    static constexpr int SMEM = 1024 + 2 * TILE_BYTES + STAGES * TILE_BYTES + 1024 + 768;
+    static constexpr int SMEM = (2 + STAGES) * TILE_BYTES + 2048 + 768;
     static_assert(SMEM <= 232448, "shared memory");
 };
 
@@ -125,12 +125,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
 {
     uint64_t d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
 __device__ __forceinline__ float low(uint64_t a) { return __uint_as_float(static_cast<uint32_t>(a)); }
@@ -318,22 +312,26 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
 {
     using Sh = PromptShape<D>;
     constexpr int NST = Sh::STAGES;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t base[];
     const uint32_t sm_q = smem_u32(base), sm_kv = sm_q + 2 * Sh::TILE_BYTES;
     float *sm_scale = reinterpret_cast<float *>(base + (2 + NST) * Sh::TILE_BYTES);  // [2][128]
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sm_scale + 256);
+    float *sm_sum = sm_scale + 256;                                                  // [2][128]
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm_sum + 256);
     const uint32_t b0 = smem_u32(bars);
     const uint32_t kv_full = b0, kv_empty = b0 + 8 * NST, v_raw = b0 + 16 * NST;
     const uint32_t misc = b0 + 24 * NST;
-    const uint32_t q_full = misc, q_empty = misc + 16, s_full = misc + 32, p_full = misc + 48, corr = misc + 64,
-                   sc_full = misc + 80, sc_empty = misc + 96, o_full = misc + 112, drain = misc + 128,
+    const uint32_t q_full = misc, q_empty = misc + 16, s_full = misc + 32, p_full = misc + 48, sc_full = misc + 64,
+                   l_full = misc + 80, l_empty = misc + 96, o_full = misc + 112, drain = misc + 128,
                    it_full = misc + 136, it_empty = it_full + 8 * ITEMS;
     Item *items = reinterpret_cast<Item *>(reinterpret_cast<uint8_t *>(bars) + 24 * NST + 136 + 16 * ITEMS);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(items + ITEMS);
     static_assert(24 * NST + 136 + 16 * ITEMS + sizeof(Item) * ITEMS + 4 <= 768, "barrier area");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if ((sm_q & 1023u) != 0u) {  // the swizzled tiles need what the declaration asks for
+        if (threadIdx.x == 0) atomicCAS(p.b.status, 0, UB_ERR_ALIGN);
+        return;
+    }
     if (threadIdx.x == 0) {
         for (int i = 0; i < NST; ++i) {
             mbar_init(kv_full + 8 * i, 1);
@@ -344,10 +342,10 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
             mbar_init(q_full + 8 * i, 1);
             mbar_init(q_empty + 8 * i, 1);
             mbar_init(s_full + 8 * i, 1);
-            mbar_init(p_full + 8 * i, 4);
-            mbar_init(corr + 8 * i, 4);
+            mbar_init(p_full + 8 * i, 8);    // P written (4 warps), O rescaled (4 warps)
             mbar_init(sc_full + 8 * i, 4);
-            mbar_init(sc_empty + 8 * i, 4);
+            mbar_init(l_full + 8 * i, 4);
+            mbar_init(l_empty + 8 * i, 4);
             mbar_init(o_full + 8 * i, 1);
         }
         mbar_init(drain, 1);
@@ -396,7 +394,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
         const int row = (warp & 3) * 32 + lane;
         const uint32_t ts = tmem + TM_S + i * 128 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const float sl = p.scale * 1.4426950408889634f;
-        uint32_t n_s = 0, n_sc = 0;                    // phases used
+        uint32_t n_s = 0, n_l = 0;                     // phases used
         Item it;
         for (uint32_t k = 0; next_item(k, it); ++k) {
             const Range2 r = ranges(it, tpt);
@@ -432,11 +430,11 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                     f = ex2((m - top) * sl);
                     m = top;
                 }
+                // The factor of the last tile has been read: its readers have arrived at p_full,
+                // or S of this tile would not be there.
                 if (j > 0) {
-                    if (!wait(sc_empty + 8 * i, (n_sc & 1) ^ 1)) break;
                     sm_scale[i * 128 + row] = f;
                     arrive(sc_full + 8 * i);
-                    ++n_sc;
                 }
                 const float ref = m == -INFINITY ? 0.f : m * sl;  // no key yet: every weight is zero
                 const uint64_t sl2 = pair_of(sl, sl), ref2 = pair_of(-ref, -ref);
@@ -460,10 +458,10 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                 l = l * f + (low(both) + high(both));
             }
             if (!alive) break;
-            if (!wait(sc_empty + 8 * i, (n_sc & 1) ^ 1)) break;
-            sm_scale[i * 128 + row] = l;
-            arrive(sc_full + 8 * i);
-            ++n_sc;
+            if (!wait(l_empty + 8 * i, (n_l & 1) ^ 1)) break;
+            ++n_l;
+            sm_sum[i * 128 + row] = l;
+            arrive(l_full + 8 * i);
             if (p.lse && token < it.ntok) {
                 const int h = (it.unit << p.pack_shift) + (row & (pack - 1));
                 p.lse[static_cast<int64_t>(it.row0 + token) * p.heads + h] = l > 0.f ? m * p.scale + logf(l) : (l == 0.f ? -INFINITY : l);
@@ -486,7 +484,6 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                         if (!wait(sc_full + 8 * i, n_sc[i] & 1)) continue;
                         ++n_sc[i];
                         const float f = sm_scale[i * 128 + row];
-                        arrive(sc_empty + 8 * i);
                         if (__any_sync(0xffffffffu, f != 1.f)) {
                             tc_fence_after();  // the softmax saw S of this tile: O of the last one is complete
                             const uint32_t to = tmem + TM_O + i * 128 + lanes;
@@ -503,7 +500,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                             tc_fence_before();
                         }
                     }
-                    arrive(corr + 8 * i);
+                    arrive(p_full + 8 * i);
                 }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -514,10 +511,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                 float inv = 0.f;
                 bool none = true;                      // no key: zeros
                 if (r.n[i] > 0) {
-                    if (!wait(sc_full + 8 * i, n_sc[i] & 1)) continue;
-                    ++n_sc[i];
-                    const float l = sm_scale[i * 128 + row];
-                    arrive(sc_empty + 8 * i);
+                    if (!wait(l_full + 8 * i, n_o[i] & 1)) continue;
+                    const float l = sm_sum[i * 128 + row];
+                    arrive(l_empty + 8 * i);
                     none = l == 0.f;
                     inv = 1.f / l;
                     if (!wait(o_full + 8 * i, n_o[i] & 1)) continue;
@@ -622,74 +618,80 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
         }
     } else if (warp == 13) {
         // ------------------------------------------------------------ MMA issue
-        uint32_t c = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
-        Item it;
-        // S_i = Q_i K^T of the tile in ring slot cs
-        auto issue_s = [&](int i, uint32_t cs, int ext, bool last) {
-            if (lane == 0) {
-                const uint32_t q = sm_q + i * Sh::TILE_BYTES, kk = sm_kv + (cs % NST) * Sh::TILE_BYTES;
+        // One lane runs the whole role: the waits and the issue are on the critical path.
+        if (lane == 0) {
+            uint32_t c = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
+            const uint64_t q_desc = smem_desc_sw128(sm_q), k_desc = smem_desc_sw128(sm_kv),
+                           v_desc = smem_desc_v(sm_kv, Sh::HALF_BYTES);
+            auto wait1 = [&](uint32_t bar, uint32_t parity) {
+                alive = mbar_wait(bar, parity, wc);
+                return alive;
+            };
+            // S_i = Q_i K^T of the tile in ring slot cs
+            auto issue_s = [&](int i, uint32_t cs, int ext, bool last) {
+                const uint64_t q = q_desc + i * (Sh::TILE_BYTES / 16), kk = k_desc + (cs % NST) * (Sh::TILE_BYTES / 16);
                 const uint32_t idesc = prompt_idesc(ext, false);
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s) {
-                    const uint32_t o = (s / 4) * Sh::HALF_BYTES + (s % 4) * 32;
-                    umma_ss(tmem + TM_S + i * 128, smem_desc_sw128(q + o), smem_desc_sw128(kk + o), idesc, s > 0);
+                    constexpr int STEP = 2, HALF = Sh::HALF_BYTES / 16;
+                    const int o = (s / 4) * HALF + (s % 4) * STEP;
+                    umma_ss(tmem + TM_S + i * 128, q + o, kk + o, idesc, s > 0);
                 }
                 umma_commit(s_full + 8 * i);
                 if (last) umma_commit(q_empty + 8 * i);
-            }
-            __syncwarp();
-        };
-        for (uint32_t k = 0; next_item(k, it); ++k) {
-            const Range2 r = ranges(it, tpt);
-            if (r.nmax == 0) continue;
-            if (!wait(kv_full + 8 * (c % NST), (c / NST) & 1)) break;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (r.n[i] == 0 || !alive) continue;
-                if (!wait(q_full + 8 * i, n_q[i] & 1)) continue;
-                ++n_q[i];
-                tc_fence_after();
-                issue_s(i, c, extent(r.lim[i], 0), r.n[i] == 1);
-            }
-            if (!alive) break;
-            if (lane == 0) umma_commit(kv_empty + 8 * (c % NST));
-            __syncwarp();
-            for (int j = 0; j < r.nmax && alive; ++j) {
-                const uint32_t cv = c + 2 * j + 1, ck = cv + 1;
-                const bool more = j + 1 < r.nmax;
-                if (!wait(kv_full + 8 * (cv % NST), (cv / NST) & 1)) break;
-                if (more && !wait(kv_full + 8 * (ck % NST), (ck / NST) & 1)) break;
-                tc_fence_after();
+            };
+            for (uint32_t k = 0;; ++k) {
+                const uint32_t slot = k % ITEMS;
+                if (!wait1(it_full + 8 * slot, (k / ITEMS) & 1)) break;
+                const Item it = items[slot];
+                mbar_arrive(it_empty + 8 * slot);
+                if (it.row0 < 0) break;
+                const Range2 r = ranges(it, tpt);
+                if (r.nmax == 0) continue;
+                if (!wait1(kv_full + 8 * (c % NST), (c / NST) & 1)) break;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    if (j >= r.n[i] || !alive) continue;
-                    if (!wait(corr + 8 * i, n_p[i] & 1) || !wait(p_full + 8 * i, n_p[i] & 1)) continue;
-                    ++n_p[i];
+                    if (r.n[i] == 0 || !alive) continue;
+                    if (!wait1(q_full + 8 * i, n_q[i] & 1)) continue;
+                    ++n_q[i];
                     tc_fence_after();
-                    if (lane == 0) {
-                        const uint32_t v = sm_kv + (cv % NST) * Sh::TILE_BYTES;
-                        const int steps = extent(r.lim[i], j) / 16;
-                        constexpr uint32_t idesc = prompt_idesc(D, true);
-                        for (int s = 0; s < steps; ++s)
-                            umma_ts(tmem + TM_O + i * 128, tmem + TM_S + i * 128 + s * 8,
-                                    smem_desc_v(v + s * 2048, Sh::HALF_BYTES), idesc, j > 0 || s > 0);
-                        if (j == r.n[i] - 1) umma_commit(o_full + 8 * i);
-                    }
-                    __syncwarp();
-                    if (j + 1 < r.n[i]) issue_s(i, ck, extent(r.lim[i], j + 1), j + 2 == r.n[i]);
+                    issue_s(i, c, extent(r.lim[i], 0), r.n[i] == 1);
                 }
                 if (!alive) break;
-                if (lane == 0) {
+                umma_commit(kv_empty + 8 * (c % NST));
+                for (int j = 0; j < r.nmax && alive; ++j) {
+                    const uint32_t cv = c + 2 * j + 1, ck = cv + 1;
+                    const bool more = j + 1 < r.nmax;
+                    if (!wait1(kv_full + 8 * (cv % NST), (cv / NST) & 1)) break;
+                    if (more && !wait1(kv_full + 8 * (ck % NST), (ck / NST) & 1)) break;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (j >= r.n[i] || !alive) continue;
+                        if (!wait1(p_full + 8 * i, n_p[i] & 1)) continue;
+                        ++n_p[i];
+                        tc_fence_after();
+                        const uint64_t v = v_desc + (cv % NST) * (Sh::TILE_BYTES / 16);
+                        const uint32_t tp = tmem + TM_S + i * 128, to = tmem + TM_O + i * 128;
+                        constexpr uint32_t idesc = prompt_idesc(D, true);
+                        const int steps = extent(r.lim[i], j) / 16;
+                        if (steps == PROMPT_KEYS / 16) {
+#pragma unroll
+                            for (int s = 0; s < PROMPT_KEYS / 16; ++s)
+                                umma_ts(to, tp + s * 8, v + s * 128, idesc, j > 0 || s > 0);
+                        } else {
+                            for (int s = 0; s < steps; ++s) umma_ts(to, tp + s * 8, v + s * 128, idesc, j > 0 || s > 0);
+                        }
+                        if (j == r.n[i] - 1) umma_commit(o_full + 8 * i);
+                        if (j + 1 < r.n[i]) issue_s(i, ck, extent(r.lim[i], j + 1), j + 2 == r.n[i]);
+                    }
+                    if (!alive) break;
                     umma_commit(kv_empty + 8 * (cv % NST));
                     if (more) umma_commit(kv_empty + 8 * (ck % NST));
                 }
-                __syncwarp();
+                if (!alive) break;
+                c += 2 * r.nmax;
             }
-            if (!alive) break;
-            c += 2 * r.nmax;
-        }
-        // everything issued has completed before TMEM goes back
-        if (lane == 0) {
+            // everything issued has completed before TMEM goes back
             umma_commit(drain);
             mbar_wait_drain(drain, 0, p.timeout_ns);
         }
