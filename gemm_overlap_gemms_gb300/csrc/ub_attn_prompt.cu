@@ -38,7 +38,7 @@ namespace {
 constexpr int PR_THREADS = 512;
 constexpr int ITEMS = 4;                 // schedule ring
 // Registers per thread by role; their sum is what the block is launched with (512 x 128).
-constexpr int SOFTMAX_REGS = 192, CORRECT_REGS = 72, SINGLE_REGS = 56;
+constexpr int SOFTMAX_REGS = 176, CORRECT_REGS = 72, SINGLE_REGS = 88;
 static_assert(2 * SOFTMAX_REGS + CORRECT_REGS + SINGLE_REGS == 4 * 128, "register split");
 constexpr int TM_S = 0, TM_O = 256;      // TMEM columns: S_i at 128 i, O_i at 256 + 128 i
 constexpr float RESCALE_LOG2 = 8.f;      // growth of the maximum (log2) that is put off
