@@ -86,6 +86,23 @@ __device__ __forceinline__ Range2 ranges(const Item &it, int tpt)
     r.limmax = r.lim[0] > r.lim[1] ? r.lim[0] : r.lim[1];
     return r;
 }
+// The same values, known to be the same in every lane.
+__device__ __forceinline__ Range2 uniform(Range2 r)
+{
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        r.lim[i] = __shfl_sync(0xffffffffu, r.lim[i], 0);
+        r.n[i] = __shfl_sync(0xffffffffu, r.n[i], 0);
+    }
+    r.nmax = r.n[0] > r.n[1] ? r.n[0] : r.n[1];
+    return r;
+}
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
 // Keys of tile j that are multiplied, for a q tile that reaches `lim` keys: a multiple of 16.
 __device__ __forceinline__ int extent(int lim, int j)
 {
@@ -322,12 +339,12 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
     const uint32_t misc = b0 + 24 * NST;
     const uint32_t q_full = misc, q_empty = misc + 16, s_full = misc + 32, p_full = misc + 48, sc_full = misc + 64,
                    l_full = misc + 80, l_empty = misc + 96, o_full = misc + 112, drain = misc + 128,
-                   it_full = misc + 136, it_empty = it_full + 8 * ITEMS;
-    Item *items = reinterpret_cast<Item *>(reinterpret_cast<uint8_t *>(bars) + 24 * NST + 136 + 16 * ITEMS);
+                   p_half = misc + 144, it_full = misc + 160, it_empty = it_full + 8 * ITEMS;
+    Item *items = reinterpret_cast<Item *>(reinterpret_cast<uint8_t *>(bars) + 24 * NST + 160 + 16 * ITEMS);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(items + ITEMS);
-    static_assert(24 * NST + 136 + 16 * ITEMS + sizeof(Item) * ITEMS + 4 <= 768, "barrier area");
+    static_assert(24 * NST + 160 + 16 * ITEMS + sizeof(Item) * ITEMS + 4 <= 768, "barrier area");
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     if ((sm_q & 1023u) != 0u) {  // the swizzled tiles need what the declaration asks for
         if (threadIdx.x == 0) atomicCAS(p.b.status, 0, UB_ERR_ALIGN);
         return;
@@ -342,7 +359,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
             mbar_init(q_full + 8 * i, 1);
             mbar_init(q_empty + 8 * i, 1);
             mbar_init(s_full + 8 * i, 1);
-            mbar_init(p_full + 8 * i, 8);    // P written (4 warps), O rescaled (4 warps)
+            mbar_init(p_half + 8 * i, 8);    // first half of P written (4 warps), O rescaled (4 warps)
+            mbar_init(p_full + 8 * i, 4);    // second half of P written
             mbar_init(sc_full + 8 * i, 4);
             mbar_init(l_full + 8 * i, 4);
             mbar_init(l_empty + 8 * i, 4);
@@ -351,7 +369,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
         mbar_init(drain, 1);
         for (int i = 0; i < ITEMS; ++i) {
             mbar_init(it_full + 8 * i, 1);
-            mbar_init(it_empty + 8 * i, 15);
+            mbar_init(it_empty + 8 * i, 15);  // every warp but the schedule's
         }
         fence_mbar_init();
         prefetch_tmap(&p.tmQ);
@@ -423,13 +441,11 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
 #pragma unroll
                     for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], s[c + 2 * u], s[c + 2 * u + 1]);
                 const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-                float f = 1.f;
-                if (j == 0) {
-                    m = top;
-                } else if ((top - m) * sl > RESCALE_LOG2) {  // also from m = -inf
-                    f = ex2((m - top) * sl);
-                    m = top;
-                }
+                // A first or much larger maximum (never from -inf to -inf: the difference is no number).
+                const float grow = (top - m) * sl;
+                const bool moves = grow > RESCALE_LOG2;
+                const float f = moves ? ex2(-grow) : 1.f;
+                m = moves ? top : m;
                 // The factor of the last tile has been read: its readers have arrived at p_full,
                 // or S of this tile would not be there.
                 if (j > 0) {
@@ -450,10 +466,12 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                         pk[c / 2] = pack_bf16x2(__float_as_uint(e0), __float_as_uint(e1));
                     }
                     tmem_st16(ts + c0 / 2, pk);
+                    if (c0 == 32 || c0 == 96) {
+                        tmem_wait_st();
+                        tc_fence_before();
+                        arrive((c0 == 32 ? p_half : p_full) + 8 * i);
+                    }
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                arrive(p_full + 8 * i);
                 const uint64_t both = add2(sum[0], sum[1]);
                 l = l * f + (low(both) + high(both));
             }
@@ -500,7 +518,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                             tc_fence_before();
                         }
                     }
-                    arrive(p_full + 8 * i);
+                    arrive(p_half + 8 * i);
                 }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -618,80 +636,95 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
         }
     } else if (warp == 13) {
         // ------------------------------------------------------------ MMA issue
-        // One lane runs the whole role: the waits and the issue are on the critical path.
-        if (lane == 0) {
-            uint32_t c = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
-            const uint64_t q_desc = smem_desc_sw128(sm_q), k_desc = smem_desc_sw128(sm_kv),
-                           v_desc = smem_desc_v(sm_kv, Sh::HALF_BYTES);
-            auto wait1 = [&](uint32_t bar, uint32_t parity) {
-                alive = mbar_wait(bar, parity, wc);
-                return alive;
-            };
-            // S_i = Q_i K^T of the tile in ring slot cs
-            auto issue_s = [&](int i, uint32_t cs, int ext, bool last) {
-                const uint64_t q = q_desc + i * (Sh::TILE_BYTES / 16), kk = k_desc + (cs % NST) * (Sh::TILE_BYTES / 16);
-                const uint32_t idesc = prompt_idesc(ext, false);
+        // The whole warp walks the tiles and one elected lane issues, on values that are the
+        // same in every lane (broadcast from lane 0, so that the compiler knows): descriptors
+        // then stay in uniform registers, and an issue costs less than the MMA takes.
+        uint32_t c = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
+        const uint64_t q_desc = smem_desc_sw128(sm_q), k_desc = smem_desc_sw128(sm_kv),
+                       v_desc = smem_desc_v(sm_kv, Sh::HALF_BYTES);
+        auto wait_kv = [&](uint32_t cs) { return wait(kv_full + 8 * (cs % NST), (cs / NST) & 1); };
+        // S_i = Q_i K^T of the tile in ring slot cs
+        auto issue_s = [&](int i, uint32_t cs, int ext, bool last) {
+            const uint64_t q = q_desc + i * (Sh::TILE_BYTES / 16), kk = k_desc + (cs % NST) * (Sh::TILE_BYTES / 16);
+            const uint32_t idesc = prompt_idesc(ext, false);
+            if (elect_one()) {
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s) {
-                    constexpr int STEP = 2, HALF = Sh::HALF_BYTES / 16;
-                    const int o = (s / 4) * HALF + (s % 4) * STEP;
+                    const int o = (s / 4) * (Sh::HALF_BYTES / 16) + (s % 4) * 2;
                     umma_ss(tmem + TM_S + i * 128, q + o, kk + o, idesc, s > 0);
                 }
                 umma_commit(s_full + 8 * i);
                 if (last) umma_commit(q_empty + 8 * i);
-            };
-            for (uint32_t k = 0;; ++k) {
-                const uint32_t slot = k % ITEMS;
-                if (!wait1(it_full + 8 * slot, (k / ITEMS) & 1)) break;
-                const Item it = items[slot];
-                mbar_arrive(it_empty + 8 * slot);
-                if (it.row0 < 0) break;
-                const Range2 r = ranges(it, tpt);
-                if (r.nmax == 0) continue;
-                if (!wait1(kv_full + 8 * (c % NST), (c / NST) & 1)) break;
+            }
+            __syncwarp();
+        };
+        Item it;
+        for (uint32_t k = 0; next_item(k, it); ++k) {
+            const Range2 r = uniform(ranges(it, tpt));
+            if (r.nmax == 0) continue;
+            if (!wait_kv(c)) break;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (r.n[i] == 0 || !alive) continue;
+                if (!wait(q_full + 8 * i, n_q[i] & 1)) continue;
+                ++n_q[i];
+                tc_fence_after();
+                issue_s(i, c, extent(r.lim[i], 0), r.n[i] == 1);
+            }
+            if (!alive) break;
+            if (elect_one()) umma_commit(kv_empty + 8 * (c % NST));
+            for (int j = 0; j < r.nmax && alive; ++j) {
+                const uint32_t cv = c + 2 * j + 1, ck = cv + 1;
+                const bool more = j + 1 < r.nmax;
+                if (!wait_kv(cv)) break;
+                if (more && !wait_kv(ck)) break;
+                const uint64_t v = v_desc + (cv % NST) * (Sh::TILE_BYTES / 16);
+                constexpr uint32_t idesc = prompt_idesc(D, true);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    if (r.n[i] == 0 || !alive) continue;
-                    if (!wait1(q_full + 8 * i, n_q[i] & 1)) continue;
-                    ++n_q[i];
+                    if (j >= r.n[i] || !alive) continue;
+                    const uint32_t tp = tmem + TM_S + i * 128, to = tmem + TM_O + i * 128;
+                    const int steps = extent(r.lim[i], j) / 16;
+                    if (!wait(p_half + 8 * i, n_p[i] & 1)) continue;
                     tc_fence_after();
-                    issue_s(i, c, extent(r.lim[i], 0), r.n[i] == 1);
+                    if (steps == 8) {
+                        if (elect_one()) {
+#pragma unroll
+                            for (int s = 0; s < 4; ++s) umma_ts(to, tp + s * 8, v + s * 128, idesc, j > 0 || s > 0);
+                        }
+                        __syncwarp();
+                        if (!wait(p_full + 8 * i, n_p[i] & 1)) continue;
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int s = 4; s < 8; ++s) umma_ts(to, tp + s * 8, v + s * 128, idesc, 1);
+                            if (j == r.n[i] - 1) umma_commit(o_full + 8 * i);
+                        }
+                        __syncwarp();
+                    } else {  // the sequence's last keys
+                        if (!wait(p_full + 8 * i, n_p[i] & 1)) continue;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            for (int s = 0; s < steps; ++s) umma_ts(to, tp + s * 8, v + s * 128, idesc, j > 0 || s > 0);
+                            umma_commit(o_full + 8 * i);
+                        }
+                        __syncwarp();
+                    }
+                    ++n_p[i];
+                    if (j + 1 < r.n[i]) issue_s(i, ck, extent(r.lim[i], j + 1), j + 2 == r.n[i]);
                 }
                 if (!alive) break;
-                umma_commit(kv_empty + 8 * (c % NST));
-                for (int j = 0; j < r.nmax && alive; ++j) {
-                    const uint32_t cv = c + 2 * j + 1, ck = cv + 1;
-                    const bool more = j + 1 < r.nmax;
-                    if (!wait1(kv_full + 8 * (cv % NST), (cv / NST) & 1)) break;
-                    if (more && !wait1(kv_full + 8 * (ck % NST), (ck / NST) & 1)) break;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (j >= r.n[i] || !alive) continue;
-                        if (!wait1(p_full + 8 * i, n_p[i] & 1)) continue;
-                        ++n_p[i];
-                        tc_fence_after();
-                        const uint64_t v = v_desc + (cv % NST) * (Sh::TILE_BYTES / 16);
-                        const uint32_t tp = tmem + TM_S + i * 128, to = tmem + TM_O + i * 128;
-                        constexpr uint32_t idesc = prompt_idesc(D, true);
-                        const int steps = extent(r.lim[i], j) / 16;
-                        if (steps == PROMPT_KEYS / 16) {
-#pragma unroll
-                            for (int s = 0; s < PROMPT_KEYS / 16; ++s)
-                                umma_ts(to, tp + s * 8, v + s * 128, idesc, j > 0 || s > 0);
-                        } else {
-                            for (int s = 0; s < steps; ++s) umma_ts(to, tp + s * 8, v + s * 128, idesc, j > 0 || s > 0);
-                        }
-                        if (j == r.n[i] - 1) umma_commit(o_full + 8 * i);
-                        if (j + 1 < r.n[i]) issue_s(i, ck, extent(r.lim[i], j + 1), j + 2 == r.n[i]);
-                    }
-                    if (!alive) break;
+                if (elect_one()) {
                     umma_commit(kv_empty + 8 * (cv % NST));
                     if (more) umma_commit(kv_empty + 8 * (ck % NST));
                 }
-                if (!alive) break;
-                c += 2 * r.nmax;
+                __syncwarp();
             }
-            // everything issued has completed before TMEM goes back
+            if (!alive) break;
+            c += 2 * r.nmax;
+        }
+        // everything issued has completed before TMEM goes back
+        if (elect_one()) {
             umma_commit(drain);
             mbar_wait_drain(drain, 0, p.timeout_ns);
         }
@@ -733,10 +766,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
         for (int o = 16; o > 0; o >>= 1) cmax = max(cmax, __shfl_xor_sync(0xffffffffu, cmax, o));
         const int64_t total = static_cast<int64_t>(tiles) * p.units;
         // Longest first, dealt forth and back over the CTAs.
-        uint32_t k = 0;
-        for (;; ++k) {
-            const int64_t round = static_cast<int64_t>(k) * gridDim.x;
-            const int64_t g = round + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        for (uint32_t k = 0;; ++k) {
+            const int64_t g = static_cast<int64_t>(k) * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
             Item it{-1, 0, 0, 0, 0, 0};
             if (g < total) {
                 it = item_at(p, static_cast<int>(g / p.units), cmax, tokens, lane);

@@ -247,6 +247,18 @@ def test_prompt_packed_long(buf):
     run_packed(buf, b, 8, 2, 128)
 
 
+def test_prompt_back_to_back(buf):
+    """Many launches in flight, items of every length: every result the same."""
+    new = [1900, 3, 130, 700, 64, 2000, 17, 128, 950]
+    b = ref.Batch(new, [0] * len(new), kv_heads=2, dim=128, pad=0, seed=1)
+    q, k, v, first = run_packed(buf, b, 8, 2, 128)
+    outs = [torch.empty_like(first) for _ in range(60)]
+    for out in outs:
+        buf.attn_prompt(q, k, v, b.starts, out=out)
+    ok(buf)
+    assert all(torch.equal(out, first) for out in outs)
+
+
 def test_prompt_growing_scores(buf):
     """Scores that grow along the keys, so that the running maximum moves at every tile."""
     b = ref.Batch([900], [0], kv_heads=1, dim=128, seed=2)
