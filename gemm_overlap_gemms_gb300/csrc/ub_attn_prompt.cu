@@ -37,6 +37,7 @@ namespace {
 
 constexpr int PR_THREADS = 512;
 constexpr int ITEMS = 4;                 // schedule ring
+constexpr int DONE = 16;                 // barriers of the ring's releases: more than can be unseen
 // Registers per thread by role; their sum is what the block is launched with (512 x 128).
 constexpr int SOFTMAX_REGS = 176, CORRECT_REGS = 72, SINGLE_REGS = 88;
 static_assert(2 * SOFTMAX_REGS + CORRECT_REGS + SINGLE_REGS == 4 * 128, "register split");
@@ -50,6 +51,7 @@ struct PromptShape {
     static constexpr int STAGES = D == 128 ? 5 : 10;
     static constexpr int SMEM = (2 + STAGES) * TILE_BYTES + 2048 + 768;
     static_assert(SMEM <= 232448, "shared memory");
+    static_assert(STAGES < DONE, "an unseen release per ring position at most");
 };
 
 // One work item as the schedule warp publishes it.
@@ -96,6 +98,19 @@ __device__ __forceinline__ Range2 uniform(Range2 r)
     }
     r.nmax = r.n[0] > r.n[1] ? r.n[0] : r.n[1];
     return r;
+}
+// One look at a barrier.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 __device__ __forceinline__ bool elect_one()
 {
@@ -335,14 +350,14 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
     float *sm_sum = sm_scale + 256;                                                  // [2][128]
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm_sum + 256);
     const uint32_t b0 = smem_u32(bars);
-    const uint32_t kv_full = b0, kv_empty = b0 + 8 * NST, v_raw = b0 + 16 * NST;
-    const uint32_t misc = b0 + 24 * NST;
+    const uint32_t kv_full = b0, v_raw = b0 + 8 * NST, kv_done = b0 + 16 * NST;
+    const uint32_t misc = b0 + 16 * NST + 8 * DONE;
     const uint32_t q_full = misc, q_empty = misc + 16, s_full = misc + 32, p_full = misc + 48, sc_full = misc + 64,
                    l_full = misc + 80, l_empty = misc + 96, o_full = misc + 112, drain = misc + 128,
                    p_half = misc + 144, it_full = misc + 160, it_empty = it_full + 8 * ITEMS;
-    Item *items = reinterpret_cast<Item *>(reinterpret_cast<uint8_t *>(bars) + 24 * NST + 160 + 16 * ITEMS);
+    Item *items = reinterpret_cast<Item *>(reinterpret_cast<uint8_t *>(bars) + 16 * NST + 8 * DONE + 160 + 16 * ITEMS);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(items + ITEMS);
-    static_assert(24 * NST + 160 + 16 * ITEMS + sizeof(Item) * ITEMS + 4 <= 768, "barrier area");
+    static_assert(16 * NST + 8 * DONE + 160 + 16 * ITEMS + sizeof(Item) * ITEMS + 4 <= 768, "barrier area");
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     if ((sm_q & 1023u) != 0u) {  // the swizzled tiles need what the declaration asks for
@@ -352,9 +367,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
     if (threadIdx.x == 0) {
         for (int i = 0; i < NST; ++i) {
             mbar_init(kv_full + 8 * i, 1);
-            mbar_init(kv_empty + 8 * i, 1);
             mbar_init(v_raw + 8 * i, 1);
         }
+        for (int i = 0; i < DONE; ++i) mbar_init(kv_done + 8 * i, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full + 8 * i, 1);
             mbar_init(q_empty + 8 * i, 1);
@@ -570,6 +585,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
       if (warp == 12) {
         // ------------------------------------------------------------ loads
         uint32_t c = 0, n_q[2] = {0, 0};               // ring position, Q loads so far
+        uint32_t n_done = 0, freed = 0;                // releases seen; ring positions that they freed
+        uint32_t two = 0, n_ends = 0;                  // bit of each release to come: frees two positions
         Item it;
         const int box = PROMPT_KEYS < (1 << p.b.page_shift) ? PROMPT_KEYS : (1 << p.b.page_shift);
         constexpr int HALVES = D / 64;
@@ -610,7 +627,16 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
 #pragma unroll
                 for (int kind = 0; kind < 2 && alive; ++kind, ++c) {
                     const uint32_t st = c % NST;
-                    if (c >= NST && !wait(kv_empty + 8 * st, (c / NST - 1) & 1)) break;
+                    while (c - freed >= NST && wait(kv_done + 8 * (n_done % DONE), (n_done / DONE) & 1)) {
+                        freed += 1u + ((two >> (n_done % 32)) & 1u);
+                        ++n_done;
+                    }
+                    if (!alive) break;
+                    // The MMA warp releases K of tile 0, then V of each tile with K of the next.
+                    if (kind == 0 || j == r.nmax - 1) {
+                        const uint32_t at = n_ends++ % 32;
+                        two = (two & ~(1u << at)) | (static_cast<uint32_t>(kind == 0 && j > 0) << at);
+                    }
                     // The last tile of V goes through the zeroing warp when it ends inside 16 keys.
                     const bool fix = kind == 1 && j == r.nmax - 1 && extent(r.limmax, j) > it.len - key0;
                     const uint32_t bar = (fix ? v_raw : kv_full) + 8 * st;
@@ -639,7 +665,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
         // The whole warp walks the tiles and one elected lane issues, on values that are the
         // same in every lane (broadcast from lane 0, so that the compiler knows): descriptors
         // then stay in uniform registers, and an issue costs less than the MMA takes.
-        uint32_t c = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
+        uint32_t c = 0, n_done = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
         const uint64_t q_desc = smem_desc_sw128(sm_q), k_desc = smem_desc_sw128(sm_kv),
                        v_desc = smem_desc_v(sm_kv, Sh::HALF_BYTES);
         auto wait_kv = [&](uint32_t cs) { return wait(kv_full + 8 * (cs % NST), (cs / NST) & 1); };
@@ -647,16 +673,13 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
         auto issue_s = [&](int i, uint32_t cs, int ext, bool last) {
             const uint64_t q = q_desc + i * (Sh::TILE_BYTES / 16), kk = k_desc + (cs % NST) * (Sh::TILE_BYTES / 16);
             const uint32_t idesc = prompt_idesc(ext, false);
-            if (elect_one()) {
 #pragma unroll
-                for (int s = 0; s < D / 16; ++s) {
-                    const int o = (s / 4) * (Sh::HALF_BYTES / 16) + (s % 4) * 2;
-                    umma_ss(tmem + TM_S + i * 128, q + o, kk + o, idesc, s > 0);
-                }
-                umma_commit(s_full + 8 * i);
-                if (last) umma_commit(q_empty + 8 * i);
+            for (int s = 0; s < D / 16; ++s) {
+                const int o = (s / 4) * (Sh::HALF_BYTES / 16) + (s % 4) * 2;
+                umma_ss(tmem + TM_S + i * 128, q + o, kk + o, idesc, s > 0);
             }
-            __syncwarp();
+            umma_commit(s_full + 8 * i);
+            if (last) umma_commit(q_empty + 8 * i);
         };
         Item it;
         for (uint32_t k = 0; next_item(k, it); ++k) {
@@ -669,56 +692,67 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                 if (!wait(q_full + 8 * i, n_q[i] & 1)) continue;
                 ++n_q[i];
                 tc_fence_after();
-                issue_s(i, c, extent(r.lim[i], 0), r.n[i] == 1);
+                if (elect_one()) issue_s(i, c, extent(r.lim[i], 0), r.n[i] == 1);
+                __syncwarp();
             }
             if (!alive) break;
-            if (elect_one()) umma_commit(kv_empty + 8 * (c % NST));
+            if (elect_one()) umma_commit(kv_done + 8 * (n_done % DONE));
+            ++n_done;
             for (int j = 0; j < r.nmax && alive; ++j) {
                 const uint32_t cv = c + 2 * j + 1, ck = cv + 1;
                 const bool more = j + 1 < r.nmax;
-                if (!wait_kv(cv)) break;
-                if (more && !wait_kv(ck)) break;
                 const uint64_t v = v_desc + (cv % NST) * (Sh::TILE_BYTES / 16);
                 constexpr uint32_t idesc = prompt_idesc(D, true);
+                // The tiles are mostly there before the weights are: their barriers are looked
+                // at together with those of the weights, one latency for all.
+                bool kv = mbar_test_wait(kv_full + 8 * (cv % NST), (cv / NST) & 1);
+                if (more) kv = mbar_test_wait(kv_full + 8 * (ck % NST), (ck / NST) & 1) && kv;
+                bool seen = false;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     if (j >= r.n[i] || !alive) continue;
                     const uint32_t tp = tmem + TM_S + i * 128, to = tmem + TM_O + i * 128;
                     const int steps = extent(r.lim[i], j) / 16;
-                    if (!wait(p_half + 8 * i, n_p[i] & 1)) continue;
-                    tc_fence_after();
-                    if (steps == 8) {
-                        if (elect_one()) {
+                    const bool last = j == r.n[i] - 1;
+                    const uint32_t par = n_p[i] & 1;
+                    const bool half = mbar_test_wait(p_half + 8 * i, par);
+                    const bool full = mbar_test_wait(p_full + 8 * i, par);
+                    bool whole = __all_sync(0xffffffffu, (seen || kv) && half && full) != 0;
+                    if (!whole) {
+                        if (!seen && (!wait_kv(cv) || (more && !wait_kv(ck)))) continue;
+                        if (!wait(p_half + 8 * i, par)) continue;
+                        if (steps == 8) {
+                            tc_fence_after();
+                            if (elect_one()) {
 #pragma unroll
-                            for (int s = 0; s < 4; ++s) umma_ts(to, tp + s * 8, v + s * 128, idesc, j > 0 || s > 0);
+                                for (int s = 0; s < 4; ++s) umma_ts(to, tp + s * 8, v + s * 128, idesc, j > 0 || s > 0);
+                            }
+                            __syncwarp();
                         }
-                        __syncwarp();
-                        if (!wait(p_full + 8 * i, n_p[i] & 1)) continue;
-                        tc_fence_after();
-                        if (elect_one()) {
+                        if (!wait(p_full + 8 * i, par)) continue;
+                    }
+                    seen = true;
+                    ++n_p[i];
+                    tc_fence_after();
+                    if (elect_one()) {
+                        if (steps == 8) {
+                            if (whole) {
+#pragma unroll
+                                for (int s = 0; s < 4; ++s) umma_ts(to, tp + s * 8, v + s * 128, idesc, j > 0 || s > 0);
+                            }
 #pragma unroll
                             for (int s = 4; s < 8; ++s) umma_ts(to, tp + s * 8, v + s * 128, idesc, 1);
-                            if (j == r.n[i] - 1) umma_commit(o_full + 8 * i);
-                        }
-                        __syncwarp();
-                    } else {  // the sequence's last keys
-                        if (!wait(p_full + 8 * i, n_p[i] & 1)) continue;
-                        tc_fence_after();
-                        if (elect_one()) {
+                        } else {  // the sequence's last keys
                             for (int s = 0; s < steps; ++s) umma_ts(to, tp + s * 8, v + s * 128, idesc, j > 0 || s > 0);
-                            umma_commit(o_full + 8 * i);
                         }
-                        __syncwarp();
+                        if (last) umma_commit(o_full + 8 * i);
+                        else issue_s(i, ck, extent(r.lim[i], j + 1), j + 2 == r.n[i]);
                     }
-                    ++n_p[i];
-                    if (j + 1 < r.n[i]) issue_s(i, ck, extent(r.lim[i], j + 1), j + 2 == r.n[i]);
+                    __syncwarp();
                 }
                 if (!alive) break;
-                if (elect_one()) {
-                    umma_commit(kv_empty + 8 * (cv % NST));
-                    if (more) umma_commit(kv_empty + 8 * (ck % NST));
-                }
-                __syncwarp();
+                if (elect_one()) umma_commit(kv_done + 8 * (n_done % DONE));
+                ++n_done;
             }
             if (!alive) break;
             c += 2 * r.nmax;
