@@ -39,8 +39,8 @@ constexpr int PR_THREADS = 512;
 constexpr int ITEMS = 4;                 // schedule ring
 constexpr int DONE = 16;                 // barriers of the ring's releases: more than can be unseen
 // Registers per thread by role; their sum is what the block is launched with (512 x 128).
-constexpr int SOFTMAX_REGS = 176, CORRECT_REGS = 72, SINGLE_REGS = 88;
-static_assert(2 * SOFTMAX_REGS + CORRECT_REGS + SINGLE_REGS == 4 * 128, "register split");
+constexpr int SOFTMAX_REGS = 176, EPILOGUE_REGS = 72, SINGLE_REGS = 88;
+static_assert(2 * SOFTMAX_REGS + EPILOGUE_REGS + SINGLE_REGS == 4 * 128, "register split");
 constexpr int TM_S = 0, TM_O = 256;      // TMEM columns: S_i at 128 i, O_i at 256 + 128 i
 constexpr float RESCALE_LOG2 = 8.f;      // growth of the maximum (log2) that is put off
 
@@ -49,7 +49,7 @@ struct PromptShape {
     static constexpr int TILE_BYTES = PROMPT_KEYS * D * 2;
     static constexpr int HALF_BYTES = PROMPT_KEYS * 128;  // 64 columns of a tile
     static constexpr int STAGES = D == 128 ? 5 : 10;
-    static constexpr int SMEM = (2 + STAGES) * TILE_BYTES + 2048 + 768;
+    static constexpr int SMEM = (2 + STAGES) * TILE_BYTES + 1024 + 768;
     static_assert(SMEM <= 232448, "shared memory");
     static_assert(STAGES < DONE, "an unseen release per ring position at most");
 };
@@ -346,13 +346,12 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
     constexpr int NST = Sh::STAGES;
     extern __shared__ __align__(1024) uint8_t base[];
     const uint32_t sm_q = smem_u32(base), sm_kv = sm_q + 2 * Sh::TILE_BYTES;
-    float *sm_scale = reinterpret_cast<float *>(base + (2 + NST) * Sh::TILE_BYTES);  // [2][128]
-    float *sm_sum = sm_scale + 256;                                                  // [2][128]
+    float *sm_sum = reinterpret_cast<float *>(base + (2 + NST) * Sh::TILE_BYTES);  // [2][128]
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm_sum + 256);
     const uint32_t b0 = smem_u32(bars);
     const uint32_t kv_full = b0, v_raw = b0 + 8 * NST, kv_done = b0 + 16 * NST;
     const uint32_t misc = b0 + 16 * NST + 8 * DONE;
-    const uint32_t q_full = misc, q_empty = misc + 16, s_full = misc + 32, p_full = misc + 48, sc_full = misc + 64,
+    const uint32_t q_full = misc, q_empty = misc + 16, s_full = misc + 32, p_full = misc + 48, o_empty = misc + 64,
                    l_full = misc + 80, l_empty = misc + 96, o_full = misc + 112, drain = misc + 128,
                    p_half = misc + 144, it_full = misc + 160, it_empty = it_full + 8 * ITEMS;
     Item *items = reinterpret_cast<Item *>(reinterpret_cast<uint8_t *>(bars) + 16 * NST + 8 * DONE + 160 + 16 * ITEMS);
@@ -374,9 +373,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
             mbar_init(q_full + 8 * i, 1);
             mbar_init(q_empty + 8 * i, 1);
             mbar_init(s_full + 8 * i, 1);
-            mbar_init(p_half + 8 * i, 8);    // first half of P written (4 warps), O rescaled (4 warps)
-            mbar_init(p_full + 8 * i, 4);    // second half of P written
-            mbar_init(sc_full + 8 * i, 4);
+            mbar_init(p_half + 8 * i, 4);    // first half of P written, O rescaled
+            mbar_init(p_full + 8 * i, 4);
+            mbar_init(o_empty + 8 * i, 4);
             mbar_init(l_full + 8 * i, 4);
             mbar_init(l_empty + 8 * i, 4);
             mbar_init(o_full + 8 * i, 1);
@@ -461,11 +460,18 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                 const bool moves = grow > RESCALE_LOG2;
                 const float f = moves ? ex2(-grow) : 1.f;
                 m = moves ? top : m;
-                // The factor of the last tile has been read: its readers have arrived at p_full,
-                // or S of this tile would not be there.
-                if (j > 0) {
-                    sm_scale[i * 128 + row] = f;
-                    arrive(sc_full + 8 * i);
+                // S of this tile being there, O of the last tile is complete.
+                if (j > 0 && __any_sync(0xffffffffu, moves)) {
+                    const uint32_t to = ts + (TM_O - TM_S);
+#pragma unroll
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t v[16];
+                        tmem_ld16(to + c, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int u = 0; u < 16; ++u) v[u] = __float_as_uint(__uint_as_float(v[u]) * f);
+                        tmem_st16(to + c, v);
+                    }
                 }
                 const float ref = m == -INFINITY ? 0.f : m * sl;  // no key yet: every weight is zero
                 const uint64_t sl2 = pair_of(sl, sl), ref2 = pair_of(-ref, -ref);
@@ -501,40 +507,14 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
             }
         }
     } else if (warp < 12) {
-        // ------------------------------------------------------------ correction, epilogue
-        fewer_registers<CORRECT_REGS>();
+        // ------------------------------------------------------------ epilogue
+        fewer_registers<EPILOGUE_REGS>();
         const int row = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        uint32_t n_sc[2] = {0, 0}, n_o[2] = {0, 0};
+        uint32_t n_o[2] = {0, 0};
         Item it;
         for (uint32_t k = 0; next_item(k, it); ++k) {
             const Range2 r = ranges(it, tpt);
-            for (int j = 0; j < r.nmax && alive; ++j)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (j >= r.n[i] || !alive) continue;
-                    if (j > 0) {
-                        if (!wait(sc_full + 8 * i, n_sc[i] & 1)) continue;
-                        ++n_sc[i];
-                        const float f = sm_scale[i * 128 + row];
-                        if (__any_sync(0xffffffffu, f != 1.f)) {
-                            tc_fence_after();  // the softmax saw S of this tile: O of the last one is complete
-                            const uint32_t to = tmem + TM_O + i * 128 + lanes;
-#pragma unroll
-                            for (int c = 0; c < D; c += 32) {
-                                uint32_t v[32];
-                                tmem_ld32(to + c, v);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int u = 0; u < 32; ++u) v[u] = __float_as_uint(__uint_as_float(v[u]) * f);
-                                tmem_st32(to + c, v);
-                            }
-                            tmem_wait_st();
-                            tc_fence_before();
-                        }
-                    }
-                    arrive(p_half + 8 * i);
-                }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 if (r.tok[i] == 0 || !alive) continue;
@@ -575,7 +555,10 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                         }
                     }
                 }
-                tc_fence_before();
+                if (r.n[i] > 0) {
+                    tc_fence_before();
+                    arrive(o_empty + 8 * i);
+                }
             }
             if (!alive) break;
         }
@@ -665,7 +648,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
         // The whole warp walks the tiles and one elected lane issues, on values that are the
         // same in every lane (broadcast from lane 0, so that the compiler knows): descriptors
         // then stay in uniform registers, and an issue costs less than the MMA takes.
-        uint32_t c = 0, n_done = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
+        uint32_t c = 0, n_done = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};  // n_q: items of the q tile
         const uint64_t q_desc = smem_desc_sw128(sm_q), k_desc = smem_desc_sw128(sm_kv),
                        v_desc = smem_desc_v(sm_kv, Sh::HALF_BYTES);
         auto wait_kv = [&](uint32_t cs) { return wait(kv_full + 8 * (cs % NST), (cs / NST) & 1); };
@@ -717,6 +700,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                     const uint32_t par = n_p[i] & 1;
                     const bool half = mbar_test_wait(p_half + 8 * i, par);
                     const bool full = mbar_test_wait(p_full + 8 * i, par);
+                    if (j == 0 && !wait(o_empty + 8 * i, n_q[i] & 1)) continue;  // (n_q - 1) items written out
                     bool whole = __all_sync(0xffffffffu, (seen || kv) && half && full) != 0;
                     if (!whole) {
                         if (!seen && (!wait_kv(cv) || (more && !wait_kv(ck)))) continue;
