@@ -15,12 +15,12 @@
 //
 // Roles (16 warps, one CTA per SM, persistent over items):
 //   warps 0-3, 4-7   softmax of q tile 0 and 1: S from TMEM, P back into the columns of S
-//   warps 8-11       correction: rescale O in TMEM when a row's maximum grew; epilogue
+//   warps 8-11       epilogue: O / l to memory, while the next item's first tiles run
 //   warp 12          loads (TMA): Q, then K and V tiles in a ring
-//   warp 13          MMA issue: S_0, S_1, then per key tile O_0, S_0', O_1, S_1'
-//   warp 14          zeroes the rows of V past a sequence's end in its last tile (their
+//   warps 13, 14     MMA issue for q tile 0 and 1: S, then per key tile O and the next S
+//   warp 15          schedule: the CTA's items, longest first over the whole call; and
+//                    zeroes the rows of V past a sequence's end in its last tile (their
 //                    weights are zero, their values may be anything)
-//   warp 15          schedule: the CTA's items, longest first over the whole call
 // The two q tiles alternate, so that the tensor core works on one while the softmax of
 // the other runs. TMEM: S_0, S_1 (128 columns each), O_0, O_1.
 //
@@ -98,19 +98,6 @@ __device__ __forceinline__ Range2 uniform(Range2 r)
     }
     r.nmax = r.n[0] > r.n[1] ? r.n[0] : r.n[1];
     return r;
-}
-// One look at a barrier.
-__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
 }
 __device__ __forceinline__ bool elect_one()
 {
@@ -353,10 +340,11 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
     const uint32_t misc = b0 + 16 * NST + 8 * DONE;
     const uint32_t q_full = misc, q_empty = misc + 16, s_full = misc + 32, p_full = misc + 48, o_empty = misc + 64,
                    l_full = misc + 80, l_empty = misc + 96, o_full = misc + 112, drain = misc + 128,
-                   p_half = misc + 144, it_full = misc + 160, it_empty = it_full + 8 * ITEMS;
+                   it_full = misc + 160, it_empty = it_full + 8 * ITEMS;
     Item *items = reinterpret_cast<Item *>(reinterpret_cast<uint8_t *>(bars) + 16 * NST + 8 * DONE + 160 + 16 * ITEMS);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(items + ITEMS);
-    static_assert(16 * NST + 8 * DONE + 160 + 16 * ITEMS + sizeof(Item) * ITEMS + 4 <= 768, "barrier area");
+    volatile uint32_t *turn = tmem_slot + 1;     // steps that the issuer of each q tile has done
+    static_assert(16 * NST + 8 * DONE + 160 + 16 * ITEMS + sizeof(Item) * ITEMS + 12 <= 768, "barrier area");
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     if ((sm_q & 1023u) != 0u) {  // the swizzled tiles need what the declaration asks for
@@ -368,12 +356,11 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
             mbar_init(kv_full + 8 * i, 1);
             mbar_init(v_raw + 8 * i, 1);
         }
-        for (int i = 0; i < DONE; ++i) mbar_init(kv_done + 8 * i, 1);
+        for (int i = 0; i < DONE; ++i) mbar_init(kv_done + 8 * i, 2);  // both issuing warps
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full + 8 * i, 1);
             mbar_init(q_empty + 8 * i, 1);
             mbar_init(s_full + 8 * i, 1);
-            mbar_init(p_half + 8 * i, 4);    // first half of P written, O rescaled
             mbar_init(p_full + 8 * i, 4);
             mbar_init(o_empty + 8 * i, 4);
             mbar_init(l_full + 8 * i, 4);
@@ -381,6 +368,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
             mbar_init(o_full + 8 * i, 1);
         }
         mbar_init(drain, 1);
+        mbar_init(drain + 8, 1);
+        turn[0] = turn[1] = 0;
         for (int i = 0; i < ITEMS; ++i) {
             mbar_init(it_full + 8 * i, 1);
             mbar_init(it_empty + 8 * i, 15);  // every warp but the schedule's
@@ -487,12 +476,10 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                         pk[c / 2] = pack_bf16x2(__float_as_uint(e0), __float_as_uint(e1));
                     }
                     tmem_st16(ts + c0 / 2, pk);
-                    if (c0 == 32 || c0 == 96) {
-                        tmem_wait_st();
-                        tc_fence_before();
-                        arrive((c0 == 32 ? p_half : p_full) + 8 * i);
-                    }
                 }
+                tmem_wait_st();
+                tc_fence_before();
+                arrive(p_full + 8 * i);
                 const uint64_t both = add2(sum[0], sum[1]);
                 l = l * f + (low(both) + high(both));
             }
@@ -643,132 +630,91 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
             }
             if (!alive) break;
         }
-    } else if (warp == 13) {
+    } else if (warp < 15) {
         // ------------------------------------------------------------ MMA issue
-        // The whole warp walks the tiles and one elected lane issues, on values that are the
-        // same in every lane (broadcast from lane 0, so that the compiler knows): descriptors
-        // then stay in uniform registers, and an issue costs less than the MMA takes.
-        uint32_t c = 0, n_done = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};  // n_q: items of the q tile
-        const uint64_t q_desc = smem_desc_sw128(sm_q), k_desc = smem_desc_sw128(sm_kv),
+        // A warp per q tile. The whole warp walks the tiles and one elected lane issues, on values
+        // that are the same in every lane (broadcast from lane 0, so that the compiler knows):
+        // descriptors then stay in uniform registers, and an issue costs less than the MMA takes.
+        // The two warps take turns, step by step: one waits for its weights while the other's
+        // MMAs are being taken by the tensor core, and the tiles stay half a period apart.
+        const int i = warp - 13;
+        uint32_t c = 0, n_done = 0, n_q = 0, n_p = 0, step = 0;
+        const uint32_t tp = tmem + TM_S + i * 128, to = tmem + TM_O + i * 128;
+        const uint64_t q_desc = smem_desc_sw128(sm_q + i * Sh::TILE_BYTES), k_desc = smem_desc_sw128(sm_kv),
                        v_desc = smem_desc_v(sm_kv, Sh::HALF_BYTES);
+        // Every tile of the ring is waited for, used or not: phases are seen one by one.
         auto wait_kv = [&](uint32_t cs) { return wait(kv_full + 8 * (cs % NST), (cs / NST) & 1); };
-        // S_i = Q_i K^T of the tile in ring slot cs
-        auto issue_s = [&](int i, uint32_t cs, int ext, bool last) {
-            const uint64_t q = q_desc + i * (Sh::TILE_BYTES / 16), kk = k_desc + (cs % NST) * (Sh::TILE_BYTES / 16);
-            const uint32_t idesc = prompt_idesc(ext, false);
-#pragma unroll
-            for (int s = 0; s < D / 16; ++s) {
-                const int o = (s / 4) * (Sh::HALF_BYTES / 16) + (s % 4) * 2;
-                umma_ss(tmem + TM_S + i * 128, q + o, kk + o, idesc, s > 0);
+        auto in_turn = [&](uint32_t g) {
+            const volatile uint32_t *other = turn + (1 - i);
+            bool mine = __all_sync(0xffffffffu, static_cast<int32_t>(*other - g) >= 0) != 0;
+            if (mine) return true;
+            WaitClock clk;
+            for (uint32_t n = 1; !mine; ++n) {
+                mine = __all_sync(0xffffffffu, static_cast<int32_t>(*other - g) >= 0) != 0;
+                if ((n & 15u) == 0 && !mine && !__all_sync(0xffffffffu, clk.ok(wc))) return alive = false;
             }
-            umma_commit(s_full + 8 * i);
-            if (last) umma_commit(q_empty + 8 * i);
+            return true;
         };
         Item it;
         for (uint32_t k = 0; next_item(k, it); ++k) {
             const Range2 r = uniform(ranges(it, tpt));
-            if (r.nmax == 0) continue;
-            if (!wait_kv(c)) break;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (r.n[i] == 0 || !alive) continue;
-                if (!wait(q_full + 8 * i, n_q[i] & 1)) continue;
-                ++n_q[i];
-                tc_fence_after();
-                if (elect_one()) issue_s(i, c, extent(r.lim[i], 0), r.n[i] == 1);
-                __syncwarp();
+            const int n = i == 0 ? r.n[0] : r.n[1], lim = i == 0 ? r.lim[0] : r.lim[1];
+            if (n > 0) {
+                if (!wait(q_full + 8 * i, n_q & 1)) break;
+                ++n_q;
             }
-            if (!alive) break;
-            if (elect_one()) umma_commit(kv_done + 8 * (n_done % DONE));
-            ++n_done;
-            for (int j = 0; j < r.nmax && alive; ++j) {
-                const uint32_t cv = c + 2 * j + 1, ck = cv + 1;
-                const bool more = j + 1 < r.nmax;
-                const uint64_t v = v_desc + (cv % NST) * (Sh::TILE_BYTES / 16);
-                constexpr uint32_t idesc = prompt_idesc(D, true);
-                // The tiles are mostly there before the weights are: their barriers are looked
-                // at together with those of the weights, one latency for all.
-                bool kv = mbar_test_wait(kv_full + 8 * (cv % NST), (cv / NST) & 1);
-                if (more) kv = mbar_test_wait(kv_full + 8 * (ck % NST), (ck / NST) & 1) && kv;
-                bool seen = false;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (j >= r.n[i] || !alive) continue;
-                    const uint32_t tp = tmem + TM_S + i * 128, to = tmem + TM_O + i * 128;
-                    const int steps = extent(r.lim[i], j) / 16;
-                    const bool last = j == r.n[i] - 1;
-                    const uint32_t par = n_p[i] & 1;
-                    const bool half = mbar_test_wait(p_half + 8 * i, par);
-                    const bool full = mbar_test_wait(p_full + 8 * i, par);
-                    if (j == 0 && !wait(o_empty + 8 * i, n_q[i] & 1)) continue;  // (n_q - 1) items written out
-                    bool whole = __all_sync(0xffffffffu, (seen || kv) && half && full) != 0;
-                    if (!whole) {
-                        if (!seen && (!wait_kv(cv) || (more && !wait_kv(ck)))) continue;
-                        if (!wait(p_half + 8 * i, par)) continue;
-                        if (steps == 8) {
-                            tc_fence_after();
-                            if (elect_one()) {
-#pragma unroll
-                                for (int s = 0; s < 4; ++s) umma_ts(to, tp + s * 8, v + s * 128, idesc, j > 0 || s > 0);
-                            }
-                            __syncwarp();
-                        }
-                        if (!wait(p_full + 8 * i, par)) continue;
-                    }
-                    seen = true;
-                    ++n_p[i];
-                    tc_fence_after();
-                    if (elect_one()) {
-                        if (steps == 8) {
-                            if (whole) {
-#pragma unroll
-                                for (int s = 0; s < 4; ++s) umma_ts(to, tp + s * 8, v + s * 128, idesc, j > 0 || s > 0);
-                            }
-#pragma unroll
-                            for (int s = 4; s < 8; ++s) umma_ts(to, tp + s * 8, v + s * 128, idesc, 1);
-                        } else {  // the sequence's last keys
-                            for (int s = 0; s < steps; ++s) umma_ts(to, tp + s * 8, v + s * 128, idesc, j > 0 || s > 0);
-                        }
-                        if (last) umma_commit(o_full + 8 * i);
-                        else issue_s(i, ck, extent(r.lim[i], j + 1), j + 2 == r.n[i]);
-                    }
-                    __syncwarp();
+            // Step j: O += P V of tile j, then S of tile j + 1. Ring: V of tile j at c - 1, K of
+            // tile j + 1 at c.
+            for (int j = -1; j < r.nmax; ++j, c += 2) {
+                const bool has_v = j >= 0, has_k = j + 1 < r.nmax;
+                const bool pv = has_v && j < n, s_next = has_k && j + 1 < n;
+                if (has_v && !wait_kv(c - 1)) break;
+                if (has_k && !wait_kv(c)) break;
+                if (j == 0 && pv && !wait(o_empty + 8 * i, n_q & 1)) break;  // n_q - 1 items written out
+                if (pv) {
+                    if (!wait(p_full + 8 * i, n_p & 1)) break;
+                    ++n_p;
                 }
-                if (!alive) break;
-                if (elect_one()) umma_commit(kv_done + 8 * (n_done % DONE));
-                ++n_done;
+                ++step;
+                if (!in_turn(step - 1 + i)) break;
+                tc_fence_after();
+                const uint64_t v = v_desc + ((c - 1) % NST) * (Sh::TILE_BYTES / 16);
+                const uint64_t kk = k_desc + (c % NST) * (Sh::TILE_BYTES / 16);
+                const int steps = pv ? extent(lim, j) / 16 : 0;
+                const uint32_t s_idesc = prompt_idesc(s_next ? extent(lim, j + 1) : 16, false);
+                constexpr uint32_t o_idesc = prompt_idesc(D, true);
+                if (elect_one()) {
+                    if (steps == PROMPT_KEYS / 16) {
+#pragma unroll
+                        for (int s = 0; s < PROMPT_KEYS / 16; ++s) umma_ts(to, tp + s * 8, v + s * 128, o_idesc, j > 0 || s > 0);
+                    } else {  // the sequence's last keys
+                        for (int s = 0; s < steps; ++s) umma_ts(to, tp + s * 8, v + s * 128, o_idesc, j > 0 || s > 0);
+                    }
+                    if (s_next) {
+#pragma unroll
+                        for (int s = 0; s < D / 16; ++s) {
+                            const int o = (s / 4) * (Sh::HALF_BYTES / 16) + (s % 4) * 2;
+                            umma_ss(tp, q_desc + o, kk + o, s_idesc, s > 0);
+                        }
+                        umma_commit(s_full + 8 * i);
+                        if (j + 2 == n) umma_commit(q_empty + 8 * i);
+                    }
+                    turn[i] = step;
+                    if (pv && j == n - 1) umma_commit(o_full + 8 * i);
+                    if (has_v || has_k) umma_commit(kv_done + 8 * (n_done % DONE));
+                }
+                __syncwarp();
+                if (has_v || has_k) ++n_done;
             }
             if (!alive) break;
-            c += 2 * r.nmax;
+            c -= 2;  // nmax + 1 steps over 2 nmax tiles
         }
         // everything issued has completed before TMEM goes back
         if (elect_one()) {
-            umma_commit(drain);
-            mbar_wait_drain(drain, 0, p.timeout_ns);
+            umma_commit(drain + 8 * i);
+            mbar_wait_drain(drain + 8 * i, 0, p.timeout_ns);
         }
         __syncwarp();
-    } else if (warp == 14) {
-        // ------------------------------------------------------------ V past the end
-        uint32_t c = 0, used = 0;                      // ring position; phase bit per stage of v_raw
-        Item it;
-        for (uint32_t k = 0; next_item(k, it); ++k) {
-            const Range2 r = ranges(it, tpt);
-            if (r.nmax == 0) continue;
-            const int j = r.nmax - 1, valid = it.len - j * PROMPT_KEYS, ext = extent(r.limmax, j);
-            if (ext > valid) {
-                const uint32_t st = (c + 2 * j + 1) % NST;
-                if (!wait(v_raw + 8 * st, (used >> st) & 1)) break;
-                used ^= 1u << st;
-                const uint32_t v = sm_kv + st * Sh::TILE_BYTES;
-                for (int u = lane; u < (ext - valid) * (D / 8); u += 32) {
-                    const int rr = valid + u / (D / 8), ch = u % (D / 8);
-                    st_shared_v4(v + (ch / 8) * Sh::HALF_BYTES + rr * 128 + (ch % 8) * 16, 0u, 0u, 0u, 0u);
-                }
-                fence_proxy_async_shared();
-                arrive(kv_full + 8 * st);
-            }
-            c += 2 * r.nmax;
-        }
     } else {
         // ------------------------------------------------------------ schedule
         const int tokens = 2 * tpt;
@@ -783,8 +729,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) cmax = max(cmax, __shfl_xor_sync(0xffffffffu, cmax, o));
         const int64_t total = static_cast<int64_t>(tiles) * p.units;
-        // Longest first, dealt forth and back over the CTAs.
-        for (uint32_t k = 0;; ++k) {
+        // Longest first, dealt forth and back over the CTAs. Item k + 2 is published before the
+        // zeroing of item k is waited for: its slot was free before item k could begin.
+        auto publish = [&](uint32_t k) {
             const int64_t g = static_cast<int64_t>(k) * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
             Item it{-1, 0, 0, 0, 0, 0};
             if (g < total) {
@@ -792,10 +739,35 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                 it.unit = static_cast<int>(g % p.units);
             }
             const uint32_t slot = k % ITEMS;
-            if (k >= ITEMS && !wait(it_empty + 8 * slot, (k / ITEMS - 1) & 1)) break;
+            if (k >= ITEMS && !wait(it_empty + 8 * slot, (k / ITEMS - 1) & 1)) return it;
             if (lane == 0) items[slot] = it;
             arrive(it_full + 8 * slot);
-            if (it.row0 < 0) break;
+            return it;
+        };
+        uint32_t c = 0, used = 0;                      // ring position; phase bit per stage of v_raw
+        Item it = publish(0), it1 = it, it2;
+        if (it.row0 >= 0) it1 = publish(1);
+        for (uint32_t k = 0; it.row0 >= 0 && alive; ++k) {
+            it2 = it1;
+            if (it1.row0 >= 0) it2 = publish(k + 2);
+            const Range2 r = ranges(it, tpt);
+            const int j = r.nmax - 1, valid = it.len - j * PROMPT_KEYS;
+            const int ext = r.nmax > 0 ? extent(r.limmax, j) : 0;
+            if (ext > valid && alive) {
+                const uint32_t st = (c + 2 * j + 1) % NST;
+                if (!wait(v_raw + 8 * st, (used >> st) & 1)) break;
+                used ^= 1u << st;
+                const uint32_t v = sm_kv + st * Sh::TILE_BYTES;
+                for (int u = lane; u < (ext - valid) * (D / 8); u += 32) {
+                    const int rr = valid + u / (D / 8), ch = u % (D / 8);
+                    st_shared_v4(v + (ch / 8) * Sh::HALF_BYTES + rr * 128 + (ch % 8) * 16, 0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_shared();
+                arrive(kv_full + 8 * st);
+            }
+            c += 2 * r.nmax;
+            it = it1;
+            it1 = it2;
         }
       }
     }
