@@ -170,8 +170,8 @@ namespace {
 
 // Control block, in 32-bit words: the readiness flags [0, UB_MAX_TP), the partial-tile
 // flags [UB_MAX_TP, UB_MAX_TP + W) with W = ws_slots * EPI_WARPS, then the abort word, the
-// status word, the gather's per-chunk counters and the decode attention's join counters
-// (both zero between calls). The words a captured call clears (flags and partial-tile
+// status word, the gather's per-chunk counters, the decode attention's join counters and
+// the prompt attention's tickets (all zero between calls). The words a captured call clears (flags and partial-tile
 // flags) are one contiguous run.
 size_t ws_flag_words(const ub_handle *h) { return static_cast<size_t>(h->ws_slots) * ubk::EPI_WARPS; }
 uint32_t *flags_of(ub_handle *h) { return h->ctrl; }
@@ -735,6 +735,7 @@ int ubk::handle_call(ub_handle_t h, cudaStream_t s, HandleCall *out)
     out->ws_floats = static_cast<size_t>(h->ws_slots) * PARTIAL_FLOATS;
     out->join_counters = join_counters_of(h);
     out->join_words = join_words(h);
+    out->tickets = join_counters_of(h) + join_words(h);
     h->counters.last_T = h->T;
     return UB_OK;
 }
@@ -855,7 +856,7 @@ int ub_create(int64_t max_tokens, int64_t hidden, int tp, ub_dtype_t dtype, ub_h
     ++h->counters.device_allocations;
     h->max_pairs = h->sm_count / 2 > 0 ? h->sm_count / 2 : 1;
     h->ws_slots = 2 * (h->sm_count > 0 ? h->sm_count : 1);
-    h->ctrl_bytes = (UB_MAX_TP + ws_flag_words(h) + 8 + UB_MAX_TP + join_words(h)) * sizeof(uint32_t);
+    h->ctrl_bytes = (UB_MAX_TP + ws_flag_words(h) + 8 + UB_MAX_TP + join_words(h) + 2) * sizeof(uint32_t);
     e = cudaMalloc(reinterpret_cast<void **>(&h->ctrl), h->ctrl_bytes);
     if (e != cudaSuccess) return cleanup(cuda_fail(e, "cudaMalloc(control block)"));
     ++h->counters.device_allocations;

@@ -28,6 +28,7 @@ struct HandleCall {
     size_t ws_floats;
     uint32_t *join_counters; // zero between calls
     int join_words;
+    uint32_t *tickets;       // two words, zero between calls
 };
 
 int handle_device(ub_handle_t h);
@@ -112,6 +113,7 @@ struct PromptParams {
     int pack_shift;          // 1 << pack_shift query heads of one key/value head share a q tile
     int units;               // kv_heads * (group >> pack_shift)
     float scale;
+    uint32_t *tickets;       // work items drawn, CTAs done; zero between calls
     uint32_t *abort_word;
     uint64_t timeout_ns;
     uint32_t epoch;

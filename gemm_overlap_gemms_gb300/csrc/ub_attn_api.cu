@@ -269,6 +269,7 @@ int ub_attn_prompt(ub_handle_t h, const ub_attn_t *in, void *stream)
     p.head_dim = a.head_dim;
     p.units = a.kv_heads * (p.group >> p.pack_shift);
     p.scale = a.scale;
+    p.tickets = c.tickets;
     p.abort_word = c.abort_word;
     p.timeout_ns = c.timeout_ns;
     p.epoch = c.epoch;

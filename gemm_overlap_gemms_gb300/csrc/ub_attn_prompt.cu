@@ -99,6 +99,22 @@ __device__ __forceinline__ Range2 uniform(Range2 r)
     r.nmax = r.n[0] > r.n[1] ? r.n[0] : r.n[1];
     return r;
 }
+// A wait on the critical path: looks at the barrier for a while without being suspended.
+__device__ __forceinline__ bool mbar_wait_hot(uint32_t bar, uint32_t parity, const WaitCtx &w)
+{
+    for (int n = 0; n < 256; ++n) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (ok) return true;
+    }
+    return mbar_wait(bar, parity, w);
+}
 __device__ __forceinline__ bool elect_one()
 {
     uint32_t e;
@@ -254,75 +270,86 @@ __device__ __forceinline__ SeqInfo seq_info(const PromptParams &p, int s)
     q.off = q.len - q.n;
     return q;
 }
-// Items (token tiles) of the sequence that reach at least `c` key tiles.
-__device__ __forceinline__ int items_from(const SeqInfo &q, int c, int tokens)
+// Items (token tiles of 1 << shift tokens) of the sequence that reach at least `c` key tiles.
+__device__ __forceinline__ int items_from(const SeqInfo &q, int c, int shift)
 {
-    const int nt = (q.n + tokens - 1) / tokens;
+    const int nt = (q.n + (1 << shift) - 1) >> shift;
+    const int x = (c - 1) * PROMPT_KEYS;
     if (c <= 0) return nt;
-    const int64_t x = static_cast<int64_t>(c - 1) * PROMPT_KEYS;
     if (q.len <= x) return 0;
-    const int64_t t = x < q.off ? 0 : (x - q.off) / tokens;
-    return nt - (t < nt ? static_cast<int>(t) : nt);
-}
-__device__ __forceinline__ int warp_sum(int v)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-__device__ int count_from(const PromptParams &p, int c, int tokens, int lane)
-{
-    int sum = 0;
-    for (int i = lane; i < p.b.n_seqs; i += 32) sum += items_from(seq_info(p, i), c, tokens);
-    return warp_sum(sum);
+    const uint32_t t = x < q.off ? 0u : (static_cast<uint32_t>(x) - static_cast<uint32_t>(q.off)) >> shift;
+    return nt - (t < static_cast<uint32_t>(nt) ? static_cast<int>(t) : nt);
 }
 
-// Item of rank g in the order "most key tiles first" (ties: by sequence, then by tile).
-__device__ Item item_at(const PromptParams &p, int g, int cmax, int tokens, int lane)
-{
-    int lo = 0, hi = cmax;  // count(lo) > g; find the largest such level
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (count_from(p, mid, tokens, lane) > g) lo = mid;
-        else hi = mid - 1;
+// The work items of a call in the order "most key tiles first" (ties: by sequence, then by
+// tile), without a list: one warp counts the items of at least c key tiles over all
+// sequences and searches for the level of a rank. Up to 32 sequences stay in registers, one
+// per lane; beyond, they are read again for every count (from L1).
+struct Schedule {
+    const PromptParams &p;
+    int lane, shift, cmax, tiles;
+    SeqInfo own;
+
+    __device__ __forceinline__ SeqInfo info(int i0) const
+    {
+        if (i0 == 0) return own;
+        return i0 + lane < p.b.n_seqs ? seq_info(p, i0 + lane) : SeqInfo{0, 0, 0, 0};
     }
-    int r = g - count_from(p, lo + 1, tokens, lane);
-    Item it{-1, 0, 0, 0, 0, 0};
-    for (int i0 = 0; i0 < p.b.n_seqs; i0 += 32) {
-        SeqInfo q{0, 0, 0, 0};
-        int mine = 0, from = 0;
-        if (i0 + lane < p.b.n_seqs) {
-            q = seq_info(p, i0 + lane);
-            from = items_from(q, lo, tokens);
-            mine = from - items_from(q, lo + 1, tokens);
+    __device__ __forceinline__ Schedule(const PromptParams &params, int ln, int sh) : p(params), lane(ln), shift(sh)
+    {
+        own = lane < p.b.n_seqs ? seq_info(p, lane) : SeqInfo{0, 0, 0, 0};
+        int most = 0, sum = 0;
+        for (int i0 = 0; i0 < p.b.n_seqs; i0 += 32) {
+            const SeqInfo q = info(i0);
+            const int n = q.n > 0 ? static_cast<int>((static_cast<uint32_t>(q.len) + PROMPT_KEYS - 1) / PROMPT_KEYS) : 0;
+            most = n > most ? n : most;
+            sum += items_from(q, 0, shift);
         }
-        int upto = mine;
+        cmax = __reduce_max_sync(0xffffffffu, most);
+        tiles = __reduce_add_sync(0xffffffffu, sum);
+    }
+    __device__ __forceinline__ int count(int c) const
+    {
+        int sum = 0;
+        for (int i0 = 0; i0 < p.b.n_seqs; i0 += 32) sum += items_from(info(i0), c, shift);
+        return __reduce_add_sync(0xffffffffu, sum);
+    }
+    __device__ Item at(int g) const
+    {
+        int lo = 0, hi = cmax;  // count(lo) > g; find the largest such level
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (count(mid) > g) lo = mid;
+            else hi = mid - 1;
+        }
+        int r = g - count(lo + 1);
+        Item it{-1, 0, 0, 0, 0, 0};
+        for (int i0 = 0; i0 < p.b.n_seqs; i0 += 32) {
+            const SeqInfo q = info(i0);
+            const int from = items_from(q, lo, shift), mine = from - items_from(q, lo + 1, shift);
+            int upto = mine;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += x;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += x;
+            }
+            const uint32_t past = __ballot_sync(0xffffffffu, upto > r);
+            if (past != 0u) {
+                const int l = __ffs(static_cast<int>(past)) - 1;
+                const int tile = items_from(q, 0, shift) - from + (r - (upto - mine));
+                const int t0 = tile << shift;
+                it.row0 = __shfl_sync(0xffffffffu, q.start + t0, l);
+                it.ntok = __shfl_sync(0xffffffffu, q.n - t0 < (1 << shift) ? q.n - t0 : 1 << shift, l);
+                it.off = __shfl_sync(0xffffffffu, q.off + t0, l);
+                it.len = __shfl_sync(0xffffffffu, q.len, l);
+                it.src = __shfl_sync(0xffffffffu, p.paged ? i0 + lane : q.start, l);
+                return it;
+            }
+            r -= __shfl_sync(0xffffffffu, upto, 31);
         }
-        const uint32_t past = __ballot_sync(0xffffffffu, upto > r);
-        if (past != 0u) {
-            const int l = __ffs(static_cast<int>(past)) - 1;
-            const int nt = (q.n + tokens - 1) / tokens;
-            const int tile = nt - from + (r - (upto - mine));
-            it.row0 = q.start + tile * tokens;
-            it.ntok = q.n - tile * tokens < tokens ? q.n - tile * tokens : tokens;
-            it.off = q.off + tile * tokens;
-            it.len = q.len;
-            it.src = p.paged ? i0 + lane : q.start;
-            it.row0 = __shfl_sync(0xffffffffu, it.row0, l);
-            it.ntok = __shfl_sync(0xffffffffu, it.ntok, l);
-            it.off = __shfl_sync(0xffffffffu, it.off, l);
-            it.len = __shfl_sync(0xffffffffu, it.len, l);
-            it.src = __shfl_sync(0xffffffffu, it.src, l);
-            return it;
-        }
-        r -= __shfl_sync(0xffffffffu, upto, 31);
+        return it;
     }
-    return it;
-}
+};
 
 // ---------------------------------------------------------------- kernel
 
@@ -339,7 +366,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
     const uint32_t kv_full = b0, v_raw = b0 + 8 * NST, kv_done = b0 + 16 * NST;
     const uint32_t misc = b0 + 16 * NST + 8 * DONE;
     const uint32_t q_full = misc, q_empty = misc + 16, s_full = misc + 32, p_full = misc + 48, o_empty = misc + 64,
-                   l_full = misc + 80, l_empty = misc + 96, o_full = misc + 112, drain = misc + 128,
+                   l_full = misc + 80, l_empty = misc + 96, o_full = misc + 112, drain = misc + 128, want = misc + 144,
                    it_full = misc + 160, it_empty = it_full + 8 * ITEMS;
     Item *items = reinterpret_cast<Item *>(reinterpret_cast<uint8_t *>(bars) + 16 * NST + 8 * DONE + 160 + 16 * ITEMS);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(items + ITEMS);
@@ -369,6 +396,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
         }
         mbar_init(drain, 1);
         mbar_init(drain + 8, 1);
+        mbar_init(want, 1);
         turn[0] = turn[1] = 0;
         for (int i = 0; i < ITEMS; ++i) {
             mbar_init(it_full + 8 * i, 1);
@@ -393,6 +421,10 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
     bool alive = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
         alive = __all_sync(0xffffffffu, mbar_wait(bar, parity, wc)) != 0;
+        return alive;
+    };
+    auto wait_hot = [&](uint32_t bar, uint32_t parity) {
+        alive = __all_sync(0xffffffffu, mbar_wait_hot(bar, parity, wc)) != 0;
         return alive;
     };
     auto arrive = [&](uint32_t bar) {
@@ -425,7 +457,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
             reach = reach > it.len ? it.len : reach;
             float m = -INFINITY, l = 0.f;
             for (int j = 0; j < r.n[i]; ++j) {
-                if (!wait(s_full + 8 * i, n_s & 1)) break;
+                if (!wait_hot(s_full + 8 * i, n_s & 1)) break;
                 ++n_s;
                 tc_fence_after();
                 float s[128];
@@ -560,7 +592,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
         Item it;
         const int box = PROMPT_KEYS < (1 << p.b.page_shift) ? PROMPT_KEYS : (1 << p.b.page_shift);
         constexpr int HALVES = D / 64;
-        for (uint32_t k = 0; next_item(k, it); ++k) {
+        for (uint32_t k = 0;; ++k) {
+            if (k >= 2) arrive(want);                  // every load of item k - 1 has been issued
+            if (!next_item(k, it)) break;
             const Range2 r = ranges(it, tpt);
             const int kvh = (it.unit << p.pack_shift) / p.group;
             const int32_t *table = p.paged ? p.b.page_table + it.src * p.b.table_row : nullptr;
@@ -671,18 +705,18 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                 if (has_v && !wait_kv(c - 1)) break;
                 if (has_k && !wait_kv(c)) break;
                 if (j == 0 && pv && !wait(o_empty + 8 * i, n_q & 1)) break;  // n_q - 1 items written out
-                if (pv) {
-                    if (!wait(p_full + 8 * i, n_p & 1)) break;
-                    ++n_p;
-                }
                 ++step;
                 if (!in_turn(step - 1 + i)) break;
-                tc_fence_after();
                 const uint64_t v = v_desc + ((c - 1) % NST) * (Sh::TILE_BYTES / 16);
                 const uint64_t kk = k_desc + (c % NST) * (Sh::TILE_BYTES / 16);
                 const int steps = pv ? extent(lim, j) / 16 : 0;
                 const uint32_t s_idesc = prompt_idesc(s_next ? extent(lim, j + 1) : 16, false);
                 constexpr uint32_t o_idesc = prompt_idesc(D, true);
+                if (pv) {
+                    if (!wait_hot(p_full + 8 * i, n_p & 1)) break;
+                    ++n_p;
+                }
+                tc_fence_after();
                 if (elect_one()) {
                     if (steps == PROMPT_KEYS / 16) {
 #pragma unroll
@@ -717,43 +751,42 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
         __syncwarp();
     } else {
         // ------------------------------------------------------------ schedule
-        const int tokens = 2 * tpt;
-        int cmax = 0, tiles = 0;
-        for (int i = lane; i < p.b.n_seqs; i += 32) {
-            const SeqInfo q = seq_info(p, i);
-            const int n = (q.len + PROMPT_KEYS - 1) / PROMPT_KEYS;
-            if (q.n > 0 && n > cmax) cmax = n;
-            tiles += (q.n + tokens - 1) / tokens;
-        }
-        tiles = warp_sum(tiles);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) cmax = max(cmax, __shfl_xor_sync(0xffffffffu, cmax, o));
-        const int64_t total = static_cast<int64_t>(tiles) * p.units;
-        // Longest first, dealt forth and back over the CTAs. Item k + 2 is published before the
-        // zeroing of item k is waited for: its slot was free before item k could begin.
+        const Schedule sched(p, lane, 8 - p.pack_shift);
+        const int64_t total = static_cast<int64_t>(sched.tiles) * p.units;
+        // Longest first. The first two items of each CTA are dealt forth and back over the CTAs,
+        // the rest by tickets, drawn when the loads of the item before have been issued.
         auto publish = [&](uint32_t k) {
-            const int64_t g = static_cast<int64_t>(k) * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            int64_t g = k == 0 ? blockIdx.x : 2 * static_cast<int64_t>(gridDim.x) - 1 - blockIdx.x;
+            if (k >= 2) {
+                uint32_t ticket = 0;
+                if (lane == 0) ticket = atomicAdd(p.tickets, 1u);
+                g = 2 * static_cast<int64_t>(gridDim.x) + __shfl_sync(0xffffffffu, ticket, 0);
+            }
             Item it{-1, 0, 0, 0, 0, 0};
             if (g < total) {
-                it = item_at(p, static_cast<int>(g / p.units), cmax, tokens, lane);
-                it.unit = static_cast<int>(g % p.units);
+                const uint32_t rank = static_cast<uint32_t>(g);  // fewer than 2^32 items: T * heads rows
+                it = sched.at(static_cast<int>(rank / static_cast<uint32_t>(p.units)));
+                it.unit = static_cast<int>(rank % static_cast<uint32_t>(p.units));
             }
-            const uint32_t slot = k % ITEMS;
-            if (k >= ITEMS && !wait(it_empty + 8 * slot, (k / ITEMS - 1) & 1)) return it;
-            if (lane == 0) items[slot] = it;
-            arrive(it_full + 8 * slot);
+            if (k >= ITEMS && !wait(it_empty + 8 * (k % ITEMS), (k / ITEMS - 1) & 1)) return it;
+            if (lane == 0) items[k % ITEMS] = it;
+            arrive(it_full + 8 * (k % ITEMS));
             return it;
         };
         uint32_t c = 0, used = 0;                      // ring position; phase bit per stage of v_raw
-        Item it = publish(0), it1 = it, it2;
+        Item it = publish(0), it1 = it;
         if (it.row0 >= 0) it1 = publish(1);
         for (uint32_t k = 0; it.row0 >= 0 && alive; ++k) {
-            it2 = it1;
-            if (it1.row0 >= 0) it2 = publish(k + 2);
+            // it: item k, it1: item k + 1, published before the zeroing of item k is waited for
+            if (k >= 1) {
+                if (!wait(want, (k - 1) & 1)) break;
+                it1 = publish(k + 1);
+                if (!alive) break;
+            }
             const Range2 r = ranges(it, tpt);
             const int j = r.nmax - 1, valid = it.len - j * PROMPT_KEYS;
             const int ext = r.nmax > 0 ? extent(r.limmax, j) : 0;
-            if (ext > valid && alive) {
+            if (ext > valid) {
                 const uint32_t st = (c + 2 * j + 1) % NST;
                 if (!wait(v_raw + 8 * st, (used >> st) & 1)) break;
                 used ^= 1u << st;
@@ -767,7 +800,6 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
             }
             c += 2 * r.nmax;
             it = it1;
-            it1 = it2;
         }
       }
     }
@@ -777,6 +809,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
     __syncthreads();
     tc_fence_after();
     if (warp == 13) tmem_dealloc(tmem, 512);
+    // The last CTA of the call leaves the tickets at zero.
+    if (threadIdx.x == 0 && atomicAdd(p.tickets + 1, 1u) == gridDim.x - 1) p.tickets[0] = p.tickets[1] = 0u;
 }
 
 template <int D>
