@@ -1697,6 +1697,8 @@ int ub_clear_status(ub_handle_t h)
     if (int rc = check_handle(h)) return rc;
     DeviceGuard g(h->device);
     UB_CUDA(cudaMemsetAsync(abort_of(h), 0, 2 * sizeof(uint32_t), h->side));  // abort and status words
+    // what a call whose wait ran out may have left counted
+    UB_CUDA(cudaMemsetAsync(join_counters_of(h), 0, (join_words(h) + 2) * sizeof(uint32_t), h->side));
     UB_CUDA(cudaStreamSynchronize(h->side));
     return UB_OK;
 }

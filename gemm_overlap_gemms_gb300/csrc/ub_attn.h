@@ -76,7 +76,7 @@ struct AppendParams {
 cudaError_t launch_kv_append(const AppendParams &p, cudaStream_t s);
 
 struct DecodeParams {
-    CUtensorMap tmK, tmV;    // [pages, kv_heads, page_size, head_dim]
+    CUtensorMap tmK, tmV;    // [pages, kv_heads, head_dim / 64, page_size, 64]
     SeqBatch b;
     const void *q;
     void *out;
@@ -95,10 +95,10 @@ struct DecodeParams {
 };
 cudaError_t launch_attn_decode(const DecodeParams &p, int grid, cudaStream_t s);
 constexpr int DECODE_KEYS = 32;          // keys of one tile
-constexpr int DECODE_CTAS_PER_SM = 2;
+constexpr int DECODE_CTAS_PER_SM = 1;
 constexpr int DECODE_HEADS = 16;         // query heads of one pass over a key/value head, at most
-constexpr int DECODE_SLOTS = 4;          // workspace slots per CTA
-constexpr int DECODE_COUNTERS = 3;       // join counters per CTA
+constexpr int DECODE_SLOTS = 2;          // workspace slots per CTA
+constexpr int DECODE_COUNTERS = 2;       // join counters per CTA
 __host__ __device__ constexpr int decode_slot_floats(int head_dim) { return DECODE_HEADS * (head_dim + 2); }
 
 struct PromptParams {

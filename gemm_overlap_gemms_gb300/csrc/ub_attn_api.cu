@@ -136,6 +136,18 @@ int encode_pages(CUtensorMap *map, const ub_pages_t &x, const ub_attn_t &a, int 
     return encode_nd(map, x.data, 4, dims, strides, box);
 }
 
+// The same with the head dimension as head_dim / 64 times 64 columns, whole in every box.
+int encode_pages_whole(CUtensorMap *map, const ub_pages_t &x, const ub_attn_t &a, int box_rows)
+{
+    const uint64_t dims[5] = {64, static_cast<uint64_t>(a.page_size), static_cast<uint64_t>(a.head_dim / 64),
+                              static_cast<uint64_t>(a.kv_heads), static_cast<uint64_t>(a.num_pages)};
+    const uint64_t strides[5] = {2, static_cast<uint64_t>(x.row) * 2, 128, static_cast<uint64_t>(x.head) * 2,
+                                 static_cast<uint64_t>(x.page) * 2};
+    const uint32_t box[5] = {64, static_cast<uint32_t>(a.page_size < box_rows ? a.page_size : box_rows),
+                             static_cast<uint32_t>(a.head_dim / 64), 1, 1};
+    return encode_nd(map, x.data, 5, dims, strides, box);
+}
+
 // Packed tokens [T, heads, head_dim] in boxes of `box_heads` heads by `box_tokens` tokens.
 int encode_tokens(CUtensorMap *map, const ub_heads_t &x, int64_t T, int heads, int head_dim, int box_heads, int box_tokens)
 {
@@ -304,8 +316,8 @@ int ub_attn_decode(ub_handle_t h, const ub_attn_t *in, void *stream)
     if (int rc = handle_call(h, s, &c)) return rc;
     DecodeParams p;
     memset(&p, 0, sizeof p);
-    if (int rc = encode_pages(&p.tmK, a.k_cache, a, DECODE_KEYS)) return rc;
-    if (int rc = encode_pages(&p.tmV, a.v_cache, a, DECODE_KEYS)) return rc;
+    if (int rc = encode_pages_whole(&p.tmK, a.k_cache, a, DECODE_KEYS)) return rc;
+    if (int rc = encode_pages_whole(&p.tmV, a.v_cache, a, DECODE_KEYS)) return rc;
     handle_count_maps(h, 2);
     p.b = batch_of(a, c);
     p.q = a.q.data;

@@ -18,16 +18,18 @@
 // Work split: the (sequence, head, 32-key tile) triples of the whole call are laid end to
 // end and every CTA takes an equal, contiguous range, found on the device from kv_lens. So
 // ragged lengths, one long sequence and many short ones all load every SM alike, without
-// the host knowing a length. An item (sequence, head) that spans CTAs is joined by the CTA
-// that finishes last: each part goes to the workspace, a counter per item tells who came
-// last, and parts are added in CTA order (deterministic). Above 16 parts the join has two
-// levels, groups of 16 consecutive parts first, so that no CTA reads all of them.
+// the host knowing a length. The parts of an item that spans CTAs go to the workspace and are
+// joined in CTA order (deterministic) once a counter per item says that all are there: up to
+// JOIN_MOST parts by the CTA that comes last, more by all their CTAs, a share of the outputs
+// each, so that no CTA reads all of a long sequence's parts.
 //
-// A CTA is a loading warp and four computing warps, two CTAs on an SM. The loading warp
-// fills a ring of stages (one tile's keys and values) with TMA boxes of one page or one
-// tile, whichever is smaller; each computing warp takes every fourth tile by itself with
-// its own running maximum, so that no barrier separates tiles; the four partials are
-// joined in shared memory at the end of an item.
+// A CTA is four loading and four computing warps, one CTA on an SM. The loading warps fill a
+// ring of 192 KB (a stage is one tile's keys and values) with TMA boxes of one page or one
+// tile, whichever is smaller, every fourth tile each: issuing a tile of four boxes takes a
+// warp about 1000 cycles (measured), more than the 700 in which an SM's share of HBM delivers
+// it. Each computing warp takes every fourth tile by itself with its own running maximum, so
+// that no barrier separates tiles; the four partials are joined in shared memory at the end
+// of an item, while the ring goes on filling.
 #include <cuda_bf16.h>
 
 #include "ub_attn.h"
@@ -39,8 +41,10 @@ namespace {
 
 constexpr int KT = DECODE_KEYS;
 constexpr int WARPS = 4;
-constexpr int DEC_THREADS = 32 * (WARPS + 1);
-constexpr int JOIN_GROUP = 16;           // parts per first-level join
+constexpr int DEC_THREADS = 32 * 2 * WARPS;
+constexpr int JOIN_MOST = 8;             // parts that one CTA joins
+constexpr int MIN_TILES = 8;
+constexpr int WHOLE_TILES = 32;
 
 template <int D, int NT>
 struct DecShape {
@@ -49,13 +53,12 @@ struct DecShape {
     static constexpr int HEADS = 8 * NT;
     static constexpr int O_ROW = D + 4;                           // padded: conflict-free writes
     static constexpr int MERGE_BYTES = WARPS * HEADS * O_ROW * 4;
-    // As many stages as fit twice on an SM (115,712 bytes per CTA with the reserve).
-    static constexpr int STAGES_FIT = (115712 - 2048 - MERGE_BYTES) / STAGE_BYTES;
     // A multiple of WARPS, so that a stage always belongs to the same warp: the loads of two
     // tiles may land in either order, and a warp that waited for the second fill of a stage
     // whose first fill (another warp's) has not landed would see the parity it waits for.
-    static constexpr int STAGES = STAGES_FIT < 8 ? STAGES_FIT / WARPS * WARPS : 8;
-    static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + MERGE_BYTES + 768;
+    static constexpr int STAGES = 196608 / STAGE_BYTES;
+    static constexpr int SMEM = STAGES * STAGE_BYTES + MERGE_BYTES + 960;
+    static_assert(SMEM <= 232448, "shared memory");
     static_assert(STAGES >= WARPS && STAGES % WARPS == 0, "one warp per stage");
 };
 
@@ -75,6 +78,13 @@ __device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t *r)
                  : "memory");
 }
 
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 __device__ __forceinline__ uint32_t transpose8(uint32_t x)
 {
     uint32_t y;
@@ -91,30 +101,23 @@ __device__ __forceinline__ void mma_16x8x16(float *c, const uint32_t *a, uint32_
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int row,
-                                            int head, int page)
+// One box: rows of one page, all of the head dimension (64 columns after 64 columns).
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int row, int head, int page)
 {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(row), "r"(head), "r"(page)
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%3, %4, %3, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(row), "r"(head), "r"(page)
         : "memory");
 }
 
-__device__ __forceinline__ float4 ld_cg4(const float *p)
+// Counts one arrival; everything this CTA wrote before the barrier in front of it is visible
+// to whoever sees the count, and what the others wrote before theirs to this thread.
+__device__ __forceinline__ uint32_t arrive_acq_rel(uint32_t *counter)
 {
-    float4 v;
-    asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "l"(p)
-                 : "memory");
-    return v;
-}
-__device__ __forceinline__ float ld_cg(const float *p)
-{
-    float v;
-    asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
-    return v;
+    uint32_t old;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
+    return old;
 }
 
 __device__ __forceinline__ void bar_compute() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
@@ -127,6 +130,12 @@ __device__ __forceinline__ int clamped_len(const SeqBatch &b, int seq)
 }
 __device__ __forceinline__ int tiles_of(int len) { return len > 0 ? (len + KT - 1) / KT : 1; }
 
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
+{
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
 // The equal split of `total` tiles over `ctas`: CTA c's first tile, and the CTA of a tile.
 struct Split {
     int64_t base, rem;
@@ -134,19 +143,26 @@ struct Split {
     __device__ __forceinline__ int owner(int64_t x) const
     {
         const int64_t cut = rem * (base + 1);
-        return static_cast<int>(x < cut ? x / (base + 1) : rem + (x - cut) / base);
+        return static_cast<int>(x < cut ? quotient(x, base + 1) : rem + quotient(x - cut, base));
     }
 };
 
-// Sum of all lengths' tiles, and the sequence that holds per-head tile `x` (one warp).
-__device__ __forceinline__ int64_t total_tiles(const SeqBatch &b, int lane)
+// Sum and maximum of the sequences' tiles (one warp).
+__device__ __forceinline__ int64_t total_tiles(const SeqBatch &b, int lane, int *most)
 {
     int64_t sum = 0;
-    for (int i = lane; i < b.n_seqs; i += 32) sum += tiles_of(clamped_len(b, i));
+    int top = 0;
+    for (int i = lane; i < b.n_seqs; i += 32) {
+        const int n = tiles_of(clamped_len(b, i));
+        sum += n;
+        top = n > top ? n : top;
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    *most = __reduce_max_sync(0xffffffffu, top);
     return sum;
 }
+// The sequence that holds tile `tile` of all heads' tiles, and the tiles before it.
 __device__ __forceinline__ void find_seq(const SeqBatch &b, int lane, int64_t tile, int heads, int *seq, int64_t *before)
 {
     int64_t seen = 0;  // tiles of the sequences before this batch of 32, over all heads
@@ -178,16 +194,19 @@ __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
 {
     using Sh = DecShape<D, NT>;
     constexpr int S = Sh::STAGES;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t base[];
     float *sm_o = reinterpret_cast<float *>(base + S * Sh::STAGE_BYTES);
     uint64_t *bars = reinterpret_cast<uint64_t *>(base + S * Sh::STAGE_BYTES + Sh::MERGE_BYTES);
     float *sm_m = reinterpret_cast<float *>(bars + 2 * S);                     // [WARPS][HEADS]
     float *sm_l = sm_m + WARPS * DECODE_HEADS;                                 // [WARPS][HEADS]
     int *sm_last = reinterpret_cast<int *>(sm_l + WARPS * DECODE_HEADS);
-    static_assert(2 * S * 8 + 2 * WARPS * DECODE_HEADS * 4 + 4 <= 768, "barrier area");
+    static_assert(2 * S * 8 + 2 * WARPS * DECODE_HEADS * 4 + 4 <= 960, "barrier area");
     const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + S);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if ((smem_u32(base) & 1023u) != 0u) {  // the swizzled tiles need what the declaration asks for
+        if (threadIdx.x == 0) atomicCAS(p.status_word(), 0, UB_ERR_ALIGN);
+        return;
+    }
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
@@ -204,44 +223,87 @@ __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
 
     const SeqBatch &b = p.b;
     const int heads = p.kv_heads * p.head_blocks;  // items per sequence
-    const int64_t total = total_tiles(b, lane) * heads;
-    // No CTA gets fewer than MIN_TILES tiles: below, one more part to join costs more than
-    // the tiles it takes off the others.
-    constexpr int MIN_TILES = 4;
-    int64_t ctas = total / MIN_TILES;
+    int most;
+    const int64_t total = total_tiles(b, lane, &most) * heads;
+    // Few short items: one CTA each. Else equal shares, of at least MIN_TILES tiles.
+    const int64_t n_items = static_cast<int64_t>(b.n_seqs) * heads;
+    const bool whole_items = most <= WHOLE_TILES && n_items <= gridDim.x;
+    int64_t ctas = whole_items ? n_items : total / MIN_TILES;
     ctas = ctas < 1 ? 1 : (ctas > gridDim.x ? gridDim.x : ctas);
     if (blockIdx.x >= ctas) return;
-    const Split split{total / ctas, total % ctas};
-    const int64_t x0 = split.first(blockIdx.x), x1 = split.first(blockIdx.x + 1);
-
-    int seq;
-    int64_t before;
-    find_seq(b, lane, x0, heads, &seq, &before);
+    const int64_t share = quotient(total, ctas);
+    const Split split{share, total - share * ctas};
+    // Where this CTA begins, and how many tiles it takes.
+    int seq, head, t0;
+    int64_t x = 0, left;
+    if (whole_items) {
+        seq = static_cast<int>(blockIdx.x) / heads;
+        head = static_cast<int>(blockIdx.x) - seq * heads;
+        t0 = 0;
+        left = tiles_of(clamped_len(b, seq));
+    } else {
+        int64_t before;
+        x = split.first(blockIdx.x);
+        left = split.first(blockIdx.x + 1) - x;
+        find_seq(b, lane, x, heads, &seq, &before);
+        const int tiles = tiles_of(clamped_len(b, seq));
+        head = static_cast<int>(quotient(x - before, tiles));
+        t0 = static_cast<int>(x - before - static_cast<int64_t>(head) * tiles);
+    }
     const WaitCtx wc{p.abort_word, p.status_word(), p.timeout_ns, p.epoch};
     bool alive = true;
     uint32_t count = 0;  // tiles of this CTA so far: stage count % S, phase count / S
+    const int tid = threadIdx.x, G = gridDim.x;
+    const float sl = p.scale * 1.4426950408889634f;
+    constexpr int SLOT = decode_slot_floats(D);
+    auto slot_of = [&](int cta, int which) { return p.ws + (static_cast<int64_t>(which) * G + cta) * SLOT; };
+    // Four outputs of head h0 + hh of sequence s, from the weighted sum and the sum of weights.
+    auto finish = [&](int s, int h0, int hh, int d, float4 acc, float M, float L) {
+        const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+        uint2 w;
+        w.x = pack_bf16x2(__float_as_uint(acc.x * inv), __float_as_uint(acc.y * inv));
+        w.y = pack_bf16x2(__float_as_uint(acc.z * inv), __float_as_uint(acc.w * inv));
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + s * p.o_row + (h0 + hh) * p.o_head + d) = w;
+        if (p.lse && d == 0) p.lse[static_cast<int64_t>(s) * p.heads + h0 + hh] = M * p.scale + logf(L);
+    };
+    struct Pending {     // an item that other CTAs have parts of
+        int64_t item0;
+        int tiles, seq, h0, g;
+    };
+    Pending pend[2] = {{0, 0, 0, 0, 0}, {0, 0, 0, 0, 0}};  // begun before this CTA; going on after it
 
-    for (int64_t x = x0; x < x1 && seq < b.n_seqs;) {
+    uint32_t upto = 0;   // ... when the current item is done
+    // A tile in shared memory: box after box, in a box 64 columns after 64 columns, there row
+    // after row of 128 bytes.
+    const int box = KT < (1 << b.page_shift) ? KT : (1 << b.page_shift);  // rows per box
+    const int box_shift = __ffs(box) - 1;
+    auto row_at = [&](int r) { return (((r >> box_shift) * (D / 64)) << box_shift) * 128 + (r & (box - 1)) * 128; };
+    const int half_at = box * 128;
+    int k_row[2], v_row[2];  // this lane's rows of the two fragments of 16 keys
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+        k_row[mt] = row_at(mt * 16 + (lane & 15));
+        v_row[mt] = row_at(mt * 16 + (lane & 7) + ((lane >> 4) << 3));
+    }
+    while (left > 0 && seq < b.n_seqs) {
         const int len = clamped_len(b, seq);
         const int tiles = tiles_of(len);
-        const int head = static_cast<int>((x - before) / tiles);
-        const int64_t item0 = before + static_cast<int64_t>(head) * tiles;
-        const int t0 = static_cast<int>(x - item0);
-        const int t1 = item0 + tiles < x1 ? tiles : static_cast<int>(x1 - item0);
+        const int64_t item0 = x - t0;
+        const int t1 = tiles - t0 < left ? tiles : t0 + static_cast<int>(left);
+        upto += t1 - t0;
         const int kvh = head / p.head_blocks, hb = head - kvh * p.head_blocks;
         const int h0 = kvh * p.group + hb * DECODE_HEADS;     // first query head
         const int g = p.group - hb * DECODE_HEADS < DECODE_HEADS ? p.group - hb * DECODE_HEADS : DECODE_HEADS;
 
-        if (warp == WARPS) {
+        if (warp >= WARPS) {
             // ---------------------------------------------------------------- loads
-            const int box = KT < (1 << b.page_shift) ? KT : (1 << b.page_shift);  // rows per box
             const int boxes = KT / box;
-            constexpr int HALVES = D / 64;
             const int32_t *table = b.page_table + seq * b.table_row;
             const int pages = (len + (1 << b.page_shift) - 1) >> b.page_shift;
             int cached0 = 0, cached_n = 0;   // page ids [cached0, cached0 + cached_n), one per lane
             int ids = -1;
             for (int t = t0; t < t1 && alive; ++t, ++count) {
+                if ((count & (WARPS - 1)) != static_cast<uint32_t>(warp - WARPS)) continue;
                 const int stage = count % S;
                 if (count >= S) alive = mbar_wait(empty0 + 8 * stage, ((count / S) - 1) & 1, wc);
                 alive = __all_sync(0xffffffffu, alive);
@@ -260,22 +322,26 @@ __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
                     }
                 }
                 const uint32_t bar = full0 + 8 * stage;
-                if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(n_box) * HALVES * 2 * box * 128);
+                int page[KT / 8];
+#pragma unroll
+                for (int bx = 0; bx < KT / 8; ++bx) page[bx] = __shfl_sync(0xffffffffu, ids, (page0 - cached0 + bx) & 31);
+                const int row = boxes > 1 ? 0 : key0 & ((1 << b.page_shift) - 1);
+                if (lane == 0) {
+                    const uint32_t dst = smem_u32(base) + stage * Sh::STAGE_BYTES;
+                    const int bytes = box * D * 2;
+                    mbar_arrive_expect_tx(bar, static_cast<uint32_t>(2 * n_box * bytes));
+#pragma unroll
+                    for (int bx = 0; bx < KT / 8; ++bx) {
+                        if (bx >= n_box) break;
+                        tma_load_5d(dst + bx * bytes, &p.tmK, bar, row, kvh, page[bx]);
+                        tma_load_5d(dst + Sh::TILE_BYTES + bx * bytes, &p.tmV, bar, row, kvh, page[bx]);
+                    }
+                }
                 __syncwarp();
-                // lane = (K or V, box, half)
-                const int kind = lane / (boxes * HALVES), rest = lane - kind * boxes * HALVES;
-                const int bx = rest / HALVES, half = rest - bx * HALVES;
-                const int page = __shfl_sync(0xffffffffu, ids, (page0 - cached0 + bx) & 31);
-                if (kind < 2 && bx < n_box)
-                    tma_load_4d(smem_u32(base) + stage * Sh::STAGE_BYTES + kind * Sh::TILE_BYTES + half * KT * 128 +
-                                    bx * box * 128,
-                                kind == 0 ? &p.tmK : &p.tmV, bar, half * 64,
-                                boxes > 1 ? 0 : key0 & ((1 << b.page_shift) - 1), kvh, page);
             }
         } else {
             // ---------------------------------------------------------------- compute
             uint32_t qf[NT][D / 16][2];
-            const float sl = p.scale * 1.4426950408889634f;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const int hh = nt * 8 + lane / 4;
@@ -312,7 +378,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
                     // their weight is zero, so their values must be finite.
                     for (int i = lane; i < KT * D / 8; i += 32) {
                         const int half = i / (KT * 8), r = (i / 8) % KT;
-                        if (r >= valid) st_shared_v4(vb + half * KT * 128 + r * 128 + (i % 8) * 16, 0u, 0u, 0u, 0u);
+                        if (r >= valid) st_shared_v4(vb + half * half_at + row_at(r) + (i % 8) * 16, 0u, 0u, 0u, 0u);
                     }
                     __syncwarp();
                 }
@@ -323,17 +389,36 @@ __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) s[mt][nt][i] = 0.f;
+                // The keys' fragments are loaded ahead of the products that use them, and the first
+                // half of the values' ahead of the softmax.
+                {
+                    uint32_t a[2][D / 16][4];
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
+                    for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
-                    for (int mt = 0; mt < 2; ++mt) {
-                        const int r = mt * 16 + (lane & 15);
-                        const int c = (ks * 2 + (lane >> 4)) & 7;
-                        uint32_t a[4];
-                        ldsm_x4(kb + (ks / 4) * KT * 128 + r * 128 + ((c ^ (r & 7)) << 4), a);
+                        for (int mt = 0; mt < 2; ++mt) {
+                            const int c = (ks * 2 + (lane >> 4)) & 7;
+                            ldsm_x4(kb + (ks / 4) * half_at + k_row[mt] + ((c ^ (lane & 7)) << 4), a[mt][ks]);
+                        }
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma_16x8x16(s[mt][nt], a, qf[nt][ks][0], qf[nt][ks][1]);
-                    }
+                    for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+                        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma_16x8x16(s[mt][nt], a[mt][ks], qf[nt][ks][0], qf[nt][ks][1]);
+                }
+                uint32_t va[D / 32][2][4];
+                auto load_v = [&](int d0) {
+#pragma unroll
+                    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+                        for (int mt = 0; mt < 2; ++mt) {
+                            const int c = ((d0 + d) * 2 + ((lane >> 3) & 1)) & 7;
+                            ldsm_x4_trans(vb + ((d0 + d) / 4) * half_at + v_row[mt] + ((c ^ (lane & 7)) << 4), va[d][mt]);
+                        }
+                };
+                load_v(0);
                 uint32_t pf[2][NT][2];
                 bool moved = false;
                 float f[NT][2];
@@ -353,7 +438,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
 #pragma unroll
                         for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
                         const float ref = mx == -INFINITY ? 0.f : mx;  // no key yet: every weight is zero
-                        f[nt][c] = exp2f((m[nt][c] - ref) * sl);
+                        f[nt][c] = ex2((m[nt][c] - ref) * sl);
                         moved |= m[nt][c] != mx;
                         m[nt][c] = mx;
                         float sum = 0.f;
@@ -362,7 +447,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
 #pragma unroll
                             for (int r = 0; r < 2; ++r) {
                                 float &v = s[mt][nt][r * 2 + c];
-                                v = exp2f(fmaf(v, sl, -ref * sl));
+                                v = ex2(fmaf(v, sl, -ref * sl));
                                 sum += v;
                             }
                         l[nt][c] = l[nt][c] * f[nt][c] + sum;
@@ -386,21 +471,21 @@ __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
                             for (int i = 0; i < 4; ++i) o[d][nt][i] *= f[nt][i & 1];
                 }
 #pragma unroll
-                for (int d = 0; d < D / 16; ++d)
+                for (int d0 = 0; d0 < D / 16; d0 += D / 32) {
+                    if (d0 > 0) load_v(d0);
 #pragma unroll
-                    for (int mt = 0; mt < 2; ++mt) {
-                        const int r = mt * 16 + (lane & 7) + ((lane >> 4) << 3);
-                        const int c = (d * 2 + ((lane >> 3) & 1)) & 7;
-                        uint32_t a[4];
-                        ldsm_x4_trans(vb + (d / 4) * KT * 128 + r * 128 + ((c ^ (r & 7)) << 4), a);
+                    for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma_16x8x16(o[d][nt], a, pf[mt][nt][0], pf[mt][nt][1]);
-                    }
+                        for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma_16x8x16(o[d0 + d][nt], va[d][mt], pf[mt][nt][0], pf[mt][nt][1]);
+                }
                 if (valid < KT) fence_proxy_async_shared();  // the zeroed rows before the next load's writes
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty0 + 8 * stage);
             }
-            count = static_cast<uint32_t>(x - x0) + (t1 - t0);
+            count = upto;
 
             // The four warps' partials, joined in shared memory.
 #pragma unroll
@@ -426,19 +511,6 @@ __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
                     }
             bar_compute();
             const bool whole = t0 == 0 && t1 == tiles;
-            const int tid = threadIdx.x;
-            constexpr int SLOT = decode_slot_floats(D);
-            const int G = gridDim.x;
-            auto slot_of = [&](int cta, int which) { return p.ws + (static_cast<int64_t>(which) * G + cta) * SLOT; };
-            auto finish = [&](int hh, int d, float4 acc, float M, float L) {
-                const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
-                uint2 w;
-                w.x = pack_bf16x2(__float_as_uint(acc.x * inv), __float_as_uint(acc.y * inv));
-                w.y = pack_bf16x2(__float_as_uint(acc.z * inv), __float_as_uint(acc.w * inv));
-                *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + seq * p.o_row +
-                                           (h0 + hh) * p.o_head + d) = w;
-                if (p.lse && d == 0) p.lse[static_cast<int64_t>(seq) * p.heads + h0 + hh] = M * p.scale + logf(L);
-            };
             float *mine = slot_of(blockIdx.x, t0 == 0 ? 1 : 0);
             for (int u = tid; u < g * (D / 4); u += 32 * WARPS) {
                 const int hh = u / (D / 4), d = (u - hh * (D / 4)) * 4;
@@ -450,7 +522,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int w = 0; w < WARPS; ++w) {
-                    const float fw = exp2f((sm_m[w * DECODE_HEADS + hh] - ref) * sl);
+                    const float fw = ex2((sm_m[w * DECODE_HEADS + hh] - ref) * sl);
                     L += sm_l[w * DECODE_HEADS + hh] * fw;
                     const float4 v = *reinterpret_cast<const float4 *>(sm_o + (w * Sh::HEADS + hh) * Sh::O_ROW + d);
                     acc.x += v.x * fw;
@@ -459,7 +531,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
                     acc.w += v.w * fw;
                 }
                 if (whole) {
-                    finish(hh, d, acc, M, L);
+                    finish(seq, h0, hh, d, acc, M, L);
                 } else {
                     *reinterpret_cast<float4 *>(mine + hh * D + d) = acc;
                     if (d == 0) {
@@ -468,80 +540,143 @@ __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
                     }
                 }
             }
-            if (!whole) {
-                // The last of an item's parts to arrive joins them, in groups of JOIN_GROUP.
-                // Counters: group 0 at CTA a, a later group at its first CTA (a CTA is inside at
-                // most one item that began before it), the groups of the item at CTA a; the
-                // joined groups' slots likewise.
-                const int a = split.owner(item0), z = split.owner(item0 + tiles - 1);
-                const int parts = z - a + 1, groups = (parts + JOIN_GROUP - 1) / JOIN_GROUP;
-                const int gi = (static_cast<int>(blockIdx.x) - a) / JOIN_GROUP;
-                auto arrive = [&](uint32_t *counter, int n) {
-                    __threadfence();
-                    bar_compute();
-                    if (tid == 0) {
-                        const bool last = atomicAdd(counter, 1u) == static_cast<uint32_t>(n - 1);
-                        if (last) *counter = 0u;  // zero again for the next call
-                        __threadfence();
-                        *sm_last = last ? 1 : 0;
-                    }
-                    bar_compute();
-                    return *sm_last != 0;
-                };
-                // Part i of n at `part(i)`; joined into `to`, or the output.
-                auto join = [&](int n, auto part, float *to) {
-                    for (int u = tid; u < g * (D / 4); u += 32 * WARPS) {
-                        const int hh = u / (D / 4), d = (u - hh * (D / 4)) * 4;
-                        float M = -INFINITY;
-                        for (int i = 0; i < n; ++i) M = fmaxf(M, ld_cg(part(i) + DECODE_HEADS * D + hh));
-                        const float ref = M == -INFINITY ? 0.f : M;
-                        float L = 0.f;
-                        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                        for (int i = 0; i < n; ++i) {
-                            const float *q = part(i);
-                            const float fw = exp2f((ld_cg(q + DECODE_HEADS * D + hh) - ref) * sl);
-                            L += ld_cg(q + DECODE_HEADS * (D + 1) + hh) * fw;
-                            const float4 v = ld_cg4(q + hh * D + d);
-                            acc.x += v.x * fw;
-                            acc.y += v.y * fw;
-                            acc.z += v.z * fw;
-                            acc.w += v.w * fw;
-                        }
-                        if (!to) {
-                            finish(hh, d, acc, M, L);
-                        } else {
-                            *reinterpret_cast<float4 *>(to + hh * D + d) = acc;
-                            if (d == 0) {
-                                to[DECODE_HEADS * D + hh] = M;
-                                to[DECODE_HEADS * (D + 1) + hh] = L;
-                            }
-                        }
-                    }
-                };
-                const int first = a + gi * JOIN_GROUP;
-                const int n = parts - gi * JOIN_GROUP < JOIN_GROUP ? parts - gi * JOIN_GROUP : JOIN_GROUP;
-                // a part's slot: 1 for the CTA in which the item begins, 0 for the others
-                auto part1 = [&](int i) { return slot_of(first + i, first + i == a ? 1 : 0); };
-                if (arrive(p.counters + (gi == 0 ? 0 : G) + first, n)) {
-                    if (groups == 1) {
-                        join(n, part1, nullptr);
-                    } else {
-                        join(n, part1, slot_of(first, gi == 0 ? 2 : 3));
-                        if (arrive(p.counters + 2 * G + a, groups)) {
-                            auto part2 = [&](int i) { return slot_of(a + i * JOIN_GROUP, i == 0 ? 2 : 3); };
-                            join(groups, part2, nullptr);
-                        }
-                    }
-                }
-            }
+            if (!whole && t0 != 0) pend[0] = Pending{item0, tiles, seq, h0, g};
+            if (!whole && t0 == 0) pend[1] = Pending{item0, tiles, seq, h0, g};
             bar_compute();  // the shared partials are free again
         }
         if (!__all_sync(0xffffffffu, alive)) alive = false;
         x += t1 - t0;
-        if (item0 + tiles == x && head == heads - 1) {
-            before += static_cast<int64_t>(tiles) * heads;
+        left -= t1 - t0;
+        t0 = 0;
+        if (++head == heads) {
+            head = 0;
             ++seq;
+        }
+    }
+    // The parts of split items, joined when the CTA's own tiles are done. Up to JOIN_MOST parts:
+    // the last CTA to arrive joins them. More (all their CTAs are resident: one per SM, no more
+    // than SMs): each waits for the others and joins its share of the outputs.
+    if (warp < WARPS) {
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            const Pending it = pend[which];
+            if (it.tiles == 0) continue;
+            const int a = split.owner(it.item0), z = split.owner(it.item0 + it.tiles - 1);
+            const int parts = z - a + 1;
+            uint32_t *arrived = p.counters + a, *done = p.counters + G + a;  // of the item that begins in CTA a
+            // part i's slot: 1 for the CTA in which the item begins, 0 for the others
+            auto part = [&](int i) { return slot_of(a + i, i == 0 ? 1 : 0); };
+            const int units = it.g * (D / 4);  // of four outputs
+            bar_compute();                     // this CTA's part is written
+            if (tid == 0) *sm_last = static_cast<int>(arrive_acq_rel(arrived)) == parts - 1 ? 1 : 0;
+            bar_compute();
+            const bool last = *sm_last != 0;
+            if (parts <= JOIN_MOST) {
+                if (!last) continue;
+                if (tid == 0) *arrived = 0u;   // zero again for the next call
+                for (int u = tid; u < units; u += 32 * WARPS) {
+                    const int hh = u / (D / 4), d = (u - hh * (D / 4)) * 4;
+                    float4 v[JOIN_MOST];
+                    float m[JOIN_MOST], l[JOIN_MOST];
+                    float M = -INFINITY, L = 0.f;
+#pragma unroll
+                    for (int i = 0; i < JOIN_MOST; ++i) {
+                        if (i >= parts) continue;
+                        v[i] = __ldcg(reinterpret_cast<const float4 *>(part(i) + hh * D + d));
+                        m[i] = __ldcg(part(i) + DECODE_HEADS * D + hh);
+                        l[i] = __ldcg(part(i) + DECODE_HEADS * (D + 1) + hh);
+                    }
+#pragma unroll
+                    for (int i = 0; i < JOIN_MOST; ++i)
+                        if (i < parts) M = fmaxf(M, m[i]);
+                    const float ref = M == -INFINITY ? 0.f : M;
+                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int i = 0; i < JOIN_MOST; ++i) {
+                        if (i >= parts) continue;
+                        const float fw = ex2((m[i] - ref) * sl);
+                        L += l[i] * fw;
+                        acc.x += v[i].x * fw;
+                        acc.y += v[i].y * fw;
+                        acc.z += v[i].z * fw;
+                        acc.w += v[i].w * fw;
+                    }
+                    finish(it.seq, it.h0, hh, d, acc, M, L);
+                }
+                continue;
+            }
+            if (!last) {
+                WaitClock clk;
+                for (uint32_t n = 1; alive; ++n) {
+                    uint32_t v;
+                    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(arrived) : "memory");
+                    if (v >= static_cast<uint32_t>(parts)) break;
+                    if ((n & 15u) == 0 && !clk.ok(wc)) alive = false;
+                }
+                alive = __all_sync(0xffffffffu, alive);
+            }
+            // Units of this CTA: one warp each, a lane adding every 32nd part.
+            const int per = (units + parts - 1) / parts, i_cta = static_cast<int>(blockIdx.x) - a;
+            for (int u = i_cta * per + warp; u < units && u < (i_cta + 1) * per && alive; u += WARPS) {
+                const int hh = u / (D / 4), d = (u - hh * (D / 4)) * 4;
+                float M = -INFINITY, L = 0.f;
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                constexpr int U = 5;           // parts in flight per lane
+                for (int i0 = lane; i0 < parts; i0 += 32 * U) {
+                    float4 v[U];
+                    float m[U], l[U], top = M;
+#pragma unroll
+                    for (int k = 0; k < U; ++k) {
+                        const int i = i0 + 32 * k;
+                        m[k] = -INFINITY;
+                        l[k] = 0.f;
+                        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (i >= parts) continue;
+                        v[k] = __ldcg(reinterpret_cast<const float4 *>(part(i) + hh * D + d));
+                        m[k] = __ldcg(part(i) + DECODE_HEADS * D + hh);
+                        l[k] = __ldcg(part(i) + DECODE_HEADS * (D + 1) + hh);
+                    }
+#pragma unroll
+                    for (int k = 0; k < U; ++k) top = fmaxf(top, m[k]);
+                    const float ref = top == -INFINITY ? 0.f : top;
+                    const float f0 = ex2((M - ref) * sl);
+                    L *= f0;
+                    acc.x *= f0;
+                    acc.y *= f0;
+                    acc.z *= f0;
+                    acc.w *= f0;
+                    M = top;
+#pragma unroll
+                    for (int k = 0; k < U; ++k) {
+                        const float fw = ex2((m[k] - ref) * sl);
+                        L += l[k] * fw;
+                        acc.x += v[k].x * fw;
+                        acc.y += v[k].y * fw;
+                        acc.z += v[k].z * fw;
+                        acc.w += v[k].w * fw;
+                    }
+                }
+                float top = M;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const float fw = ex2((M - (top == -INFINITY ? 0.f : top)) * sl);
+                L *= fw;
+                acc.x *= fw;
+                acc.y *= fw;
+                acc.z *= fw;
+                acc.w *= fw;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    L += __shfl_xor_sync(0xffffffffu, L, o);
+                    acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o);
+                    acc.y += __shfl_xor_sync(0xffffffffu, acc.y, o);
+                    acc.z += __shfl_xor_sync(0xffffffffu, acc.z, o);
+                    acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
+                }
+                if (lane == 0) finish(it.seq, it.h0, hh, d, acc, top, L);
+            }
+            bar_compute();                     // every warp has seen the count
+            if (tid == 0 && arrive_acq_rel(done) == static_cast<uint32_t>(parts - 1)) *arrived = *done = 0u;
         }
     }
     // A wait ran out: the copies already issued land before the CTA gives its memory back.

@@ -13,7 +13,6 @@ hidden], tp_size, dtype=torch.bfloat16)`` registers a buffer at capacity, and
 from __future__ import annotations
 
 import ctypes
-import math
 import os
 import struct
 
@@ -222,49 +221,96 @@ def _bf16_cuda(t: torch.Tensor, name: str, shape=None, device=None):
 # decoding step's call takes microseconds): 8 ints, scale, reserved, 4 sizes, four
 # [data, row, head], two [data, page, head, row], six pointers.
 _ATTN = struct.Struct("=I7ifI4q" + "Q2q" * 4 + "Q3q" * 2 + "6Q")
-_NO_HEADS = (0, 0, 0)
-_NO_PAGES = (0, 0, 0, 0)
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+# What a wrong argument raises while its view is read; the checks below are on the path of
+# every decoding step, so each argument is read once and its faults are named afterwards.
+_UNREADABLE = (AttributeError, TypeError, ValueError)
 
 
-def _attn_error(t, name: str, dtype, device, what: str):
+def _attn_error(t, name: str, dtype, device: int, what: str):
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if t.dtype != dtype or not t.is_cuda:
         raise TypeError("%s must be a CUDA %s tensor, got %s on %s" % (name, dtype, t.dtype, t.device))
-    if t.device != device:
-        raise ValueError("%s is on %s, the user buffer on %s" % (name, t.device, device))
+    if t.get_device() != device:
+        raise ValueError("%s is on %s, the user buffer on cuda:%d" % (name, t.device, device))
     raise ValueError("%s must be %s, got %s with strides %s" % (name, what, tuple(t.shape), t.stride()))
 
 
-def _heads_view(t: torch.Tensor, name: str, T: int, D: int | None, device):
-    """([data, row, head], heads, head_dim) of a [T, heads, D] bf16 view with a contiguous head dimension."""
-    if (not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.device != device or t.dim() != 3
-            or t.shape[0] != T or (D is not None and t.shape[2] != D) or t.stride(2) != 1):
-        _attn_error(t, name, torch.bfloat16, device, "[%d, heads, %s] with a contiguous last dimension" % (T, D or "head_dim"))
-    row, head, _ = t.stride()
-    return (t.data_ptr(), row, head), t.shape[1], t.shape[2]
+def _heads_view(t: torch.Tensor, name: str, T: int, D: int, device: int):
+    """(data, row, head, heads) of a [T, heads, D] bf16 view with a contiguous head dimension."""
+    try:
+        n, heads, d = t.shape
+        row, head, one = t.stride()
+        if n == T and d == D and one == 1 and t.dtype is _BF16 and t.get_device() == device:
+            return t.data_ptr(), row, head, heads
+    except _UNREADABLE:
+        pass
+    _attn_error(t, name, _BF16, device, "[%d, heads, %d] with a contiguous last dimension" % (T, D))
 
 
-def _pages_view(t: torch.Tensor, name: str, D: int, device, like=None):
-    if (not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.device != device or t.dim() != 4
-            or t.shape[3] != D or t.stride(3) != 1 or (like is not None and t.shape != like)):
-        _attn_error(t, name, torch.bfloat16, device, "[pages, kv_heads, page_size, %d] with a contiguous last dimension%s"
-                    % (D, "" if like is None else ", as k_cache"))
-    return (t.data_ptr(),) + t.stride()[:3]
+def _head_dim(q) -> int:
+    try:
+        return q.shape[2]
+    except (AttributeError, IndexError, TypeError):
+        return -1  # no [T, heads, D] view: named by the check of q
 
 
-def _ints(t: torch.Tensor, name: str, shape, device) -> int:
-    if (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device or tuple(t.shape) != shape
-            or not t.is_contiguous()):
-        _attn_error(t, name, torch.int32, device, "%s and contiguous" % (shape,))
-    return t.data_ptr()
+def _pages_view(t: torch.Tensor, name: str, D: int, device: int):
+    """(data, page, head, row, pages, kv_heads, page_size) of a cache."""
+    try:
+        pages, heads, size, d = t.shape
+        page, head, row, one = t.stride()
+        if d == D and one == 1 and t.dtype is _BF16 and t.get_device() == device:
+            return t.data_ptr(), page, head, row, pages, heads, size
+    except _UNREADABLE:
+        pass
+    _attn_error(t, name, _BF16, device, "[pages, kv_heads, page_size, %d] with a contiguous last dimension" % D)
 
 
-def _table(t: torch.Tensor, n: int, device):
-    if (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device or t.dim() != 2
-            or t.shape[0] != n or t.stride(1) != 1):
-        _attn_error(t, "page_table", torch.int32, device, "[%d, entries] with a contiguous last dimension" % n)
-    return t.data_ptr(), t.shape[1], t.stride(0)
+def _caches(k_cache, v_cache, D: int, device: int):
+    """(k data and strides, v data and strides, pages, kv_heads, page_size)."""
+    kp, k0, k1, k2, pages, heads, size = _pages_view(k_cache, "k_cache", D, device)
+    vp, v0, v1, v2, pages_v, heads_v, size_v = _pages_view(v_cache, "v_cache", D, device)
+    if pages_v != pages or heads_v != heads or size_v != size:
+        raise ValueError("v_cache has shape %s, k_cache %s" % (tuple(v_cache.shape), tuple(k_cache.shape)))
+    return (kp, k0, k1, k2, vp, v0, v1, v2), pages, heads, size
+
+
+def _ints(t: torch.Tensor, name: str, n: int | None, device: int):
+    """(data, length) of a contiguous int32 vector (of n entries, if given)."""
+    try:
+        (length,) = t.shape
+        if ((n is None or length == n) and (length < 2 or t.stride(0) == 1) and t.dtype is _I32
+                and t.get_device() == device):
+            return t.data_ptr(), length
+    except _UNREADABLE:
+        pass
+    _attn_error(t, name, _I32, device, "[%s] and contiguous" % ("n" if n is None else n))
+
+
+def _table(t: torch.Tensor, n: int, device: int):
+    """(data, entries, row) of a page table."""
+    try:
+        rows, width = t.shape
+        row, one = t.stride()
+        if rows == n and (one == 1 or width < 2) and t.dtype is _I32 and t.get_device() == device:
+            return t.data_ptr(), width, row
+    except _UNREADABLE:
+        pass
+    _attn_error(t, "page_table", _I32, device, "[%d, entries] with a contiguous last dimension" % n)
+
+
+def _rotations(t: torch.Tensor, name: str, shape, device: int):
+    """(data, positions, rotated elements) of a table of cosines or sines."""
+    try:
+        positions, half = t.shape
+        if (t.is_contiguous() and t.dtype is _F32 and t.get_device() == device
+                and (shape is None or shape == (positions, half))):
+            return t.data_ptr(), positions, 2 * half
+    except _UNREADABLE:
+        pass
+    _attn_error(t, name, _F32, device, "[positions, rot / 2] and contiguous, cos like sin")
 
 
 class _DeviceArray:
@@ -566,29 +612,36 @@ class UserBuffer:
 
 
     # -- attention between the QKV and the attention-out projections
-    def _stream(self, stream):
-        return torch.cuda.current_stream(self.device) if stream is None else stream
-
     def _new(self, shape, dtype, stream):
         """A new tensor of the stream that the call runs on, so that its memory is not reused too early."""
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
         with torch.cuda.stream(stream):
             return torch.empty(shape, dtype=dtype, device=self.device)
 
-    def _attn_outputs(self, q, out, lse, T, H, D, stream):
-        """(out, its view, lse, its pointer); lse=True allocates it."""
+    def _raw_stream(self, stream) -> int:
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(self.device.index)
+        return stream.cuda_stream
+
+    def _out(self, out, name, T, H, D, stream):
         if out is None:
-            out = self._new((T, H, D), torch.bfloat16, stream)
-        o, oh, _ = _heads_view(out, "out", T, D, self.device)
-        if oh != H:
-            raise ValueError("out has %d heads, q has %d" % (oh, H))
-        if lse is True:
-            lse = self._new((T, H), torch.float32, stream)
+            out = self._new((T, H, D), _BF16, stream)
+        data, row, head, heads = _heads_view(out, name, T, D, self.device.index)
+        if heads != H:
+            raise ValueError("%s has %d heads, q has %d" % (name, heads, H))
+        return out, data, row, head
+
+    def _lse(self, lse, T, H, stream):
+        """(lse, its pointer); True allocates it."""
         if lse is None or lse is False:
-            return out, o, None, 0
-        if (not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32 or lse.device != self.device
+            return None, 0
+        if lse is True:
+            lse = self._new((T, H), _F32, stream)
+        if (not isinstance(lse, torch.Tensor) or lse.dtype != _F32 or lse.device != self.device
                 or tuple(lse.shape) != (T, H) or not lse.is_contiguous()):
-            _attn_error(lse, "lse", torch.float32, self.device, "(%d, %d) and contiguous" % (T, H))
-        return out, o, lse, lse.data_ptr()
+            _attn_error(lse, "lse", _F32, self.device.index, "(%d, %d) and contiguous" % (T, H))
+        return lse, lse.data_ptr()
 
     def kv_append(self, q, k, v, cos, sin, seq_starts, kv_lens, page_table, k_cache, v_cache, q_out=None,
                   interleaved: bool = False, stream=None):
@@ -600,36 +653,26 @@ class UserBuffer:
         multiple of 16 up to D (None: no rotation). seq_starts int32 [n + 1], kv_lens int32 [n]
         (the tokens of this call included), page_table int32 [n, entries], on the device.
         k_cache, v_cache [pages, kv_heads, page_size, D]. q_out: like q, q itself allowed."""
-        dev = self.device
+        dev = self.device.index
         T = self.active_shape[0]
-        qv, H, D = _heads_view(q, "q", T, None, dev)
-        kv, G, _ = _heads_view(k, "k", T, D, dev)
-        vv, Gv, _ = _heads_view(v, "v", T, D, dev)
-        kc = _pages_view(k_cache, "k_cache", D, dev)
-        vc = _pages_view(v_cache, "v_cache", D, dev, k_cache.shape)
-        pages, Gc, page, _ = k_cache.shape
+        D = _head_dim(q)
+        qp, q0, q1, H = _heads_view(q, "q", T, D, dev)
+        kp, k0, k1, G = _heads_view(k, "k", T, D, dev)
+        vp, v0, v1, Gv = _heads_view(v, "v", T, D, dev)
+        caches, pages, Gc, page = _caches(k_cache, v_cache, D, dev)
         if Gv != G or Gc != G:
             raise ValueError("k has %d heads, v %d, the caches %d" % (G, Gv, Gc))
-        n = kv_lens.shape[0] if kv_lens.dim() else 0
+        lens, n = _ints(kv_lens, "kv_lens", None, dev)
+        starts, _ = _ints(seq_starts, "seq_starts", n + 1, dev)
         table, width, table_row = _table(page_table, n, dev)
-        rot, positions, cp, sp = 0, 0, 0, 0
+        rot = positions = cp = sp = 0
         if cos is not None or sin is not None:
-            for name, t in (("cos", cos), ("sin", sin)):
-                if (not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.device != dev or t.dim() != 2
-                        or not t.is_contiguous() or t.shape != cos.shape):
-                    _attn_error(t, name, torch.float32, dev, "[positions, rot / 2] and contiguous, cos like sin")
-            positions, rot = cos.shape[0], 2 * cos.shape[1]
-            cp, sp = cos.data_ptr(), sin.data_ptr()
-        s = self._stream(stream)
-        if q_out is None:
-            q_out = self._new((T, H, D), torch.bfloat16, s)
-        ov, Ho, _ = _heads_view(q_out, "q_out", T, D, dev)
-        if Ho != H:
-            raise ValueError("q_out has %d heads, q has %d" % (Ho, H))
+            cp, positions, rot = _rotations(cos, "cos", None, dev)
+            sp, _, _ = _rotations(sin, "sin", (positions, rot // 2), dev)
+        q_out, op, o0, o1 = self._out(q_out, "q_out", T, H, D, stream)
         a = _ATTN.pack(_ATTN.size, n, H, G, D, page, rot, 1 if interleaved else 0, 1.0, 0, pages, width, table_row,
-                       positions, *qv, *kv, *vv, *ov, *kc, *vc, _ints(seq_starts, "seq_starts", (n + 1,), dev),
-                       _ints(kv_lens, "kv_lens", (n,), dev), table, cp, sp, 0)
-        _check(load().ub_kv_append(self._h, a, s.cuda_stream))
+                       positions, qp, q0, q1, kp, k0, k1, vp, v0, v1, op, o0, o1, *caches, starts, lens, table, cp, sp, 0)
+        _check(load().ub_kv_append(self._h, a, self._raw_stream(stream)))
         return q_out
 
     def attn_prompt(self, q, k, v, seq_starts, out=None, lse=None, scale: float | None = None, stream=None):
@@ -637,42 +680,41 @@ class UserBuffer:
         [seq_starts[s], seq_starts[s + 1]) of q [T, heads, D] and of k, v [T, kv_heads, D].
         scale: 1 / sqrt(D) if None. lse: an fp32 [T, heads] tensor, or True for a new one.
         Returns out, or (out, lse) where lse is asked for. Rows of no sequence stay as they are."""
-        dev = self.device
+        dev = self.device.index
         T = self.active_shape[0]
-        qv, H, D = _heads_view(q, "q", T, None, dev)
-        kv, G, _ = _heads_view(k, "k", T, D, dev)
-        vv, Gv, _ = _heads_view(v, "v", T, D, dev)
+        D = _head_dim(q)
+        qp, q0, q1, H = _heads_view(q, "q", T, D, dev)
+        kp, k0, k1, G = _heads_view(k, "k", T, D, dev)
+        vp, v0, v1, Gv = _heads_view(v, "v", T, D, dev)
         if Gv != G:
             raise ValueError("k has %d heads, v %d" % (G, Gv))
-        n = seq_starts.shape[0] - 1 if seq_starts.dim() else 0
-        s = self._stream(stream)
-        out, ov, lse, lp = self._attn_outputs(q, out, lse, T, H, D, s)
-        a = _ATTN.pack(_ATTN.size, n, H, G, D, 0, 0, 0, 1.0 / math.sqrt(D) if scale is None else scale, 0, 0, 0, 0, 0,
-                       *qv, *kv, *vv, *ov, *_NO_PAGES, *_NO_PAGES, _ints(seq_starts, "seq_starts", (n + 1,), dev),
-                       0, 0, 0, 0, lp)
-        _check(load().ub_attn_prompt(self._h, a, s.cuda_stream))
+        starts, n = _ints(seq_starts, "seq_starts", None, dev)
+        out, op, o0, o1 = self._out(out, "out", T, H, D, stream)
+        lse, lp = self._lse(lse, T, H, stream)
+        a = _ATTN.pack(_ATTN.size, n - 1, H, G, D, 0, 0, 0, D ** -0.5 if scale is None else scale, 0, 0, 0, 0, 0,
+                       qp, q0, q1, kp, k0, k1, vp, v0, v1, op, o0, o1, 0, 0, 0, 0, 0, 0, 0, 0, starts, 0, 0, 0, 0, lp)
+        _check(load().ub_attn_prompt(self._h, a, self._raw_stream(stream)))
         return out if lse is None else (out, lse)
 
     def attn_prompt_paged(self, q, k_cache, v_cache, seq_starts, kv_lens, page_table, out=None, lse=None,
                           scale: float | None = None, stream=None):
         """Causal attention of prompts, or of chunks of prompts, over the paged cache that holds
         their keys and values (after kv_append); arguments as there and in attn_prompt."""
-        dev = self.device
+        dev = self.device.index
         T = self.active_shape[0]
-        qv, H, D = _heads_view(q, "q", T, None, dev)
-        kc = _pages_view(k_cache, "k_cache", D, dev)
-        vc = _pages_view(v_cache, "v_cache", D, dev, k_cache.shape)
-        pages, G, page, _ = k_cache.shape
-        n = kv_lens.shape[0] if kv_lens.dim() else 0
-        table, width, table_row = _table(page_table, n, dev)
-        s = self._stream(stream)
-        out, ov, lse, lp = self._attn_outputs(q, out, lse, T, H, D, s)
+        D = _head_dim(q)
+        qp, q0, q1, H = _heads_view(q, "q", T, D, dev)
+        caches, pages, G, page = _caches(k_cache, v_cache, D, dev)
         if page == 0:
             raise ValueError("pages of no rows")
-        a = _ATTN.pack(_ATTN.size, n, H, G, D, page, 0, 0, 1.0 / math.sqrt(D) if scale is None else scale, 0, pages,
-                       width, table_row, 0, *qv, *_NO_HEADS, *_NO_HEADS, *ov, *kc, *vc,
-                       _ints(seq_starts, "seq_starts", (n + 1,), dev), _ints(kv_lens, "kv_lens", (n,), dev), table, 0, 0, lp)
-        _check(load().ub_attn_prompt(self._h, a, s.cuda_stream))
+        lens, n = _ints(kv_lens, "kv_lens", None, dev)
+        starts, _ = _ints(seq_starts, "seq_starts", n + 1, dev)
+        table, width, table_row = _table(page_table, n, dev)
+        out, op, o0, o1 = self._out(out, "out", T, H, D, stream)
+        lse, lp = self._lse(lse, T, H, stream)
+        a = _ATTN.pack(_ATTN.size, n, H, G, D, page, 0, 0, D ** -0.5 if scale is None else scale, 0, pages, width,
+                       table_row, 0, qp, q0, q1, 0, 0, 0, 0, 0, 0, op, o0, o1, *caches, starts, lens, table, 0, 0, lp)
+        _check(load().ub_attn_prompt(self._h, a, self._raw_stream(stream)))
         return out if lse is None else (out, lse)
 
     def attn_decode(self, q, k_cache, v_cache, kv_lens, page_table, out=None, lse=None, scale: float | None = None,
@@ -680,20 +722,18 @@ class UserBuffer:
         """Attention of one new token per sequence over the paged cache (ub_attn_decode): row s of
         q [T, heads, D] is sequence s, n = kv_lens.shape[0] <= T; arguments as in kv_append and
         attn_prompt. Rows from n on stay as they are."""
-        dev = self.device
+        dev = self.device.index
         T = self.active_shape[0]
-        qv, H, D = _heads_view(q, "q", T, None, dev)
-        kc = _pages_view(k_cache, "k_cache", D, dev)
-        vc = _pages_view(v_cache, "v_cache", D, dev, k_cache.shape)
-        pages, G, page, _ = k_cache.shape
-        n = kv_lens.shape[0] if kv_lens.dim() else 0
+        D = _head_dim(q)
+        qp, q0, q1, H = _heads_view(q, "q", T, D, dev)
+        caches, pages, G, page = _caches(k_cache, v_cache, D, dev)
+        lens, n = _ints(kv_lens, "kv_lens", None, dev)
         table, width, table_row = _table(page_table, n, dev)
-        s = self._stream(stream)
-        out, ov, lse, lp = self._attn_outputs(q, out, lse, T, H, D, s)
-        a = _ATTN.pack(_ATTN.size, n, H, G, D, page, 0, 0, 1.0 / math.sqrt(D) if scale is None else scale, 0, pages,
-                       width, table_row, 0, *qv, *_NO_HEADS, *_NO_HEADS, *ov, *kc, *vc, 0,
-                       _ints(kv_lens, "kv_lens", (n,), dev), table, 0, 0, lp)
-        _check(load().ub_attn_decode(self._h, a, s.cuda_stream))
+        out, op, o0, o1 = self._out(out, "out", T, H, D, stream)
+        lse, lp = self._lse(lse, T, H, stream)
+        a = _ATTN.pack(_ATTN.size, n, H, G, D, page, 0, 0, D ** -0.5 if scale is None else scale, 0, pages, width,
+                       table_row, 0, qp, q0, q1, 0, 0, 0, 0, 0, 0, op, o0, o1, *caches, 0, lens, table, 0, 0, lp)
+        _check(load().ub_attn_decode(self._h, a, self._raw_stream(stream)))
         return out if lse is None else (out, lse)
 
 
