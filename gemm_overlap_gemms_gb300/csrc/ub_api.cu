@@ -171,7 +171,7 @@ namespace {
 // Control block, in 32-bit words: the readiness flags [0, UB_MAX_TP), the partial-tile
 // flags [UB_MAX_TP, UB_MAX_TP + W) with W = ws_slots * EPI_WARPS, then the abort word, the
 // status word, the gather's per-chunk counters, the decode attention's join counters and
-// the prompt attention's tickets (all zero between calls). The words a captured call clears (flags and partial-tile
+// the prompt attention's tickets. The words a captured call clears (flags and partial-tile
 // flags) are one contiguous run.
 size_t ws_flag_words(const ub_handle *h) { return static_cast<size_t>(h->ws_slots) * ubk::EPI_WARPS; }
 uint32_t *flags_of(ub_handle *h) { return h->ctrl; }

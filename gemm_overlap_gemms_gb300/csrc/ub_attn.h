@@ -26,7 +26,7 @@ struct HandleCall {
     uint32_t epoch;
     float *ws;
     size_t ws_floats;
-    uint32_t *join_counters; // zero between calls
+    uint32_t *join_counters; // of the decode attention
     int join_words;
     uint32_t *tickets;       // two words, zero between calls
 };
@@ -84,9 +84,10 @@ struct DecodeParams {
     int64_t q_row, q_head, o_row, o_head;
     int heads, kv_heads, head_dim, group;
     int head_blocks;         // blocks of up to 16 query heads per key/value head
+    int many_tiles;          // the table could hold 2^31 tiles or more over all heads
     float scale;
     float *ws;
-    uint32_t *counters;      // DECODE_COUNTERS words per CTA, zero between calls
+    uint32_t *counters;      // DECODE_COUNTERS words per CTA
     uint32_t *abort_word;
     uint64_t timeout_ns;
     uint32_t epoch;

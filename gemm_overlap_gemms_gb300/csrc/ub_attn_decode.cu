@@ -56,7 +56,7 @@ struct DecShape {
     // A multiple of WARPS, so that a stage always belongs to the same warp: the loads of two
     // tiles may land in either order, and a warp that waited for the second fill of a stage
     // whose first fill (another warp's) has not landed would see the parity it waits for.
-    static constexpr int STAGES = 196608 / STAGE_BYTES;
+    static constexpr int STAGES = 131072 / STAGE_BYTES;
     static constexpr int SMEM = STAGES * STAGE_BYTES + MERGE_BYTES + 960;
     static_assert(SMEM <= 232448, "shared memory");
     static_assert(STAGES >= WARPS && STAGES % WARPS == 0, "one warp per stage");
@@ -147,32 +147,41 @@ struct Split {
     }
 };
 
-// Sum and maximum of the sequences' tiles (one warp).
-__device__ __forceinline__ int64_t total_tiles(const SeqBatch &b, int lane, int *most)
+__device__ __forceinline__ int64_t warp_sum(int64_t v)
 {
-    int64_t sum = 0;
-    int top = 0;
-    for (int i = lane; i < b.n_seqs; i += 32) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+__device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
+
+// Sum and maximum of the sequences' tiles (one warp). I: a type that holds the sum over all heads.
+template <typename I>
+__device__ __forceinline__ I total_tiles(const SeqBatch &b, int lane, int own, int *most)
+{
+    I sum = own;
+    int top = own;
+    for (int i = lane + 32; i < b.n_seqs; i += 32) {
         const int n = tiles_of(clamped_len(b, i));
         sum += n;
         top = n > top ? n : top;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     *most = __reduce_max_sync(0xffffffffu, top);
-    return sum;
+    return warp_sum(sum);
 }
-// The sequence that holds tile `tile` of all heads' tiles, and the tiles before it.
-__device__ __forceinline__ void find_seq(const SeqBatch &b, int lane, int64_t tile, int heads, int *seq, int64_t *before)
+// The sequence that holds per-head tile `tile` over all heads, and the tiles before it. own:
+// the tiles of sequence `lane` (0 past the last).
+template <typename I>
+__device__ __forceinline__ void find_seq(const SeqBatch &b, int lane, int own, I tile, int heads, int *seq, I *before)
 {
-    int64_t seen = 0;  // tiles of the sequences before this batch of 32, over all heads
+    I seen = 0;  // tiles of the sequences before this batch of 32, over all heads
     for (int i0 = 0; i0 < b.n_seqs; i0 += 32) {
-        const int64_t mine =
-            i0 + lane < b.n_seqs ? static_cast<int64_t>(tiles_of(clamped_len(b, i0 + lane))) * heads : 0;
-        int64_t upto = mine;
+        I mine = i0 == 0 ? own : (i0 + lane < b.n_seqs ? tiles_of(clamped_len(b, i0 + lane)) : 0);
+        mine *= heads;
+        I upto = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+            const I x = __shfl_up_sync(0xffffffffu, upto, o);
             if (lane >= o) upto += x;
         }
         const uint32_t past = __ballot_sync(0xffffffffu, seen + upto > tile);
@@ -188,6 +197,44 @@ __device__ __forceinline__ void find_seq(const SeqBatch &b, int lane, int64_t ti
     *before = seen;
 }
 
+// What a CTA does: its first item and tile, and how many tiles it takes (0: nothing).
+struct Share {
+    Split split;
+    int64_t x, left;  // first tile of the whole call (not counted for whole items), tiles
+    int seq, head, t0;
+};
+template <typename I>
+__device__ __forceinline__ Share share_of(const SeqBatch &b, int lane, int heads, int cta, int grid)
+{
+    Share s{{0, 0}, 0, 0, 0, 0, 0};
+    const int own = lane < b.n_seqs ? tiles_of(clamped_len(b, lane)) : 0;
+    int most;
+    const I total = total_tiles<I>(b, lane, own, &most) * heads;
+    // Few short items: one CTA each. Else equal shares, of at least MIN_TILES tiles.
+    const int64_t n_items = static_cast<int64_t>(b.n_seqs) * heads;
+    const bool whole_items = most <= WHOLE_TILES && n_items <= grid;
+    I ctas = whole_items ? static_cast<I>(n_items) : total / MIN_TILES;
+    ctas = ctas < 1 ? 1 : (ctas > grid ? grid : ctas);
+    if (cta >= ctas) return s;
+    const I base = static_cast<I>(quotient(total, ctas));
+    s.split = Split{base, total - base * ctas};
+    if (whole_items) {
+        s.seq = cta / heads;
+        s.head = cta - s.seq * heads;
+        s.left = tiles_of(clamped_len(b, s.seq));
+        return s;
+    }
+    const I x = static_cast<I>(s.split.first(cta));
+    I before;
+    find_seq<I>(b, lane, own, x, heads, &s.seq, &before);
+    const int tiles = tiles_of(clamped_len(b, s.seq));
+    s.x = x;
+    s.left = s.split.first(cta + 1) - x;
+    s.head = static_cast<int>(quotient(x - before, tiles));
+    s.t0 = static_cast<int>(x - before - static_cast<I>(s.head) * tiles);
+    return s;
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
     ub_attn_decode_kernel(const __grid_constant__ DecodeParams p)
@@ -200,7 +247,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
     float *sm_m = reinterpret_cast<float *>(bars + 2 * S);                     // [WARPS][HEADS]
     float *sm_l = sm_m + WARPS * DECODE_HEADS;                                 // [WARPS][HEADS]
     int *sm_last = reinterpret_cast<int *>(sm_l + WARPS * DECODE_HEADS);
-    static_assert(2 * S * 8 + 2 * WARPS * DECODE_HEADS * 4 + 4 <= 960, "barrier area");
+    static_assert(2 * S * 8 + 2 * WARPS * DECODE_HEADS * 4 + 8 <= 960, "barrier area");
     const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + S);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if ((smem_u32(base) & 1023u) != 0u) {  // the swizzled tiles need what the declaration asks for
@@ -223,33 +270,12 @@ __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
 
     const SeqBatch &b = p.b;
     const int heads = p.kv_heads * p.head_blocks;  // items per sequence
-    int most;
-    const int64_t total = total_tiles(b, lane, &most) * heads;
-    // Few short items: one CTA each. Else equal shares, of at least MIN_TILES tiles.
-    const int64_t n_items = static_cast<int64_t>(b.n_seqs) * heads;
-    const bool whole_items = most <= WHOLE_TILES && n_items <= gridDim.x;
-    int64_t ctas = whole_items ? n_items : total / MIN_TILES;
-    ctas = ctas < 1 ? 1 : (ctas > gridDim.x ? gridDim.x : ctas);
-    if (blockIdx.x >= ctas) return;
-    const int64_t share = quotient(total, ctas);
-    const Split split{share, total - share * ctas};
-    // Where this CTA begins, and how many tiles it takes.
-    int seq, head, t0;
-    int64_t x = 0, left;
-    if (whole_items) {
-        seq = static_cast<int>(blockIdx.x) / heads;
-        head = static_cast<int>(blockIdx.x) - seq * heads;
-        t0 = 0;
-        left = tiles_of(clamped_len(b, seq));
-    } else {
-        int64_t before;
-        x = split.first(blockIdx.x);
-        left = split.first(blockIdx.x + 1) - x;
-        find_seq(b, lane, x, heads, &seq, &before);
-        const int tiles = tiles_of(clamped_len(b, seq));
-        head = static_cast<int>(quotient(x - before, tiles));
-        t0 = static_cast<int>(x - before - static_cast<int64_t>(head) * tiles);
-    }
+    const Share sh = p.many_tiles ? share_of<int64_t>(b, lane, heads, blockIdx.x, gridDim.x)
+                                  : share_of<int>(b, lane, heads, blockIdx.x, gridDim.x);
+    if (sh.left == 0) return;
+    const Split split = sh.split;
+    int seq = sh.seq, head = sh.head, t0 = sh.t0;
+    int64_t x = sh.x, left = sh.left;
     const WaitCtx wc{p.abort_word, p.status_word(), p.timeout_ns, p.epoch};
     bool alive = true;
     uint32_t count = 0;  // tiles of this CTA so far: stage count % S, phase count / S
@@ -555,25 +581,42 @@ __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
     }
     // The parts of split items, joined when the CTA's own tiles are done. Up to JOIN_MOST parts:
     // the last CTA to arrive joins them. More (all their CTAs are resident: one per SM, no more
-    // than SMs): each waits for the others and joins its share of the outputs.
-    if (warp < WARPS) {
+    // than SMs): each waits for the others and joins its share of the outputs. A CTA arrives for
+    // both its items before it waits for either, or the items would wait for one another in a row.
+    if (warp < WARPS && (pend[0].tiles | pend[1].tiles) != 0) {
+        uint32_t before[2] = {0u, 0u};  // how many times such an item has been complete: a count
+                                        // that is never reset, and changes only after this CTA has arrived
+#pragma unroll
+        for (int which = 0; which < 2; ++which)
+            if (pend[which].tiles != 0)
+                before[which] = *static_cast<volatile uint32_t *>(p.counters + G + split.owner(pend[which].item0));
+        bar_compute();                  // this CTA's parts are written
+        if (warp < 2 && lane == 0) {    // a warp for each
+            const Pending it = warp == 0 ? pend[0] : pend[1];
+            if (it.tiles != 0) {
+                const int a = split.owner(it.item0), parts = split.owner(it.item0 + it.tiles - 1) - a + 1;
+                const bool last = static_cast<int>(arrive_acq_rel(p.counters + a)) == parts - 1;
+                if (last) {
+                    p.counters[a] = 0u;  // zero again for the next call
+                    if (parts > JOIN_MOST) st_release_u32(p.counters + G + a, (warp == 0 ? before[0] : before[1]) + 1u);
+                }
+                sm_last[warp] = last ? 1 : 0;
+            }
+        }
+        bar_compute();
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
             const Pending it = pend[which];
             if (it.tiles == 0) continue;
+            const bool last = sm_last[which] != 0;
             const int a = split.owner(it.item0), z = split.owner(it.item0 + it.tiles - 1);
             const int parts = z - a + 1;
-            uint32_t *arrived = p.counters + a, *done = p.counters + G + a;  // of the item that begins in CTA a
+            const uint32_t *times = p.counters + G + a;
             // part i's slot: 1 for the CTA in which the item begins, 0 for the others
             auto part = [&](int i) { return slot_of(a + i, i == 0 ? 1 : 0); };
             const int units = it.g * (D / 4);  // of four outputs
-            bar_compute();                     // this CTA's part is written
-            if (tid == 0) *sm_last = static_cast<int>(arrive_acq_rel(arrived)) == parts - 1 ? 1 : 0;
-            bar_compute();
-            const bool last = *sm_last != 0;
             if (parts <= JOIN_MOST) {
                 if (!last) continue;
-                if (tid == 0) *arrived = 0u;   // zero again for the next call
                 for (int u = tid; u < units; u += 32 * WARPS) {
                     const int hh = u / (D / 4), d = (u - hh * (D / 4)) * 4;
                     float4 v[JOIN_MOST];
@@ -609,8 +652,8 @@ __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
                 WaitClock clk;
                 for (uint32_t n = 1; alive; ++n) {
                     uint32_t v;
-                    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(arrived) : "memory");
-                    if (v >= static_cast<uint32_t>(parts)) break;
+                    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(times) : "memory");
+                    if (v != before[which]) break;
                     if ((n & 15u) == 0 && !clk.ok(wc)) alive = false;
                 }
                 alive = __all_sync(0xffffffffu, alive);
@@ -675,8 +718,6 @@ __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
                 }
                 if (lane == 0) finish(it.seq, it.h0, hh, d, acc, top, L);
             }
-            bar_compute();                     // every warp has seen the count
-            if (tid == 0 && arrive_acq_rel(done) == static_cast<uint32_t>(parts - 1)) *arrived = *done = 0u;
         }
     }
     // A wait ran out: the copies already issued land before the CTA gives its memory back.

@@ -25,7 +25,7 @@
 namespace ubk {
 namespace {
 
-constexpr int APPEND_THREADS = 256;
+constexpr int APPEND_THREADS = 128;
 
 __device__ __forceinline__ void unpack8(const uint4 &x, float *f)
 {
