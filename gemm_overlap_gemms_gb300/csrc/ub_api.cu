@@ -180,6 +180,8 @@ uint32_t *abort_of(ub_handle *h) { return h->ctrl + UB_MAX_TP + ws_flag_words(h)
 int32_t *status_of(ub_handle *h) { return reinterpret_cast<int32_t *>(abort_of(h) + 1); }
 uint32_t *gather_counters_of(ub_handle *h) { return abort_of(h) + 8; }  // UB_MAX_TP words
 int join_words(const ub_handle *h) { return ubk::DECODE_COUNTERS * ubk::DECODE_CTAS_PER_SM * h->sm_count; }
+// Two tickets and the counters of split items of the prompt attention, behind them.
+constexpr int kPromptWords = 2 + 4 * ubk::PROMPT_SLOTS / 2;
 uint32_t *join_counters_of(ub_handle *h) { return gather_counters_of(h) + UB_MAX_TP; }
 
 // Makes the handle's device current for the duration of a call.
@@ -736,6 +738,8 @@ int ubk::handle_call(ub_handle_t h, cudaStream_t s, HandleCall *out)
     out->join_counters = join_counters_of(h);
     out->join_words = join_words(h);
     out->tickets = join_counters_of(h) + join_words(h);
+    out->piece_counters = out->tickets + 2;
+    out->ws_rows = h->ws + out->ws_floats;
     h->counters.last_T = h->T;
     return UB_OK;
 }
@@ -856,12 +860,12 @@ int ub_create(int64_t max_tokens, int64_t hidden, int tp, ub_dtype_t dtype, ub_h
     ++h->counters.device_allocations;
     h->max_pairs = h->sm_count / 2 > 0 ? h->sm_count / 2 : 1;
     h->ws_slots = 2 * (h->sm_count > 0 ? h->sm_count : 1);
-    h->ctrl_bytes = (UB_MAX_TP + ws_flag_words(h) + 8 + UB_MAX_TP + join_words(h) + 2) * sizeof(uint32_t);
+    h->ctrl_bytes = (UB_MAX_TP + ws_flag_words(h) + 8 + UB_MAX_TP + join_words(h) + kPromptWords) * sizeof(uint32_t);
     e = cudaMalloc(reinterpret_cast<void **>(&h->ctrl), h->ctrl_bytes);
     if (e != cudaSuccess) return cleanup(cuda_fail(e, "cudaMalloc(control block)"));
     ++h->counters.device_allocations;
     e = cudaMalloc(reinterpret_cast<void **>(&h->ws),
-                   static_cast<size_t>(h->ws_slots) * ubk::PARTIAL_FLOATS * sizeof(float));
+                   (static_cast<size_t>(h->ws_slots) * ubk::PARTIAL_FLOATS + 512 * ubk::PROMPT_SLOTS) * sizeof(float));
     if (e != cudaSuccess) return cleanup(cuda_fail(e, "cudaMalloc(split workspace)"));
     ++h->counters.device_allocations;
     e = cudaStreamCreateWithFlags(&h->side, cudaStreamNonBlocking);
@@ -1698,7 +1702,7 @@ int ub_clear_status(ub_handle_t h)
     DeviceGuard g(h->device);
     UB_CUDA(cudaMemsetAsync(abort_of(h), 0, 2 * sizeof(uint32_t), h->side));  // abort and status words
     // what a call whose wait ran out may have left counted
-    UB_CUDA(cudaMemsetAsync(join_counters_of(h), 0, (join_words(h) + 2) * sizeof(uint32_t), h->side));
+    UB_CUDA(cudaMemsetAsync(join_counters_of(h), 0, (join_words(h) + kPromptWords) * sizeof(uint32_t), h->side));
     UB_CUDA(cudaStreamSynchronize(h->side));
     return UB_OK;
 }

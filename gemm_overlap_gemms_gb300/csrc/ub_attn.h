@@ -29,6 +29,9 @@ struct HandleCall {
     uint32_t *join_counters; // of the decode attention
     int join_words;
     uint32_t *tickets;       // two words, zero between calls
+    uint32_t *piece_counters; // of the prompt attention's split items: 4 per item, zero between calls
+    float *ws_rows;          // PROMPT_SLOTS * 512
+
 };
 
 int handle_device(ub_handle_t h);
@@ -115,11 +118,16 @@ struct PromptParams {
     int units;               // kv_heads * (group >> pack_shift)
     float scale;
     uint32_t *tickets;       // work items drawn, CTAs done; zero between calls
+    float *ws;               // parts of items split over their keys: `slots` of 256 rows
+    float *ws_rows;          // their rows' maxima and sums: 512 per slot
+    uint32_t *counters;      // 4 words per split item, zero between calls
+    int slots;
     uint32_t *abort_word;
     uint64_t timeout_ns;
     uint32_t epoch;
     int pdl;
 };
+constexpr int PROMPT_SLOTS = 608;        // parts of split items, at most (half of it for heads of 128)
 constexpr int PROMPT_ROWS = 128;         // rows (tokens x packed heads) of one q tile, two per CTA
 constexpr int PROMPT_KEYS = 128;         // keys of one tile
 cudaError_t launch_attn_prompt(const PromptParams &p, int grid, cudaStream_t s);

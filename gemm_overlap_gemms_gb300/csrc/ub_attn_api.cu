@@ -282,6 +282,11 @@ int ub_attn_prompt(ub_handle_t h, const ub_attn_t *in, void *stream)
     p.units = a.kv_heads * (p.group >> p.pack_shift);
     p.scale = a.scale;
     p.tickets = c.tickets;
+    p.ws = c.ws;
+    p.ws_rows = c.ws_rows;
+    p.counters = c.piece_counters;
+    const size_t slots = c.ws_floats / (2 * PROMPT_ROWS * static_cast<size_t>(a.head_dim));
+    p.slots = static_cast<int>(slots < PROMPT_SLOTS ? slots : PROMPT_SLOTS);
     p.abort_word = c.abort_word;
     p.timeout_ns = c.timeout_ns;
     p.epoch = c.epoch;

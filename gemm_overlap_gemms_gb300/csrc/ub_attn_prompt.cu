@@ -39,7 +39,7 @@ constexpr int PR_THREADS = 512;
 constexpr int ITEMS = 4;                 // schedule ring
 constexpr int DONE = 16;                 // barriers of the ring's releases: more than can be unseen
 // Registers per thread by role; their sum is what the block is launched with (512 x 128).
-constexpr int SOFTMAX_REGS = 176, EPILOGUE_REGS = 72, SINGLE_REGS = 88;
+constexpr int SOFTMAX_REGS = 176, EPILOGUE_REGS = 88, SINGLE_REGS = 72;
 static_assert(2 * SOFTMAX_REGS + EPILOGUE_REGS + SINGLE_REGS == 4 * 128, "register split");
 constexpr int TM_S = 0, TM_O = 256;      // TMEM columns: S_i at 128 i, O_i at 256 + 128 i
 constexpr float RESCALE_LOG2 = 8.f;      // growth of the maximum (log2) that is put off
@@ -49,7 +49,7 @@ struct PromptShape {
     static constexpr int TILE_BYTES = PROMPT_KEYS * D * 2;
     static constexpr int HALF_BYTES = PROMPT_KEYS * 128;  // 64 columns of a tile
     static constexpr int STAGES = D == 128 ? 5 : 10;
-    static constexpr int SMEM = (2 + STAGES) * TILE_BYTES + 1024 + 768;
+    static constexpr int SMEM = (2 + STAGES) * TILE_BYTES + 2048 + 768;
     static_assert(SMEM <= 232448, "shared memory");
     static_assert(STAGES < DONE, "an unseen release per ring position at most");
 };
@@ -62,11 +62,22 @@ struct Item {
     int len;     // keys of the sequence
     int src;     // first key row (packed) or sequence (paged)
     int unit;
+    int j0, j1;  // its key tiles (a piece of a split item: a part of them)
+    int slot;    // first workspace slot of a split item; -1: not split
+    int piece, pieces;
+    int n;       // key tiles of the whole item
 };
+constexpr Item kNoItem = {-1, 0, 0, 0, 0, 0, 0, 0, -1, 0, 1, 0};
+// First key tile of piece i of an item of n tiles.
+__device__ __forceinline__ int piece_begin(int n, int i, int pieces)
+{
+    const int base = n / pieces, rem = n - base * pieces;
+    return i * base + (i < rem ? i : rem);
+}
 
 struct Range2 {
     int lim[2];  // keys that q tile i reaches
-    int n[2];    // its key tiles
+    int n[2];    // its key tiles, of those of the item or piece
     int tok[2];  // its tokens
     int nmax;
     int limmax;
@@ -82,7 +93,8 @@ __device__ __forceinline__ Range2 ranges(const Item &it, int tpt)
         lim = lim < 0 ? 0 : (lim > it.len ? it.len : lim);
         r.tok[i] = tok;
         r.lim[i] = lim;
-        r.n[i] = (lim + PROMPT_KEYS - 1) / PROMPT_KEYS;
+        const int n = (lim + PROMPT_KEYS - 1) / PROMPT_KEYS, most = it.j1 - it.j0;
+        r.n[i] = n - it.j0 < 0 ? 0 : (n - it.j0 > most ? most : n - it.j0);
     }
     r.nmax = r.n[0] > r.n[1] ? r.n[0] : r.n[1];
     r.limmax = r.lim[0] > r.lim[1] ? r.lim[0] : r.lim[1];
@@ -98,22 +110,6 @@ __device__ __forceinline__ Range2 uniform(Range2 r)
     }
     r.nmax = r.n[0] > r.n[1] ? r.n[0] : r.n[1];
     return r;
-}
-// A wait on the critical path: looks at the barrier for a while without being suspended.
-__device__ __forceinline__ bool mbar_wait_hot(uint32_t bar, uint32_t parity, const WaitCtx &w)
-{
-    for (int n = 0; n < 256; ++n) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity)
-            : "memory");
-        if (ok) return true;
-    }
-    return mbar_wait(bar, parity, w);
 }
 __device__ __forceinline__ bool elect_one()
 {
@@ -283,8 +279,9 @@ __device__ __forceinline__ int items_from(const SeqInfo &q, int c, int shift)
 
 // The work items of a call in the order "most key tiles first" (ties: by sequence, then by
 // tile), without a list: one warp counts the items of at least c key tiles over all
-// sequences and searches for the level of a rank. Up to 32 sequences stay in registers, one
-// per lane; beyond, they are read again for every count (from L1).
+// sequences, 32 levels c at once (one per lane, the sequences broadcast one by one), and so
+// finds the level of a rank. Up to 32 sequences stay in registers, one per lane; beyond, they
+// are read again for every count (from L1).
 struct Schedule {
     const PromptParams &p;
     int lane, shift, cmax, tiles;
@@ -308,22 +305,51 @@ struct Schedule {
         cmax = __reduce_max_sync(0xffffffffu, most);
         tiles = __reduce_add_sync(0xffffffffu, sum);
     }
-    __device__ __forceinline__ int count(int c) const
+    // Key tiles of all items together, about (each sequence's run evenly from its first item's
+    // to its last item's).
+    __device__ __forceinline__ float work() const
+    {
+        float sum = 0.f;
+        for (int i0 = 0; i0 < p.b.n_seqs; i0 += 32) {
+            const SeqInfo q = info(i0);
+            const int first = q.off + (1 << shift) < q.len ? q.off + (1 << shift) : q.len;
+            sum += 0.5f * items_from(q, 0, shift) * ((first > 0 ? first : 0) + q.len) * (1.f / PROMPT_KEYS);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        return sum;
+    }
+    // Items of at least c key tiles, for each lane's own c. (One copy of the code: it runs cold,
+    // before anything else of the call can start.)
+    __device__ __noinline__ int counts(int c) const
     {
         int sum = 0;
-        for (int i0 = 0; i0 < p.b.n_seqs; i0 += 32) sum += items_from(info(i0), c, shift);
-        return __reduce_add_sync(0xffffffffu, sum);
-    }
-    __device__ Item at(int g) const
-    {
-        int lo = 0, hi = cmax;  // count(lo) > g; find the largest such level
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (count(mid) > g) lo = mid;
-            else hi = mid - 1;
+        for (int i0 = 0; i0 < p.b.n_seqs; i0 += 32) {
+            const SeqInfo q = info(i0);
+            const int m = p.b.n_seqs - i0 < 32 ? p.b.n_seqs - i0 : 32;
+            for (int i = 0; i < m; ++i) {
+                const SeqInfo x{0, __shfl_sync(0xffffffffu, q.n, i), __shfl_sync(0xffffffffu, q.len, i),
+                                __shfl_sync(0xffffffffu, q.off, i)};
+                sum += items_from(x, c, shift);
+            }
         }
-        int r = g - count(lo + 1);
-        Item it{-1, 0, 0, 0, 0, 0};
+        return sum;
+    }
+    // *level: the key tiles of the item
+    __device__ __noinline__ Item at(int g, int *level) const
+    {
+        // The largest level lo with count(lo) > g, in strides that fall to 1; the last pass
+        // covers lo + 1 too (31 levels at most are left for it).
+        int lo = 0, stride = cmax <= 30 ? 1 : (cmax + 32) / 32, k, n;
+        for (;; stride = stride <= 31 ? 1 : (stride + 30) / 31) {
+            n = counts(lo + lane * stride);
+            k = 31 - __clz(static_cast<int>(__ballot_sync(0xffffffffu, n > g) | 1u));
+            lo += k * stride;
+            if (stride == 1) break;
+        }
+        int r = g - __shfl_sync(0xffffffffu, n, k + 1);
+        *level = lo;
+        Item it = kNoItem;
         for (int i0 = 0; i0 < p.b.n_seqs; i0 += 32) {
             const SeqInfo q = info(i0);
             const int from = items_from(q, lo, shift), mine = from - items_from(q, lo + 1, shift);
@@ -351,6 +377,67 @@ struct Schedule {
     }
 };
 
+// Few rows over many keys (a call of fewer items than CTAs): items of more than `limit` key
+// tiles are cut into `pieces` pieces each, so that every CTA has work; limit is a CTA's even
+// share of the call (at least MIN_PIECE tiles), or what the workspace's slots allow. With
+// more items than CTAs nothing is split: joining costs more than an uneven end (measured: 256
+// rows of parts are joined in 13 us; 8152 packed tokens, whose longest items are 1.3 even
+// shares, took 61 us split in halves against 49 us whole).
+struct Plan {
+    int pieces;          // 1: nothing is split
+    uint32_t split_end;  // ranks [0, split_end): pieces of the split items, item by item
+    uint32_t total;      // ... then the whole items
+    int n_split;         // token tiles (of each unit) that are split
+};
+constexpr int MIN_PIECE = 8;
+__device__ Plan plan_of(const Schedule &sc, int units, int ctas, int slots)
+{
+    Plan pl{1, 0u, static_cast<uint32_t>(sc.tiles) * units, 0};
+    if (pl.total >= static_cast<uint32_t>(ctas) || sc.cmax <= MIN_PIECE) return pl;
+    int limit = static_cast<int>(sc.work() * units / ctas) + 1;
+    limit = limit < MIN_PIECE ? MIN_PIECE : limit;
+    // 32 limits at once; the smallest whose pieces fit the slots.
+    limit += static_cast<int>(static_cast<uint32_t>(limit) * static_cast<uint32_t>(sc.lane) / 4u);
+    const int n = sc.counts(limit + 1);
+    int pieces = (sc.cmax + limit - 1) / limit;
+    pieces = pieces < limit ? pieces : limit;  // none of a split item's is empty
+    const bool fits = limit < sc.cmax && static_cast<float>(n) * units * pieces <= slots;
+    const uint32_t good = __ballot_sync(0xffffffffu, fits);
+    if (good == 0u) return pl;
+    const int pick = __ffs(static_cast<int>(good)) - 1;
+    pl.pieces = __shfl_sync(0xffffffffu, pieces, pick);
+    pl.n_split = __shfl_sync(0xffffffffu, n, pick);
+    pl.split_end = static_cast<uint32_t>(pl.n_split * units * pl.pieces);
+    pl.total += static_cast<uint32_t>(pl.n_split * units * (pl.pieces - 1));
+    return pl;
+}
+__device__ Item item_of(const Schedule &sc, const Plan &pl, int units, uint32_t g)
+{
+    uint32_t rank = g;   // among the items; fewer than 2^32: T * heads rows
+    int piece = 0, pieces = 1;
+    if (g < pl.split_end) {
+        pieces = pl.pieces;
+        rank = g / static_cast<uint32_t>(pieces);
+        piece = static_cast<int>(g - rank * pieces);
+    } else if (pl.pieces > 1) {
+        rank = g - static_cast<uint32_t>(pl.n_split * units * (pl.pieces - 1));
+    }
+    const uint32_t tile = rank / static_cast<uint32_t>(units);
+    int level;
+    Item it = sc.at(static_cast<int>(tile), &level);
+    it.unit = static_cast<int>(rank - tile * units);
+    it.j0 = 0;
+    it.j1 = it.n = level;
+    if (pieces > 1) {
+        it.j0 = piece_begin(level, piece, pieces);
+        it.j1 = piece_begin(level, piece + 1, pieces);
+        it.slot = static_cast<int>(rank) * pieces;
+        it.piece = piece;
+        it.pieces = pieces;
+    }
+    return it;
+}
+
 // ---------------------------------------------------------------- kernel
 
 template <int D>
@@ -361,7 +448,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
     extern __shared__ __align__(1024) uint8_t base[];
     const uint32_t sm_q = smem_u32(base), sm_kv = sm_q + 2 * Sh::TILE_BYTES;
     float *sm_sum = reinterpret_cast<float *>(base + (2 + NST) * Sh::TILE_BYTES);  // [2][128]
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sm_sum + 256);
+    float *sm_max = sm_sum + 256;                                                  // [2][128]
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm_max + 256);
     const uint32_t b0 = smem_u32(bars);
     const uint32_t kv_full = b0, v_raw = b0 + 8 * NST, kv_done = b0 + 16 * NST;
     const uint32_t misc = b0 + 16 * NST + 8 * DONE;
@@ -423,10 +511,6 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
         alive = __all_sync(0xffffffffu, mbar_wait(bar, parity, wc)) != 0;
         return alive;
     };
-    auto wait_hot = [&](uint32_t bar, uint32_t parity) {
-        alive = __all_sync(0xffffffffu, mbar_wait_hot(bar, parity, wc)) != 0;
-        return alive;
-    };
     auto arrive = [&](uint32_t bar) {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
@@ -457,14 +541,14 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
             reach = reach > it.len ? it.len : reach;
             float m = -INFINITY, l = 0.f;
             for (int j = 0; j < r.n[i]; ++j) {
-                if (!wait_hot(s_full + 8 * i, n_s & 1)) break;
+                if (!wait(s_full + 8 * i, n_s & 1)) break;
                 ++n_s;
                 tc_fence_after();
                 float s[128];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, reinterpret_cast<uint32_t *>(s) + c * 32);
                 tmem_wait_ld();
-                const int cols = reach - j * PROMPT_KEYS;
+                const int cols = reach - (it.j0 + j) * PROMPT_KEYS;
                 if (cols < PROMPT_KEYS) {
 #pragma unroll
                     for (int c = 0; c < 128; ++c)
@@ -519,67 +603,135 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
             if (!wait(l_empty + 8 * i, (n_l & 1) ^ 1)) break;
             ++n_l;
             sm_sum[i * 128 + row] = l;
+            sm_max[i * 128 + row] = m;
             arrive(l_full + 8 * i);
-            if (p.lse && token < it.ntok) {
-                const int h = (it.unit << p.pack_shift) + (row & (pack - 1));
-                p.lse[static_cast<int64_t>(it.row0 + token) * p.heads + h] = l > 0.f ? m * p.scale + logf(l) : (l == 0.f ? -INFINITY : l);
-            }
         }
     } else if (warp < 12) {
         // ------------------------------------------------------------ epilogue
         fewer_registers<EPILOGUE_REGS>();
         const int row = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const float sl = p.scale * 1.4426950408889634f;
         uint32_t n_o[2] = {0, 0};
         Item it;
         for (uint32_t k = 0; next_item(k, it); ++k) {
             const Range2 r = ranges(it, tpt);
+            // A split item's part: [columns / 4][256 rows][4] fp32 and the rows' maxima and sums.
+            auto part_o = [&](int piece, int i) {
+                return reinterpret_cast<float4 *>(p.ws) + static_cast<int64_t>(it.slot + piece) * (64 * D) + i * 128 + row;
+            };
+            auto part_m = [&](int piece, int i) { return p.ws_rows + static_cast<int64_t>(it.slot + piece) * 512 + i * 128 + row; };
+            // One row's 32 columns from c on, times f, or zeros.
+            auto store = [&](int i, int c, const float *v, float f, bool none) {
+                const int token = i * tpt + (row >> p.pack_shift);
+                const int h = (it.unit << p.pack_shift) + (row & (pack - 1));
+                if (token >= it.ntok) return;
+                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + (it.row0 + token) * p.o_row + h * p.o_head + c;
+#pragma unroll
+                for (int u = 0; u < 32; u += 8) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = none ? 0u : pack_bf16x2(__float_as_uint(v[u + 2 * e] * f), __float_as_uint(v[u + 2 * e + 1] * f));
+                    *reinterpret_cast<uint4 *>(dst + u) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            };
+            auto store_lse = [&](int i, float m, float l) {
+                const int token = i * tpt + (row >> p.pack_shift);
+                const int h = (it.unit << p.pack_shift) + (row & (pack - 1));
+                if (p.lse && token < it.ntok)
+                    p.lse[static_cast<int64_t>(it.row0 + token) * p.heads + h] =
+                        l > 0.f ? m * p.scale + logf(l) : (l == 0.f ? -INFINITY : l);
+            };
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 if (r.tok[i] == 0 || !alive) continue;
-                const int token = i * tpt + (row >> p.pack_shift);
-                const int h = (it.unit << p.pack_shift) + (row & (pack - 1));
-                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + (it.row0 + token) * p.o_row + h * p.o_head;
-                float inv = 0.f;
-                bool none = true;                      // no key: zeros
-                if (r.n[i] > 0) {
-                    if (!wait(l_full + 8 * i, n_o[i] & 1)) continue;
-                    const float l = sm_sum[i * 128 + row];
-                    arrive(l_empty + 8 * i);
-                    none = l == 0.f;
-                    inv = 1.f / l;
-                    if (!wait(o_full + 8 * i, n_o[i] & 1)) continue;
-                    ++n_o[i];
-                    tc_fence_after();
-                } else if (p.lse && token < it.ntok) {
-                    p.lse[static_cast<int64_t>(it.row0 + token) * p.heads + h] = -INFINITY;
+                if (r.n[i] == 0) {
+                    if (it.slot >= 0) continue;        // no key in this piece: not a part of this q tile
+                    const float zero[32] = {};
+                    for (int c = 0; c < D; c += 32) store(i, c, zero, 0.f, true);
+                    store_lse(i, -INFINITY, 0.f);
+                    continue;
                 }
+                if (!wait(l_full + 8 * i, n_o[i] & 1)) continue;
+                const float l = sm_sum[i * 128 + row], m = sm_max[i * 128 + row];
+                arrive(l_empty + 8 * i);
+                if (!wait(o_full + 8 * i, n_o[i] & 1)) continue;
+                ++n_o[i];
+                tc_fence_after();
+                const float inv = 1.f / l;
 #pragma unroll
                 for (int c = 0; c < D; c += 32) {
-                    uint32_t v[32];
-                    if (r.n[i] > 0) {
-                        tmem_ld32(tmem + TM_O + i * 128 + lanes + c, v);
-                        tmem_wait_ld();
-                    }
-                    if (token < it.ntok) {
+                    float v[32];
+                    tmem_ld32(tmem + TM_O + i * 128 + lanes + c, reinterpret_cast<uint32_t *>(v));
+                    tmem_wait_ld();
+                    if (it.slot < 0) {
+                        store(i, c, v, inv, l == 0.f);
+                    } else {
+                        float4 *to = part_o(it.piece, i) + c / 4 * 256;
 #pragma unroll
-                        for (int u = 0; u < 32; u += 8) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                w[e] = none ? 0u
-                                            : pack_bf16x2(__float_as_uint(__uint_as_float(v[u + 2 * e]) * inv),
-                                                          __float_as_uint(__uint_as_float(v[u + 2 * e + 1]) * inv));
-                            *reinterpret_cast<uint4 *>(dst + c + u) = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
+                        for (int u = 0; u < 32; u += 4) to[u / 4 * 256] = make_float4(v[u], v[u + 1], v[u + 2], v[u + 3]);
                     }
                 }
-                if (r.n[i] > 0) {
-                    tc_fence_before();
-                    arrive(o_empty + 8 * i);
+                tc_fence_before();
+                arrive(o_empty + 8 * i);
+                if (it.slot < 0) {
+                    store_lse(i, m, l);
+                } else {
+                    part_m(it.piece, i)[0] = m;
+                    part_m(it.piece, i)[256] = l;
                 }
             }
             if (!alive) break;
+            if (it.slot < 0) continue;
+            // The last piece to come joins all, each warp its own rows: a counter per item and warp.
+            // (Bound by latency: 32 columns of one part in flight per row.)
+            __syncwarp();
+            uint32_t come = 0;
+            if (lane == 0) {
+                uint32_t *counter = p.counters + (it.slot / it.pieces) * 4 + (warp & 3);
+                asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(come) : "l"(counter) : "memory");
+                if (come == static_cast<uint32_t>(it.pieces - 1)) *counter = 0u;  // zero again for the next call
+            }
+            come = __shfl_sync(0xffffffffu, come, 0);
+            __syncwarp();
+            if (come != static_cast<uint32_t>(it.pieces - 1)) continue;
+            const int level = it.n;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (r.tok[i] == 0) continue;
+                // Pieces that begin before this q tile's last key have a part of it.
+                const int n = (r.lim[i] + PROMPT_KEYS - 1) / PROMPT_KEYS;
+                int parts = 0;
+                while (parts < it.pieces && piece_begin(level, parts, it.pieces) < n) ++parts;
+                float M = -INFINITY, L = 0.f;
+                for (int q = 0; q < parts; ++q) M = fmaxf(M, __ldcg(part_m(q, i)));
+                const float ref = M == -INFINITY ? 0.f : M;
+                for (int q = 0; q < parts; ++q) L += __ldcg(part_m(q, i) + 256) * ex2((__ldcg(part_m(q, i)) - ref) * sl);
+                const float inv = 1.f / L;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    float acc[32];
+#pragma unroll
+                    for (int u = 0; u < 32; ++u) acc[u] = 0.f;
+#pragma unroll 1
+                    for (int q = 0; q < parts; ++q) {
+                        const float f = ex2((__ldcg(part_m(q, i)) - ref) * sl);
+                        float4 v[8];
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) v[u] = __ldcg(part_o(q, i) + (c / 4 + u) * 256);
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) {
+                            acc[4 * u] += v[u].x * f;
+                            acc[4 * u + 1] += v[u].y * f;
+                            acc[4 * u + 2] += v[u].z * f;
+                            acc[4 * u + 3] += v[u].w * f;
+                        }
+                    }
+                    store(i, c, acc, inv, L == 0.f);
+                }
+                store_lse(i, M, L);
+            }
         }
     } else {
       // the four single warps
@@ -614,9 +766,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
             };
             load_q(0);
             for (int j = 0; j < r.nmax && alive; ++j) {
-                const int key0 = j * PROMPT_KEYS;
+                const int key0 = (it.j0 + j) * PROMPT_KEYS;
                 // every key that is multiplied is loaded (pages past the length as zeros)
-                const int n_box = p.paged ? (extent(r.limmax, j) + box - 1) / box : 1;
+                const int n_box = p.paged ? (extent(r.limmax, it.j0 + j) + box - 1) / box : 1;
                 const int page0 = key0 >> p.b.page_shift;
                 const int boxes = PROMPT_KEYS / box;
                 if (p.paged && page0 + boxes > cached0 + cached_n) {
@@ -642,7 +794,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                         two = (two & ~(1u << at)) | (static_cast<uint32_t>(kind == 0 && j > 0) << at);
                     }
                     // The last tile of V goes through the zeroing warp when it ends inside 16 keys.
-                    const bool fix = kind == 1 && j == r.nmax - 1 && extent(r.limmax, j) > it.len - key0;
+                    const bool fix = kind == 1 && j == r.nmax - 1 && extent(r.limmax, it.j0 + j) > it.len - key0;
                     const uint32_t bar = (fix ? v_raw : kv_full) + 8 * st;
                     const CUtensorMap *map = kind == 0 ? &p.tmK : &p.tmV;
                     const uint32_t dst = sm_kv + st * Sh::TILE_BYTES;
@@ -693,6 +845,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
         for (uint32_t k = 0; next_item(k, it); ++k) {
             const Range2 r = uniform(ranges(it, tpt));
             const int n = i == 0 ? r.n[0] : r.n[1], lim = i == 0 ? r.lim[0] : r.lim[1];
+            const int j0 = __shfl_sync(0xffffffffu, it.j0, 0);
             if (n > 0) {
                 if (!wait(q_full + 8 * i, n_q & 1)) break;
                 ++n_q;
@@ -709,11 +862,11 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                 if (!in_turn(step - 1 + i)) break;
                 const uint64_t v = v_desc + ((c - 1) % NST) * (Sh::TILE_BYTES / 16);
                 const uint64_t kk = k_desc + (c % NST) * (Sh::TILE_BYTES / 16);
-                const int steps = pv ? extent(lim, j) / 16 : 0;
-                const uint32_t s_idesc = prompt_idesc(s_next ? extent(lim, j + 1) : 16, false);
+                const int steps = pv ? extent(lim, j0 + j) / 16 : 0;
+                const uint32_t s_idesc = prompt_idesc(s_next ? extent(lim, j0 + j + 1) : 16, false);
                 constexpr uint32_t o_idesc = prompt_idesc(D, true);
                 if (pv) {
-                    if (!wait_hot(p_full + 8 * i, n_p & 1)) break;
+                    if (!wait(p_full + 8 * i, n_p & 1)) break;
                     ++n_p;
                 }
                 tc_fence_after();
@@ -752,22 +905,18 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
     } else {
         // ------------------------------------------------------------ schedule
         const Schedule sched(p, lane, 8 - p.pack_shift);
-        const int64_t total = static_cast<int64_t>(sched.tiles) * p.units;
+        const Plan plan = plan_of(sched, p.units, gridDim.x, p.slots);
         // Longest first. The first two items of each CTA are dealt forth and back over the CTAs,
         // the rest by tickets, drawn when the loads of the item before have been issued.
         auto publish = [&](uint32_t k) {
-            int64_t g = k == 0 ? blockIdx.x : 2 * static_cast<int64_t>(gridDim.x) - 1 - blockIdx.x;
+            uint32_t g = k == 0 ? blockIdx.x : 2 * gridDim.x - 1 - blockIdx.x;
             if (k >= 2) {
                 uint32_t ticket = 0;
                 if (lane == 0) ticket = atomicAdd(p.tickets, 1u);
-                g = 2 * static_cast<int64_t>(gridDim.x) + __shfl_sync(0xffffffffu, ticket, 0);
+                g = 2 * gridDim.x + __shfl_sync(0xffffffffu, ticket, 0);
             }
-            Item it{-1, 0, 0, 0, 0, 0};
-            if (g < total) {
-                const uint32_t rank = static_cast<uint32_t>(g);  // fewer than 2^32 items: T * heads rows
-                it = sched.at(static_cast<int>(rank / static_cast<uint32_t>(p.units)));
-                it.unit = static_cast<int>(rank % static_cast<uint32_t>(p.units));
-            }
+            Item it = kNoItem;
+            if (g < plan.total) it = item_of(sched, plan, p.units, g);
             if (k >= ITEMS && !wait(it_empty + 8 * (k % ITEMS), (k / ITEMS - 1) & 1)) return it;
             if (lane == 0) items[k % ITEMS] = it;
             arrive(it_full + 8 * (k % ITEMS));
@@ -784,8 +933,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                 if (!alive) break;
             }
             const Range2 r = ranges(it, tpt);
-            const int j = r.nmax - 1, valid = it.len - j * PROMPT_KEYS;
-            const int ext = r.nmax > 0 ? extent(r.limmax, j) : 0;
+            const int j = r.nmax - 1, valid = it.len - (it.j0 + j) * PROMPT_KEYS;
+            const int ext = r.nmax > 0 ? extent(r.limmax, it.j0 + j) : 0;
             if (ext > valid) {
                 const uint32_t st = (c + 2 * j + 1) % NST;
                 if (!wait(v_raw + 8 * st, (used >> st) & 1)) break;

@@ -299,6 +299,27 @@ def test_prompt_paged(buf, page, heads, kv_heads, dim):
     check_prompt(b, q, lambda s: (b.rows(b.k_cache, s), b.rows(b.v_cache, s)), out, lse)
 
 
+@pytest.mark.parametrize("heads,kv_heads,dim", [(2, 2, 128), (8, 1, 64), (6, 3, 128)])
+@pytest.mark.parametrize("new,kv", [([40, 1, 300], [9000, 5001, 300]), ([1], [20000]), ([700, 3, 16], [2500, 1030, 16]),
+                                    ([130, 0, 129], [6000, 50, 4097])])
+def test_prompt_chunks_over_long_caches(buf, new, kv, heads, kv_heads, dim):
+    """Few tokens over many cached keys: items split over their keys and joined."""
+    b = ref.Batch(new, kv, page=32, kv_heads=kv_heads, dim=dim, pad=1, seed=heads, fill=float("nan"))
+    buf.set_active_shape([b.T, 256])
+    q = b.randn(b.T, heads, dim, std=1.5)
+    out = sentinel((b.T, heads, dim))
+    out, lse = buf.attn_prompt_paged(q, b.k_cache, b.v_cache, b.starts, b.lens, b.table, out=out, lse=True)
+    ok(buf)
+    check_prompt(b, q, lambda s: (b.rows(b.k_cache, s), b.rows(b.v_cache, s)), out, lse)
+    for _ in range(5):
+        assert torch.equal(buf.attn_prompt_paged(q, b.k_cache, b.v_cache, b.starts, b.lens, b.table)[:sum(new)], out[:sum(new)])
+
+
+def test_prompt_packed_split(buf):
+    b = ref.Batch([3000, 129, 2500, 17], [0] * 4, kv_heads=1, dim=128, pad=2, seed=4)
+    run_packed(buf, b, 1, 1, 128)
+
+
 def test_prompt_paged_rows_without_keys(buf):
     b = ref.Batch([300, 200, 40], [0, 3, 150], page=16, kv_heads=1, dim=64, pad=1, seed=1, fill=float("nan"))
     buf.set_active_shape([b.T, 256])
