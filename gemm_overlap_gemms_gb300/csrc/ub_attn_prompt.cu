@@ -42,6 +42,10 @@ constexpr int DONE = 16;                 // barriers of the ring's releases: mor
 constexpr int SOFTMAX_REGS = 176, EPILOGUE_REGS = 88, SINGLE_REGS = 72;
 static_assert(2 * SOFTMAX_REGS + EPILOGUE_REGS + SINGLE_REGS == 4 * 128, "register split");
 constexpr int TM_S = 0, TM_O = 256;      // TMEM columns: S_i at 128 i, O_i at 256 + 128 i
+// Heads of 128: the weights of the first PART steps of 16 keys are handed over while the rest
+// are computed (16384 tokens: 337 against 350 us; heads of 64, whose products are half as
+// long, lose by it: 78 against 75 us for chunks over a cache).
+constexpr int PART = 4;
 constexpr float RESCALE_LOG2 = 8.f;      // growth of the maximum (log2) that is put off
 
 template <int D>
@@ -445,6 +449,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
 {
     using Sh = PromptShape<D>;
     constexpr int NST = Sh::STAGES;
+    constexpr bool EARLY = D == 128;
     extern __shared__ __align__(1024) uint8_t base[];
     const uint32_t sm_q = smem_u32(base), sm_kv = sm_q + 2 * Sh::TILE_BYTES;
     float *sm_sum = reinterpret_cast<float *>(base + (2 + NST) * Sh::TILE_BYTES);  // [2][128]
@@ -453,13 +458,13 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
     const uint32_t b0 = smem_u32(bars);
     const uint32_t kv_full = b0, v_raw = b0 + 8 * NST, kv_done = b0 + 16 * NST;
     const uint32_t misc = b0 + 16 * NST + 8 * DONE;
-    const uint32_t q_full = misc, q_empty = misc + 16, s_full = misc + 32, p_full = misc + 48, o_empty = misc + 64,
+    const uint32_t q_full = misc, q_empty = misc + 16, s_full = misc + 32, p_full = misc + 48, p_part = misc + 152, o_empty = misc + 64,
                    l_full = misc + 80, l_empty = misc + 96, o_full = misc + 112, drain = misc + 128, want = misc + 144,
-                   it_full = misc + 160, it_empty = it_full + 8 * ITEMS;
-    Item *items = reinterpret_cast<Item *>(reinterpret_cast<uint8_t *>(bars) + 16 * NST + 8 * DONE + 160 + 16 * ITEMS);
+                   it_full = misc + 168, it_empty = it_full + 8 * ITEMS;
+    Item *items = reinterpret_cast<Item *>(reinterpret_cast<uint8_t *>(bars) + 16 * NST + 8 * DONE + 168 + 16 * ITEMS);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(items + ITEMS);
     volatile uint32_t *turn = tmem_slot + 1;     // steps that the issuer of each q tile has done
-    static_assert(16 * NST + 8 * DONE + 160 + 16 * ITEMS + sizeof(Item) * ITEMS + 12 <= 768, "barrier area");
+    static_assert(16 * NST + 8 * DONE + 168 + 16 * ITEMS + sizeof(Item) * ITEMS + 12 <= 768, "barrier area");
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     if ((sm_q & 1023u) != 0u) {  // the swizzled tiles need what the declaration asks for
@@ -476,6 +481,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
             mbar_init(q_full + 8 * i, 1);
             mbar_init(q_empty + 8 * i, 1);
             mbar_init(s_full + 8 * i, 1);
+            mbar_init(p_part + 8 * i, 4);    // the first PART steps of P written, O rescaled
             mbar_init(p_full + 8 * i, 4);
             mbar_init(o_empty + 8 * i, 4);
             mbar_init(l_full + 8 * i, 4);
@@ -592,10 +598,12 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                         pk[c / 2] = pack_bf16x2(__float_as_uint(e0), __float_as_uint(e1));
                     }
                     tmem_st16(ts + c0 / 2, pk);
+                    if ((EARLY && c0 + 32 == PART * 16) || c0 == 96) {
+                        tmem_wait_st();
+                        tc_fence_before();
+                        arrive((c0 == 96 ? p_full : p_part) + 8 * i);
+                    }
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                arrive(p_full + 8 * i);
                 const uint64_t both = add2(sum[0], sum[1]);
                 l = l * f + (low(both) + high(both));
             }
@@ -866,6 +874,15 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                 const uint32_t s_idesc = prompt_idesc(s_next ? extent(lim, j0 + j + 1) : 16, false);
                 constexpr uint32_t o_idesc = prompt_idesc(D, true);
                 if (pv) {
+                    if (EARLY) {
+                        if (!wait(p_part + 8 * i, n_p & 1)) break;
+                        tc_fence_after();
+                        if (steps == PROMPT_KEYS / 16 && elect_one()) {
+#pragma unroll
+                            for (int s = 0; s < PART; ++s) umma_ts(to, tp + s * 8, v + s * 128, o_idesc, j > 0 || s > 0);
+                        }
+                        __syncwarp();
+                    }
                     if (!wait(p_full + 8 * i, n_p & 1)) break;
                     ++n_p;
                 }
@@ -873,7 +890,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                 if (elect_one()) {
                     if (steps == PROMPT_KEYS / 16) {
 #pragma unroll
-                        for (int s = 0; s < PROMPT_KEYS / 16; ++s) umma_ts(to, tp + s * 8, v + s * 128, o_idesc, j > 0 || s > 0);
+                        for (int s = EARLY ? PART : 0; s < PROMPT_KEYS / 16; ++s)
+                            umma_ts(to, tp + s * 8, v + s * 128, o_idesc, j > 0 || s > 0);
                     } else {  // the sequence's last keys
                         for (int s = 0; s < steps; ++s) umma_ts(to, tp + s * 8, v + s * 128, o_idesc, j > 0 || s > 0);
                     }
