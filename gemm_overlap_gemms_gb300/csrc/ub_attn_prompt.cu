@@ -209,18 +209,6 @@ __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *v)
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(v[0]),
-        "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
-        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]),
-        "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
-        "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(taddr)
-        : "memory");
-}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *v)
 {
     asm volatile(
@@ -270,15 +258,18 @@ __device__ __forceinline__ SeqInfo seq_info(const PromptParams &p, int s)
     q.off = q.len - q.n;
     return q;
 }
-// Items (token tiles of 1 << shift tokens) of the sequence that reach at least `c` key tiles.
+// Of the `nt` items (token tiles of 1 << shift tokens) of a sequence, those that reach at
+// least `c` key tiles.
+__device__ __forceinline__ int reaching(int nt, int len, int off, int c, int shift)
+{
+    const int x = (c - 1) * PROMPT_KEYS;
+    const uint32_t t = x < off ? 0u : (static_cast<uint32_t>(x) - static_cast<uint32_t>(off)) >> shift;
+    const int n = nt - (t < static_cast<uint32_t>(nt) ? static_cast<int>(t) : nt);
+    return c <= 0 ? nt : (len <= x ? 0 : n);
+}
 __device__ __forceinline__ int items_from(const SeqInfo &q, int c, int shift)
 {
-    const int nt = (q.n + (1 << shift) - 1) >> shift;
-    const int x = (c - 1) * PROMPT_KEYS;
-    if (c <= 0) return nt;
-    if (q.len <= x) return 0;
-    const uint32_t t = x < q.off ? 0u : (static_cast<uint32_t>(x) - static_cast<uint32_t>(q.off)) >> shift;
-    return nt - (t < static_cast<uint32_t>(nt) ? static_cast<int>(t) : nt);
+    return reaching((q.n + (1 << shift) - 1) >> shift, q.len, q.off, c, shift);
 }
 
 // The work items of a call in the order "most key tiles first" (ties: by sequence, then by
@@ -288,19 +279,18 @@ __device__ __forceinline__ int items_from(const SeqInfo &q, int c, int shift)
 // are read again for every count (from L1).
 struct Schedule {
     const PromptParams &p;
-    int lane, shift, cmax, tiles;
+    int lane, shift, n_seqs, cmax, tiles;
     SeqInfo own;
 
     __device__ __forceinline__ SeqInfo info(int i0) const
     {
         if (i0 == 0) return own;
-        return i0 + lane < p.b.n_seqs ? seq_info(p, i0 + lane) : SeqInfo{0, 0, 0, 0};
+        return i0 + lane < n_seqs ? seq_info(p, i0 + lane) : SeqInfo{0, 0, 0, 0};
     }
-    __device__ __forceinline__ Schedule(const PromptParams &params, int ln, int sh) : p(params), lane(ln), shift(sh)
+    __device__ __forceinline__ void measure()  // cmax, tiles
     {
-        own = lane < p.b.n_seqs ? seq_info(p, lane) : SeqInfo{0, 0, 0, 0};
         int most = 0, sum = 0;
-        for (int i0 = 0; i0 < p.b.n_seqs; i0 += 32) {
+        for (int i0 = 0; i0 < n_seqs; i0 += 32) {
             const SeqInfo q = info(i0);
             const int n = q.n > 0 ? static_cast<int>((static_cast<uint32_t>(q.len) + PROMPT_KEYS - 1) / PROMPT_KEYS) : 0;
             most = n > most ? n : most;
@@ -314,7 +304,7 @@ struct Schedule {
     __device__ __forceinline__ float work() const
     {
         float sum = 0.f;
-        for (int i0 = 0; i0 < p.b.n_seqs; i0 += 32) {
+        for (int i0 = 0; i0 < n_seqs; i0 += 32) {
             const SeqInfo q = info(i0);
             const int first = q.off + (1 << shift) < q.len ? q.off + (1 << shift) : q.len;
             sum += 0.5f * items_from(q, 0, shift) * ((first > 0 ? first : 0) + q.len) * (1.f / PROMPT_KEYS);
@@ -328,14 +318,14 @@ struct Schedule {
     __device__ __noinline__ int counts(int c) const
     {
         int sum = 0;
-        for (int i0 = 0; i0 < p.b.n_seqs; i0 += 32) {
+        for (int i0 = 0; i0 < n_seqs; i0 += 32) {
             const SeqInfo q = info(i0);
-            const int m = p.b.n_seqs - i0 < 32 ? p.b.n_seqs - i0 : 32;
-            for (int i = 0; i < m; ++i) {
-                const SeqInfo x{0, __shfl_sync(0xffffffffu, q.n, i), __shfl_sync(0xffffffffu, q.len, i),
-                                __shfl_sync(0xffffffffu, q.off, i)};
-                sum += items_from(x, c, shift);
-            }
+            const int m = n_seqs - i0 < 32 ? n_seqs - i0 : 32;
+            const int nt = items_from(q, 0, shift);
+#pragma unroll 4
+            for (int i = 0; i < m; ++i)
+                sum += reaching(__shfl_sync(0xffffffffu, nt, i), __shfl_sync(0xffffffffu, q.len, i),
+                                __shfl_sync(0xffffffffu, q.off, i), c, shift);
         }
         return sum;
     }
@@ -354,7 +344,7 @@ struct Schedule {
         int r = g - __shfl_sync(0xffffffffu, n, k + 1);
         *level = lo;
         Item it = kNoItem;
-        for (int i0 = 0; i0 < p.b.n_seqs; i0 += 32) {
+        for (int i0 = 0; i0 < n_seqs; i0 += 32) {
             const SeqInfo q = info(i0);
             const int from = items_from(q, lo, shift), mine = from - items_from(q, lo + 1, shift);
             int upto = mine;
@@ -506,8 +496,10 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    pdl_wait();
-    pdl_trigger();
+    if (warp != 15) {
+        pdl_wait();
+        pdl_trigger();
+    }
 
     const WaitCtx wc{p.abort_word, p.b.status, p.timeout_ns, p.epoch};
     const int pack = 1 << p.pack_shift;
@@ -922,32 +914,53 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
         __syncwarp();
     } else {
         // ------------------------------------------------------------ schedule
-        const Schedule sched(p, lane, 8 - p.pack_shift);
-        const Plan plan = plan_of(sched, p.units, gridDim.x, p.slots);
+        // The first item is looked up twice, at first in a call of made-up numbers and before the
+        // grid ahead has finished: the code is in the instruction cache by the time that this
+        // call's numbers may be read, and everything else waits for the first item.
+        Schedule sched{p, lane, 8 - p.pack_shift, 1, 0, 0, {0, lane == 0 ? 65536 : 0, lane == 0 ? 65536 : 0, 0}};
+        Plan plan;
+        Item it;
+#pragma unroll 1
+        for (int real = 0; real < 2; ++real) {
+            if (real) {
+                pdl_wait();
+                pdl_trigger();
+                sched.n_seqs = p.b.n_seqs;
+                sched.own = lane < p.b.n_seqs ? seq_info(p, lane) : SeqInfo{0, 0, 0, 0};
+            }
+            sched.measure();
+            plan = plan_of(sched, p.units, gridDim.x, p.slots);
+            it = kNoItem;
+            if (blockIdx.x < plan.total) it = item_of(sched, plan, p.units, blockIdx.x);
+        }
         // Longest first. The first two items of each CTA are dealt forth and back over the CTAs,
         // the rest by tickets, drawn when the loads of the item before have been issued.
-        auto publish = [&](uint32_t k) {
-            uint32_t g = k == 0 ? blockIdx.x : 2 * gridDim.x - 1 - blockIdx.x;
+        auto publish = [&](uint32_t k, Item it) {
+            if (k >= ITEMS && !wait(it_empty + 8 * (k % ITEMS), (k / ITEMS - 1) & 1)) return;
+            if (lane == 0) items[k % ITEMS] = it;
+            arrive(it_full + 8 * (k % ITEMS));
+        };
+        auto draw = [&](uint32_t k) {
+            uint32_t g = 2 * gridDim.x - 1 - blockIdx.x;
             if (k >= 2) {
                 uint32_t ticket = 0;
                 if (lane == 0) ticket = atomicAdd(p.tickets, 1u);
                 g = 2 * gridDim.x + __shfl_sync(0xffffffffu, ticket, 0);
             }
-            Item it = kNoItem;
-            if (g < plan.total) it = item_of(sched, plan, p.units, g);
-            if (k >= ITEMS && !wait(it_empty + 8 * (k % ITEMS), (k / ITEMS - 1) & 1)) return it;
-            if (lane == 0) items[k % ITEMS] = it;
-            arrive(it_full + 8 * (k % ITEMS));
-            return it;
+            Item drawn = kNoItem;
+            if (g < plan.total) drawn = item_of(sched, plan, p.units, g);
+            publish(k, drawn);
+            return drawn;
         };
         uint32_t c = 0, used = 0;                      // ring position; phase bit per stage of v_raw
-        Item it = publish(0), it1 = it;
-        if (it.row0 >= 0) it1 = publish(1);
+        publish(0, it);
+        Item it1 = it;
+        if (it.row0 >= 0) it1 = draw(1);
         for (uint32_t k = 0; it.row0 >= 0 && alive; ++k) {
             // it: item k, it1: item k + 1, published before the zeroing of item k is waited for
             if (k >= 1) {
                 if (!wait(want, (k - 1) & 1)) break;
-                it1 = publish(k + 1);
+                it1 = draw(k + 1);
                 if (!alive) break;
             }
             const Range2 r = ranges(it, tpt);
