@@ -337,6 +337,7 @@ class UserBuffer:
         self.max_tokens, self.hidden, self.tp = int(shape[0]), int(shape[1]), int(tp_size)
         self._active = None
         self.device = torch.device("cuda", torch.cuda.current_device())
+        self._dev = self.device.index
 
     # -- lifetime
     def close(self):
@@ -621,13 +622,13 @@ class UserBuffer:
 
     def _raw_stream(self, stream) -> int:
         if stream is None:
-            return torch._C._cuda_getCurrentRawStream(self.device.index)
+            return torch._C._cuda_getCurrentRawStream(self._dev)
         return stream.cuda_stream
 
     def _out(self, out, name, T, H, D, stream):
         if out is None:
             out = self._new((T, H, D), _BF16, stream)
-        data, row, head, heads = _heads_view(out, name, T, D, self.device.index)
+        data, row, head, heads = _heads_view(out, name, T, D, self._dev)
         if heads != H:
             raise ValueError("%s has %d heads, q has %d" % (name, heads, H))
         return out, data, row, head
@@ -640,7 +641,7 @@ class UserBuffer:
             lse = self._new((T, H), _F32, stream)
         if (not isinstance(lse, torch.Tensor) or lse.dtype != _F32 or lse.device != self.device
                 or tuple(lse.shape) != (T, H) or not lse.is_contiguous()):
-            _attn_error(lse, "lse", _F32, self.device.index, "(%d, %d) and contiguous" % (T, H))
+            _attn_error(lse, "lse", _F32, self._dev, "(%d, %d) and contiguous" % (T, H))
         return lse, lse.data_ptr()
 
     def kv_append(self, q, k, v, cos, sin, seq_starts, kv_lens, page_table, k_cache, v_cache, q_out=None,
@@ -653,8 +654,8 @@ class UserBuffer:
         multiple of 16 up to D (None: no rotation). seq_starts int32 [n + 1], kv_lens int32 [n]
         (the tokens of this call included), page_table int32 [n, entries], on the device.
         k_cache, v_cache [pages, kv_heads, page_size, D]. q_out: like q, q itself allowed."""
-        dev = self.device.index
-        T = self.active_shape[0]
+        dev = self._dev
+        T, _ = self._active or self.active_shape
         D = _head_dim(q)
         qp, q0, q1, H = _heads_view(q, "q", T, D, dev)
         kp, k0, k1, G = _heads_view(k, "k", T, D, dev)
@@ -672,7 +673,9 @@ class UserBuffer:
         q_out, op, o0, o1 = self._out(q_out, "q_out", T, H, D, stream)
         a = _ATTN.pack(_ATTN.size, n, H, G, D, page, rot, 1 if interleaved else 0, 1.0, 0, pages, width, table_row,
                        positions, qp, q0, q1, kp, k0, k1, vp, v0, v1, op, o0, o1, *caches, starts, lens, table, cp, sp, 0)
-        _check(load().ub_kv_append(self._h, a, self._raw_stream(stream)))
+        rc = (_lib or load()).ub_kv_append(self._h, a, self._raw_stream(stream))
+        if rc:
+            _check(rc)
         return q_out
 
     def attn_prompt(self, q, k, v, seq_starts, out=None, lse=None, scale: float | None = None, stream=None):
@@ -680,8 +683,8 @@ class UserBuffer:
         [seq_starts[s], seq_starts[s + 1]) of q [T, heads, D] and of k, v [T, kv_heads, D].
         scale: 1 / sqrt(D) if None. lse: an fp32 [T, heads] tensor, or True for a new one.
         Returns out, or (out, lse) where lse is asked for. Rows of no sequence stay as they are."""
-        dev = self.device.index
-        T = self.active_shape[0]
+        dev = self._dev
+        T, _ = self._active or self.active_shape
         D = _head_dim(q)
         qp, q0, q1, H = _heads_view(q, "q", T, D, dev)
         kp, k0, k1, G = _heads_view(k, "k", T, D, dev)
@@ -693,15 +696,17 @@ class UserBuffer:
         lse, lp = self._lse(lse, T, H, stream)
         a = _ATTN.pack(_ATTN.size, n - 1, H, G, D, 0, 0, 0, D ** -0.5 if scale is None else scale, 0, 0, 0, 0, 0,
                        qp, q0, q1, kp, k0, k1, vp, v0, v1, op, o0, o1, 0, 0, 0, 0, 0, 0, 0, 0, starts, 0, 0, 0, 0, lp)
-        _check(load().ub_attn_prompt(self._h, a, self._raw_stream(stream)))
+        rc = (_lib or load()).ub_attn_prompt(self._h, a, self._raw_stream(stream))
+        if rc:
+            _check(rc)
         return out if lse is None else (out, lse)
 
     def attn_prompt_paged(self, q, k_cache, v_cache, seq_starts, kv_lens, page_table, out=None, lse=None,
                           scale: float | None = None, stream=None):
         """Causal attention of prompts, or of chunks of prompts, over the paged cache that holds
         their keys and values (after kv_append); arguments as there and in attn_prompt."""
-        dev = self.device.index
-        T = self.active_shape[0]
+        dev = self._dev
+        T, _ = self._active or self.active_shape
         D = _head_dim(q)
         qp, q0, q1, H = _heads_view(q, "q", T, D, dev)
         caches, pages, G, page = _caches(k_cache, v_cache, D, dev)
@@ -714,7 +719,9 @@ class UserBuffer:
         lse, lp = self._lse(lse, T, H, stream)
         a = _ATTN.pack(_ATTN.size, n, H, G, D, page, 0, 0, D ** -0.5 if scale is None else scale, 0, pages, width,
                        table_row, 0, qp, q0, q1, 0, 0, 0, 0, 0, 0, op, o0, o1, *caches, starts, lens, table, 0, 0, lp)
-        _check(load().ub_attn_prompt(self._h, a, self._raw_stream(stream)))
+        rc = (_lib or load()).ub_attn_prompt(self._h, a, self._raw_stream(stream))
+        if rc:
+            _check(rc)
         return out if lse is None else (out, lse)
 
     def attn_decode(self, q, k_cache, v_cache, kv_lens, page_table, out=None, lse=None, scale: float | None = None,
@@ -722,8 +729,8 @@ class UserBuffer:
         """Attention of one new token per sequence over the paged cache (ub_attn_decode): row s of
         q [T, heads, D] is sequence s, n = kv_lens.shape[0] <= T; arguments as in kv_append and
         attn_prompt. Rows from n on stay as they are."""
-        dev = self.device.index
-        T = self.active_shape[0]
+        dev = self._dev
+        T, _ = self._active or self.active_shape
         D = _head_dim(q)
         qp, q0, q1, H = _heads_view(q, "q", T, D, dev)
         caches, pages, G, page = _caches(k_cache, v_cache, D, dev)
@@ -733,7 +740,9 @@ class UserBuffer:
         lse, lp = self._lse(lse, T, H, stream)
         a = _ATTN.pack(_ATTN.size, n, H, G, D, page, 0, 0, D ** -0.5 if scale is None else scale, 0, pages, width,
                        table_row, 0, qp, q0, q1, 0, 0, 0, 0, 0, 0, op, o0, o1, *caches, 0, lens, table, 0, 0, lp)
-        _check(load().ub_attn_decode(self._h, a, self._raw_stream(stream)))
+        rc = (_lib or load()).ub_attn_decode(self._h, a, self._raw_stream(stream))
+        if rc:
+            _check(rc)
         return out if lse is None else (out, lse)
 
 
