@@ -432,6 +432,98 @@ def test_lengths_beyond_the_table_and_starts_out_of_order(buf):
         buf.clear_status()
 
 
+def test_everything_strided(buf):
+    """Token-by-token caches, keys beside values; strided q, k, v and outputs; rows between stay as they are."""
+    b = ref.Batch([70, 1, 200], [300, 90, 200], page=32, kv_heads=3, dim=64, seed=7)
+    both = torch.zeros(b.pages, 32, 2, 3, 64, dtype=torch.bfloat16, device="cuda")
+    both[:, :, 0], both[:, :, 1] = b.k_cache.transpose(1, 2), b.v_cache.transpose(1, 2)
+    b.k_cache, b.v_cache = both[:, :, 0].transpose(1, 2), both[:, :, 1].transpose(1, 2)
+    buf.set_active_shape([b.T, 256])
+    y = b.randn(b.T, 40, 80)[..., :64]
+    q, k, v = y[:, 0:18:3], y[:, 20:32:4], y[:, 33:39:2]
+    big = sentinel((2 * b.T, 12, 128))
+    out = big[1::2, ::2, 64:]
+    buf.kv_append(q, k, v, None, None, b.starts, b.lens, b.table, b.k_cache, b.v_cache, q_out=out)
+    ok(buf)
+    assert torch.equal(out, q)
+    for s, n in enumerate(b.new):
+        t0 = b.starts_list[s]
+        assert torch.equal(b.rows(b.k_cache, s)[:, -n:].transpose(0, 1), k[t0:t0 + n])
+        assert torch.equal(b.rows(b.v_cache, s)[:, -n:].transpose(0, 1), v[t0:t0 + n])
+    buf.attn_prompt_paged(q, b.k_cache, b.v_cache, b.starts, b.lens, b.table, out=out)
+    ok(buf)
+    check_prompt(b, q, lambda s: (b.rows(b.k_cache, s), b.rows(b.v_cache, s)), out, None)
+    buf.attn_prompt(q, k, v, b.starts, out=out)
+    ok(buf)
+    check_prompt(b, q, lambda s: tuple(x[b.starts_list[s]:b.starts_list[s + 1]].transpose(0, 1) for x in (k, v)), out, None)
+    assert is_sentinel(big[::2]) and is_sentinel(big[1::2, 1::2]) and is_sentinel(big[1::2, ::2, :64])
+
+
+def test_append_and_prompt_over_a_cache_past_32_bits(buf):
+    pages = (1 << 31) // (64 * 128) + 100
+    k = torch.zeros(pages, 1, 64, 128, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    b = ref.Batch([50, 3], [150, 90], page=64, kv_heads=1, dim=128, free=0, seed=8)
+    k[pages - b.pages:], v[pages - b.pages:] = b.k_cache, b.v_cache
+    b.k_cache, b.v_cache = k, v
+    b.table[b.table >= 0] += pages - b.pages
+    b.pages = pages
+    buf.set_active_shape([53, 256])
+    q, kk, vv = slices(b, 4, 1, 128)
+    out = buf.kv_append(q, kk, vv, None, None, b.starts, b.lens, b.table, k, v)
+    ok(buf)
+    assert torch.equal(b.rows(k, 0)[0, -50:], kk[:50, 0]) and torch.equal(b.rows(v, 1)[0, -3:], vv[50:, 0])
+    got = buf.attn_prompt_paged(out, k, v, b.starts, b.lens, b.table)
+    ok(buf)
+    check_prompt(b, q, lambda s: (b.rows(k, s), b.rows(v, s)), got, None)
+
+
+def test_prompt_from_a_graph_with_new_lengths(buf):
+    b = ref.Batch([60, 40], [300, 40], page=16, kv_heads=2, dim=128, free=40, seed=4)
+    b.table = torch.arange(b.pages, device="cuda", dtype=torch.int32)[:60].reshape(2, 30).contiguous()
+    buf.set_active_shape([100, 256])
+    q = b.randn(100, 4, 128)
+    out = sentinel((100, 4, 128))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        buf.attn_prompt_paged(q, b.k_cache, b.v_cache, b.starts, b.lens, b.table, out=out, stream=side)
+    for new, kv in (([60, 40], [300, 40]), ([1, 99], [480, 99]), ([100, 0], [100, 7])):
+        b.new, b.kv, b.starts_list = new, kv, [0, new[0], 100]
+        b.starts.copy_(torch.tensor(b.starts_list, dtype=torch.int32))
+        b.lens.copy_(torch.tensor(kv, dtype=torch.int32))
+        torch.cuda.synchronize()
+        graph.replay()
+        ok(buf)
+        check_prompt(b, q, lambda s: (b.rows(b.k_cache, s), b.rows(b.v_cache, s)), out, None)
+
+
+@pytest.mark.parametrize("options", [{"pdl": 0}, {"sm_margin": 100}, {"sm_margin": 151, "pdl": 0}, {"profile": 1}])
+def test_options(buf, options):
+    """Plain launches, few SMs and launch timing give the same results."""
+    b = ref.Batch([700, 3, 16], [2500, 1030, 16], page=32, kv_heads=2, dim=64, seed=3)
+    d = ref.Batch([1] * 5, [9000, 17, 300, 1, 0], page=32, kv_heads=2, dim=64, seed=4)
+    buf.set_active_shape([b.T, 256])
+    q = b.randn(b.T, 8, 64)
+    before = {k: buf.get_option(k) for k in options}
+    for k, v in options.items():
+        buf.set_option(k, v)
+    try:
+        out = sentinel((b.T, 8, 64))
+        buf.attn_prompt_paged(q, b.k_cache, b.v_cache, b.starts, b.lens, b.table, out=out)
+        ok(buf)
+        check_prompt(b, q, lambda s: (b.rows(b.k_cache, s), b.rows(b.v_cache, s)), out, None)
+        run_decode(buf, d, 8, 64)
+        if "profile" in options:
+            for op in ("attn_prompt", "attn_decode"):
+                ms, launches = buf.kernel_time(op)
+                assert launches == 1 and 0 < ms < 100
+    finally:
+        for k, v in before.items():
+            buf.set_option(k, v)
+
+
 # ---------------------------------------------------------------- refusals
 
 def test_refusals(buf):
