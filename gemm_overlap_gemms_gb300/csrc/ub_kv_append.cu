@@ -16,6 +16,12 @@
 // 16-byte vectors that the rotation pairs. With few tokens the heads of a token are dealt
 // over several warps instead, so that the loads of a decoding step are all in flight at
 // once.
+//
+// Measured (GB300): 16166 tokens, 32 + 8 + 8 heads of 128 (401 MB): 64 us, 6.3 TB/s; 8145 tokens,
+// 8 + 8 + 8 heads (104 MB): 20.4 us, 5.1 TB/s, of which about 4 us are launch and ramp. CTAs of
+// 128 threads (of 256: 68 us) and four heads in flight per lane (two: 66 us, eight: 73 us);
+// loading the first heads ahead of the token's place costs registers, and so warps: 77 us.
+// Four tokens: 2.4 us of GPU time, 9.5 us a call, bound by the host's side of it.
 #include <cuda_bf16.h>
 
 #include "ub_attn.h"

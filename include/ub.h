@@ -437,8 +437,13 @@ typedef struct {
  *
  * ub_attn_decode: the same for one new token per sequence: row s of q and out is sequence s
  * (n_seqs <= T), over all kv_lens[s] cached keys; 0 and lse -inf where there is none. The
- * cache's length is split over the whole GPU and joined in a fixed order; uses the handle's
- * workspace.
+ * cache's length is split over the whole GPU and joined in a fixed order.
+ *
+ * One kernel each, on `stream`. Attention uses the handle's workspace for the parts of split
+ * work, and counts finished parts there; results do not depend on which part finishes when.
+ * A sequence that ub_attn_decode spreads over more than 8 SMs is joined by CTAs that wait for
+ * one another (bounded, UB_ERR_TIMEOUT), as split GEMM tiles are: see ag_gemm, Concurrency.
+ * ub_clear_status also resets what such a call may have left counted.
  *
  * Errors: UB_ERR_ARG (null pointers, size, heads not a multiple of kv_heads, head_dim,
  * page_size, rot_dim, scale), UB_ERR_ZERO (n_seqs, heads, kv_heads, num_pages or table_width
@@ -489,8 +494,8 @@ int ub_get_counters(ub_handle_t h, ub_counters_t *out);
 
 /*
  * An addition of this library (kernel timing for the benchmark; the pages define none).
- * With UB_OPT_PROFILE = 1, every GEMM kernel launch of operation `op` (a UB_OP_* id) is
- * bracketed by CUDA events on its launch stream (up to 4096 launches are kept). This
+ * With UB_OPT_PROFILE = 1, every GEMM or attention kernel launch of operation `op` (a UB_OP_*
+ * id) is bracketed by CUDA events on its launch stream (up to 4096 launches are kept). This
  * call waits for the last recorded launch, returns the summed kernel time in
  * milliseconds and the launch count, and clears the record.
  */
