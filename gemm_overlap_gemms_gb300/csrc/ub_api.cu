@@ -181,7 +181,7 @@ int32_t *status_of(ub_handle *h) { return reinterpret_cast<int32_t *>(abort_of(h
 uint32_t *gather_counters_of(ub_handle *h) { return abort_of(h) + 8; }  // UB_MAX_TP words
 int join_words(const ub_handle *h) { return ubk::DECODE_COUNTERS * ubk::DECODE_CTAS_PER_SM * h->sm_count; }
 // Two tickets and the counters of split items of the prompt attention, behind them.
-constexpr int kPromptWords = 2 + 4 * ubk::PROMPT_SLOTS / 2;
+constexpr int kPromptWords = 2 + ubk::PROMPT_SLOTS;
 uint32_t *join_counters_of(ub_handle *h) { return gather_counters_of(h) + UB_MAX_TP; }
 
 // Makes the handle's device current for the duration of a call.

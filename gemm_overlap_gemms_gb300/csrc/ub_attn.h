@@ -29,7 +29,7 @@ struct HandleCall {
     uint32_t *join_counters; // of the decode attention
     int join_words;
     uint32_t *tickets;       // two words, zero between calls
-    uint32_t *piece_counters; // of the prompt attention's split items: 4 per item, zero between calls
+    uint32_t *piece_counters; // of the prompt attention's split items: PROMPT_SLOTS words
     float *ws_rows;          // PROMPT_SLOTS * 512
 
 };
@@ -120,7 +120,8 @@ struct PromptParams {
     uint32_t *tickets;       // work items drawn, CTAs done; zero between calls
     float *ws;               // parts of items split over their keys: `slots` of 256 rows
     float *ws_rows;          // their rows' maxima and sums: 512 per slot
-    uint32_t *counters;      // 4 words per split item, zero between calls
+    uint32_t *counters;      // of split items: PROMPT_SLOTS / 2 counts, zero between calls, then as many
+                             // that are never reset
     int slots;
     uint32_t *abort_word;
     uint64_t timeout_ns;
@@ -128,6 +129,7 @@ struct PromptParams {
     int pdl;
 };
 constexpr int PROMPT_SLOTS = 608;        // parts of split items, at most (half of it for heads of 128)
+constexpr int PROMPT_WHOLE_KEYS = 1408;  // items of no more keys are never split
 constexpr int PROMPT_ROWS = 128;         // rows (tokens x packed heads) of one q tile, two per CTA
 constexpr int PROMPT_KEYS = 128;         // keys of one tile
 cudaError_t launch_attn_prompt(const PromptParams &p, int grid, cudaStream_t s);

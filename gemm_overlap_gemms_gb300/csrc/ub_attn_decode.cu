@@ -217,10 +217,12 @@ __device__ __forceinline__ Share share_of(const SeqBatch &b, int lane, int heads
     const int own = lane < b.n_seqs ? tiles_of(clamped_len(b, lane)) : 0;
     int most;
     const I total = total_tiles<I>(b, lane, own, &most) * heads;
-    // Few short items: one CTA each. Else equal shares, of at least MIN_TILES tiles.
+    // Few short items: one CTA each. Else equal shares, of at least MIN_TILES tiles, or one CTA
+    // per item where those are shorter (355 items of one tile: 8.7 against 18.4 us).
     const int64_t n_items = static_cast<int64_t>(b.n_seqs) * heads;
     const bool whole_items = most <= WHOLE_TILES && n_items <= grid;
     I ctas = whole_items ? static_cast<I>(n_items) : total / MIN_TILES;
+    if (!whole_items && ctas < n_items) ctas = n_items < total ? static_cast<I>(n_items) : total;
     ctas = ctas < 1 ? 1 : (ctas > grid ? grid : ctas);
     if (cta >= ctas) return s;
     const I base = static_cast<I>(quotient(total, ctas));

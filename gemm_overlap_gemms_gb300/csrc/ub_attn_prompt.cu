@@ -37,6 +37,7 @@
 // tokens in four sequences, 8 heads each way: 43 us, of which the 24 key tiles of the longest
 // item take 36). Heads of 64: half the MMAs, the same softmax: 2440 cycles a step.
 #include <cuda_bf16.h>
+#include <limits.h>
 
 #include "ub_attn.h"
 #include "ub_device.cuh"
@@ -382,33 +383,35 @@ struct Schedule {
 };
 
 // Few rows over many keys (a call of fewer items than CTAs): items of more than `limit` key
-// tiles are cut into `pieces` pieces each, so that every CTA has work; limit is a CTA's even
-// share of the call (at least MIN_PIECE tiles), or what the workspace's slots allow. With
-// more items than CTAs nothing is split: joining costs more than an uneven end (measured: 256
-// rows of parts are joined in 13 us; 8152 packed tokens, whose longest items are 1.3 even
-// shares, took 61 us split in halves against 49 us whole).
+// tiles are cut into `pieces` pieces each, as even as the number of CTAs allows, which is one
+// piece or whole item for each: the pieces' CTAs then join their item together. With more
+// items than CTAs nothing is split, nor where no item has more than MIN_SPLIT key tiles: the
+// join takes about 6 us, a key tile 1.1 (four chunks of 16 tokens, 12 query and 4 key/value
+// heads of 128, split against whole: 1280 keys 21.2 and 18.2 us, 1536 keys 20.3 and 20.5, 2048
+// keys 21.9 and 25.1, 4096 keys 28.4 and 44.0).
 struct Plan {
     int pieces;          // 1: nothing is split
     uint32_t split_end;  // ranks [0, split_end): pieces of the split items, item by item
     uint32_t total;      // ... then the whole items
     int n_split;         // token tiles (of each unit) that are split
 };
-constexpr int MIN_PIECE = 8;
+constexpr int MIN_SPLIT = PROMPT_WHOLE_KEYS / PROMPT_KEYS, MIN_PIECE = 5;
 __device__ Plan plan_of(const Schedule &sc, int units, int ctas, int slots)
 {
     Plan pl{1, 0u, static_cast<uint32_t>(sc.tiles) * units, 0};
-    if (pl.total >= static_cast<uint32_t>(ctas) || sc.cmax <= MIN_PIECE) return pl;
+    if (pl.total >= static_cast<uint32_t>(ctas) || sc.cmax <= MIN_SPLIT) return pl;
+    // 32 limits at once, from an even share up; of those that give no more pieces than there
+    // are CTAs and slots, the one of the shortest longest piece.
     int limit = static_cast<int>(sc.work() * units / ctas) + 1;
     limit = limit < MIN_PIECE ? MIN_PIECE : limit;
-    // 32 limits at once; the smallest whose pieces fit the slots.
-    limit += static_cast<int>(static_cast<uint32_t>(limit) * static_cast<uint32_t>(sc.lane) / 4u);
-    const int n = sc.counts(limit + 1);
-    int pieces = (sc.cmax + limit - 1) / limit;
-    pieces = pieces < limit ? pieces : limit;  // none of a split item's is empty
-    const bool fits = limit < sc.cmax && static_cast<float>(n) * units * pieces <= slots;
-    const uint32_t good = __ballot_sync(0xffffffffu, fits);
-    if (good == 0u) return pl;
-    const int pick = __ffs(static_cast<int>(good)) - 1;
+    limit += static_cast<int>(static_cast<uint32_t>(limit) * static_cast<uint32_t>(sc.lane) / 8u);
+    const int n = sc.counts(limit + 1), pieces = (sc.cmax + limit - 1) / limit;
+    const float split = static_cast<float>(n) * units * pieces;
+    const bool fits = limit < sc.cmax && split <= slots && split + static_cast<float>(sc.tiles - n) * units <= ctas;
+    const int longest = (sc.cmax + pieces - 1) / pieces;
+    const int best = __reduce_min_sync(0xffffffffu, fits ? longest : INT_MAX);
+    if (best == INT_MAX) return pl;
+    const int pick = __ffs(static_cast<int>(__ballot_sync(0xffffffffu, fits && longest == best))) - 1;
     pl.pieces = __shfl_sync(0xffffffffu, pieces, pick);
     pl.n_split = __shfl_sync(0xffffffffu, n, pick);
     pl.split_end = static_cast<uint32_t>(pl.n_split * units * pl.pieces);
@@ -460,11 +463,12 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
     const uint32_t misc = b0 + 16 * NST + 8 * DONE;
     const uint32_t q_full = misc, q_empty = misc + 16, s_full = misc + 32, p_full = misc + 48, p_part = misc + 152, o_empty = misc + 64,
                    l_full = misc + 80, l_empty = misc + 96, o_full = misc + 112, drain = misc + 128, want = misc + 144,
-                   it_full = misc + 168, it_empty = it_full + 8 * ITEMS;
-    Item *items = reinterpret_cast<Item *>(reinterpret_cast<uint8_t *>(bars) + 16 * NST + 8 * DONE + 168 + 16 * ITEMS);
+                   parts_done = misc + 168, join_go = misc + 176,
+                   it_full = misc + 184, it_empty = it_full + 8 * ITEMS;
+    Item *items = reinterpret_cast<Item *>(reinterpret_cast<uint8_t *>(bars) + 16 * NST + 8 * DONE + 184 + 16 * ITEMS);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(items + ITEMS);
     volatile uint32_t *turn = tmem_slot + 1;     // steps that the issuer of each q tile has done
-    static_assert(16 * NST + 8 * DONE + 168 + 16 * ITEMS + sizeof(Item) * ITEMS + 12 <= 768, "barrier area");
+    static_assert(16 * NST + 8 * DONE + 184 + 16 * ITEMS + sizeof(Item) * ITEMS + 12 <= 768, "barrier area");
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     if ((sm_q & 1023u) != 0u) {  // the swizzled tiles need what the declaration asks for
@@ -491,6 +495,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
         mbar_init(drain, 1);
         mbar_init(drain + 8, 1);
         mbar_init(want, 1);
+        mbar_init(parts_done, 4);
+        mbar_init(join_go, 1);
         turn[0] = turn[1] = 0;
         for (int i = 0; i < ITEMS; ++i) {
             mbar_init(it_full + 8 * i, 1);
@@ -616,21 +622,115 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
             sm_max[i * 128 + row] = m;
             arrive(l_full + 8 * i);
         }
+        // A split item is the only one of its CTA and of the CTAs of its other pieces. When all
+        // pieces' parts are there, each CTA joins a share: 16 columns of 128 rows at a time.
+        it = items[0];
+        if (it.slot >= 0 && alive) {
+            if (warp == 0) {
+                // a count of the item's pieces, and one, never reset, of how often all have come
+                uint32_t *counter = p.counters + it.slot / it.pieces, *times = counter + PROMPT_SLOTS / 2;
+                if (wait(parts_done, 0) && lane == 0) {
+                    const uint32_t before = *static_cast<volatile uint32_t *>(times);
+                    uint32_t come;
+                    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(come) : "l"(counter) : "memory");
+                    if (come == static_cast<uint32_t>(it.pieces - 1)) {
+                        *counter = 0u;                 // zero again for the next call
+                        st_release_u32(times, before + 1u);
+                    } else {
+                        WaitClock clk;
+                        for (uint32_t n = 1; alive; ++n) {
+                            uint32_t v;
+                            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(times) : "memory");
+                            if (v != before) break;
+                            if ((n & 15u) == 0 && !clk.ok(wc)) alive = false;
+                        }
+                    }
+                }
+                alive = __all_sync(0xffffffffu, alive) != 0;
+                arrive(join_go);
+            }
+            if (alive && wait(join_go, 0)) {
+                const Range2 r = ranges(it, tpt);
+                const int per = D / 16;                // units of a q tile
+                for (int u = it.piece + it.pieces * i; u < 2 * per; u += 2 * it.pieces) {
+                    const int t = u / per, c = (u - t * per) * 16;
+                    const int rows_tok = t == 0 ? r.tok[0] : r.tok[1], lim = t == 0 ? r.lim[0] : r.lim[1];
+                    if (rows_tok == 0) continue;
+                    const int n = (lim + PROMPT_KEYS - 1) / PROMPT_KEYS;  // key tiles that q tile t reaches
+                    const float *rows = p.ws_rows + static_cast<int64_t>(it.slot) * 512 + t * 128 + row;
+                    const float4 *cols = reinterpret_cast<const float4 *>(p.ws) + static_cast<int64_t>(it.slot) * (64 * D) +
+                                         c / 4 * 256 + t * 128 + row;
+                    float M = -INFINITY, L = 0.f, acc[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+                    for (int q0 = 0; q0 < it.pieces; q0 += 4) {
+                        float4 v[4][4];
+                        float m[4], l[4], top = M;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int b = piece_begin(it.n, q0 + q, it.pieces);
+                            m[q] = -INFINITY;          // no such part, or no key of this q tile in it
+                            l[q] = 0.f;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) v[q][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (q0 + q >= it.pieces || b >= n || piece_begin(it.n, q0 + q + 1, it.pieces) == b) continue;
+                            m[q] = __ldcg(rows + (q0 + q) * 512);
+                            l[q] = __ldcg(rows + (q0 + q) * 512 + 256);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) v[q][e] = __ldcg(cols + static_cast<int64_t>(q0 + q) * (64 * D) + e * 256);
+                        }
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) top = fmaxf(top, m[q]);
+                        const float ref = top == -INFINITY ? 0.f : top, f0 = ex2((M - ref) * sl);
+                        M = top;
+                        L *= f0;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) acc[e] *= f0;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const float f = ex2((m[q] - ref) * sl);
+                            L += l[q] * f;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                acc[4 * e] += v[q][e].x * f;
+                                acc[4 * e + 1] += v[q][e].y * f;
+                                acc[4 * e + 2] += v[q][e].z * f;
+                                acc[4 * e + 3] += v[q][e].w * f;
+                            }
+                        }
+                    }
+                    const int token = t * tpt + (row >> p.pack_shift);
+                    const int h = (it.unit << p.pack_shift) + (row & (pack - 1));
+                    if (token >= it.ntok) continue;
+                    const float inv = 1.f / L;
+                    __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + (it.row0 + token) * p.o_row + h * p.o_head + c;
+#pragma unroll
+                    for (int e = 0; e < 16; e += 8) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            w[x] = L == 0.f ? 0u
+                                            : pack_bf16x2(__float_as_uint(acc[e + 2 * x] * inv), __float_as_uint(acc[e + 2 * x + 1] * inv));
+                        *reinterpret_cast<uint4 *>(dst + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    if (p.lse && c == 0)
+                        p.lse[static_cast<int64_t>(it.row0 + token) * p.heads + h] =
+                            L > 0.f ? M * p.scale + logf(L) : (L == 0.f ? -INFINITY : L);
+                }
+            }
+        }
     } else if (warp < 12) {
         // ------------------------------------------------------------ epilogue
         fewer_registers<EPILOGUE_REGS>();
         const int row = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const float sl = p.scale * 1.4426950408889634f;
         uint32_t n_o[2] = {0, 0};
         Item it;
         for (uint32_t k = 0; next_item(k, it); ++k) {
             const Range2 r = ranges(it, tpt);
             // A split item's part: [columns / 4][256 rows][4] fp32 and the rows' maxima and sums.
-            auto part_o = [&](int piece, int i) {
-                return reinterpret_cast<float4 *>(p.ws) + static_cast<int64_t>(it.slot + piece) * (64 * D) + i * 128 + row;
-            };
-            auto part_m = [&](int piece, int i) { return p.ws_rows + static_cast<int64_t>(it.slot + piece) * 512 + i * 128 + row; };
+            float4 *part_o = reinterpret_cast<float4 *>(p.ws) + static_cast<int64_t>(it.slot + it.piece) * (64 * D) + row;
+            float *part_m = p.ws_rows + static_cast<int64_t>(it.slot + it.piece) * 512 + row;
             // One row's 32 columns from c on, times f, or zeros.
             auto store = [&](int i, int c, const float *v, float f, bool none) {
                 const int token = i * tpt + (row >> p.pack_shift);
@@ -678,7 +778,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                     if (it.slot < 0) {
                         store(i, c, v, inv, l == 0.f);
                     } else {
-                        float4 *to = part_o(it.piece, i) + c / 4 * 256;
+                        float4 *to = part_o + i * 128 + c / 4 * 256;
 #pragma unroll
                         for (int u = 0; u < 32; u += 4) to[u / 4 * 256] = make_float4(v[u], v[u + 1], v[u + 2], v[u + 3]);
                     }
@@ -688,60 +788,13 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                 if (it.slot < 0) {
                     store_lse(i, m, l);
                 } else {
-                    part_m(it.piece, i)[0] = m;
-                    part_m(it.piece, i)[256] = l;
+                    part_m[i * 128] = m;
+                    part_m[i * 128 + 256] = l;
                 }
             }
             if (!alive) break;
             if (it.slot < 0) continue;
-            // The last piece to come joins all, each warp its own rows: a counter per item and warp.
-            // (Bound by latency: 32 columns of one part in flight per row.)
-            __syncwarp();
-            uint32_t come = 0;
-            if (lane == 0) {
-                uint32_t *counter = p.counters + (it.slot / it.pieces) * 4 + (warp & 3);
-                asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(come) : "l"(counter) : "memory");
-                if (come == static_cast<uint32_t>(it.pieces - 1)) *counter = 0u;  // zero again for the next call
-            }
-            come = __shfl_sync(0xffffffffu, come, 0);
-            __syncwarp();
-            if (come != static_cast<uint32_t>(it.pieces - 1)) continue;
-            const int level = it.n;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (r.tok[i] == 0) continue;
-                // Pieces that begin before this q tile's last key have a part of it.
-                const int n = (r.lim[i] + PROMPT_KEYS - 1) / PROMPT_KEYS;
-                int parts = 0;
-                while (parts < it.pieces && piece_begin(level, parts, it.pieces) < n) ++parts;
-                float M = -INFINITY, L = 0.f;
-                for (int q = 0; q < parts; ++q) M = fmaxf(M, __ldcg(part_m(q, i)));
-                const float ref = M == -INFINITY ? 0.f : M;
-                for (int q = 0; q < parts; ++q) L += __ldcg(part_m(q, i) + 256) * ex2((__ldcg(part_m(q, i)) - ref) * sl);
-                const float inv = 1.f / L;
-#pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    float acc[32];
-#pragma unroll
-                    for (int u = 0; u < 32; ++u) acc[u] = 0.f;
-#pragma unroll 1
-                    for (int q = 0; q < parts; ++q) {
-                        const float f = ex2((__ldcg(part_m(q, i)) - ref) * sl);
-                        float4 v[8];
-#pragma unroll
-                        for (int u = 0; u < 8; ++u) v[u] = __ldcg(part_o(q, i) + (c / 4 + u) * 256);
-#pragma unroll
-                        for (int u = 0; u < 8; ++u) {
-                            acc[4 * u] += v[u].x * f;
-                            acc[4 * u + 1] += v[u].y * f;
-                            acc[4 * u + 2] += v[u].z * f;
-                            acc[4 * u + 3] += v[u].w * f;
-                        }
-                    }
-                    store(i, c, acc, inv, L == 0.f);
-                }
-                store_lse(i, M, L);
-            }
+            arrive(parts_done);                        // the softmax warps join it
         }
     } else {
       // the four single warps

@@ -76,6 +76,14 @@ def test_decode_lengths(buf, kv):
     run_decode(buf, b, 8, 128)
 
 
+@pytest.mark.parametrize("heads,kv_heads,kv", [(5, 5, [1 + 7 * i % 30 for i in range(71)]), (8, 8, [17 + 13 * i % 53 for i in range(49)]),
+                                               (12, 4, [0, 5, 0, 300, 33, 0] * 13), (12, 1, [2900 - i for i in range(15)])])
+def test_decode_many_short_items(buf, heads, kv_heads, kv):
+    """A CTA for about every short item, several CTAs for the longer ones."""
+    b = ref.Batch([1] * len(kv), kv, page=64, kv_heads=kv_heads, dim=128, seed=heads, fill=float("nan"))
+    run_decode(buf, b, heads, 128)
+
+
 def test_decode_is_deterministic_and_leaves_its_counters_clean(buf):
     b = ref.Batch([1] * 3, [30000, 5000, 11], page=32, kv_heads=2, dim=64, seed=5)
     q, first = run_decode(buf, b, 8, 64)
@@ -313,6 +321,25 @@ def test_prompt_chunks_over_long_caches(buf, new, kv, heads, kv_heads, dim):
     check_prompt(b, q, lambda s: (b.rows(b.k_cache, s), b.rows(b.v_cache, s)), out, lse)
     for _ in range(5):
         assert torch.equal(buf.attn_prompt_paged(q, b.k_cache, b.v_cache, b.starts, b.lens, b.table)[:sum(new)], out[:sum(new)])
+
+
+def test_prompt_split_plans_one_after_another(buf):
+    """Calls that split differently, back to back, on the same workspace and counters."""
+    calls = []
+    for i, (new, kv) in enumerate([([64, 64], [2000, 1999]), ([5], [30000]), ([300, 1], [1409, 1500]), ([17] * 3, [6000, 0, 40])]):
+        b = ref.Batch(new, kv, page=64, kv_heads=2, dim=(64, 128)[i % 2], seed=i, fill=float("nan"))
+        q = b.randn(b.T, 4, b.k_cache.shape[3], std=1.5)
+        out = sentinel(q.shape)
+        calls.append((b, q, out))
+    for _ in range(3):
+        for b, q, out in calls:
+            buf.set_active_shape([b.T, 256])
+            buf.attn_prompt_paged(q, b.k_cache, b.v_cache, b.starts, b.lens, b.table, out=out)
+    ok(buf)
+    for b, q, out in calls:
+        buf.set_active_shape([b.T, 256])
+        _, lse = buf.attn_prompt_paged(q, b.k_cache, b.v_cache, b.starts, b.lens, b.table, out=out, lse=True)
+        check_prompt(b, q, lambda s: (b.rows(b.k_cache, s), b.rows(b.v_cache, s)), out, lse)
 
 
 def test_prompt_packed_split(buf):
