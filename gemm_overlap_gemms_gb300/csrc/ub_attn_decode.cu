@@ -35,7 +35,8 @@
 // GB): 350 us, 6.8 TB/s, HBM-bound (a ring of 192 KB: 360 us, SMs drift further apart; 64 KB:
 // 414 us). One sequence of 131071 keys, one key/value head (67 MB): 18.5 us, of which 10 us
 // stream; 3-4 us pass before the first tile lands, 5 us after the last (parts written, counted,
-// joined). 64 sequences, 127938 keys, 2 key/value heads (131 MB): 32 us, 18 of them streaming.
+// joined). 64 sequences, 127938 keys, 2 key/value heads (131 MB): 31 us, 18 of them streaming.
+// 15 sequences of 2900 keys, one key/value head, 8 query heads (22 MB, 10 parts each): 12.4 us.
 // Four sequences of 300 keys, 8 heads: 8 us a call, bound by the host's side of it.
 #include <cuda_bf16.h>
 
@@ -49,7 +50,9 @@ namespace {
 constexpr int KT = DECODE_KEYS;
 constexpr int WARPS = 4;
 constexpr int DEC_THREADS = 32 * 2 * WARPS;
-constexpr int JOIN_MOST = 8;             // parts that one CTA joins
+// Parts that one CTA joins: 2, 4 and 8 are within 1 us of one another at 2 to 10 parts (16
+// sequences of 500 to 1500 keys, 8 heads: 15.9, 14.8 and 15.6 us).
+constexpr int JOIN_MOST = 4;
 constexpr int MIN_TILES = 8;
 constexpr int WHOLE_TILES = 32;
 
@@ -667,19 +670,23 @@ __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
                 }
                 alive = __all_sync(0xffffffffu, alive);
             }
-            // Units of this CTA: one warp each, a lane adding every 32nd part.
+            // Units of this CTA: `width` lanes each, as few as have all parts in flight at once.
+            constexpr int U = 5;               // parts in flight per lane
+            const int width_shift = parts <= 4 * U ? 2 : (parts <= 8 * U ? 3 : (parts <= 16 * U ? 4 : 5));
+            const int width = 1 << width_shift, at_once = (32 * WARPS) >> width_shift;
             const int per = (units + parts - 1) / parts, i_cta = static_cast<int>(blockIdx.x) - a;
-            for (int u = i_cta * per + warp; u < units && u < (i_cta + 1) * per && alive; u += WARPS) {
+            const int end = (i_cta + 1) * per < units ? (i_cta + 1) * per : units;
+            for (int u0 = i_cta * per; u0 < end && alive; u0 += at_once) {
+                const int u = u0 + (tid >> width_shift);
                 const int hh = u / (D / 4), d = (u - hh * (D / 4)) * 4;
                 float M = -INFINITY, L = 0.f;
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                constexpr int U = 5;           // parts in flight per lane
-                for (int i0 = lane; i0 < parts; i0 += 32 * U) {
+                for (int i0 = lane & (width - 1); i0 < parts && u < end; i0 += width * U) {
                     float4 v[U];
                     float m[U], l[U], top = M;
 #pragma unroll
                     for (int k = 0; k < U; ++k) {
-                        const int i = i0 + 32 * k;
+                        const int i = i0 + width * k;
                         m[k] = -INFINITY;
                         l[k] = 0.f;
                         v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -709,23 +716,21 @@ __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
                     }
                 }
                 float top = M;
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                for (int o = width >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                 const float fw = ex2((M - (top == -INFINITY ? 0.f : top)) * sl);
                 L *= fw;
                 acc.x *= fw;
                 acc.y *= fw;
                 acc.z *= fw;
                 acc.w *= fw;
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
+                for (int o = width >> 1; o > 0; o >>= 1) {
                     L += __shfl_xor_sync(0xffffffffu, L, o);
                     acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o);
                     acc.y += __shfl_xor_sync(0xffffffffu, acc.y, o);
                     acc.z += __shfl_xor_sync(0xffffffffu, acc.z, o);
                     acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
                 }
-                if (lane == 0) finish(it.seq, it.h0, hh, d, acc, top, L);
+                if ((lane & (width - 1)) == 0 && u < end) finish(it.seq, it.h0, hh, d, acc, top, L);
             }
         }
     }
