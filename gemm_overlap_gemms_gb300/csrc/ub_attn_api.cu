@@ -293,7 +293,7 @@ int ub_attn_prompt(ub_handle_t h, const ub_attn_t *in, void *stream)
     p.pdl = c.pdl;
     // One persistent CTA per SM, no more than there can be work items, unless they may have to
     // be split over their keys.
-    const int64_t tokens = 2 * PROMPT_ROWS / pack;
+    const int64_t tokens = PROMPT_ROWS / pack;
     const int64_t most = (T / tokens + (a.n_seqs < T ? a.n_seqs : T)) * p.units;
     const int64_t keys = paged ? a.table_width * a.page_size : T;
     const int64_t grid = most < c.sms && keys <= PROMPT_WHOLE_KEYS ? most : c.sms;

@@ -9,7 +9,9 @@
 //
 // A work item is 256 rows, two q tiles of 128: consecutive tokens of one sequence, and,
 // where query heads share a key/value head, a power of two of those heads per token (row =
-// token * pack + head). Per 128 keys and q tile the tensor core computes S = Q K^T (128 x
+// token * pack + head). Where items of 128 rows, one q tile, are no more than the CTAs, they
+// are the items (882 tokens, 12 heads: 18 against 20 us; in calls of more items the second
+// tile runs in the first one's pauses and saves reading keys and values twice). Per 128 keys and q tile the tensor core computes S = Q K^T (128 x
 // 128, both operands from shared memory) and O += P V (P from TMEM, V read MN-major); the
 // softmax in between is per TMEM lane, one thread per row, without shuffles.
 //
@@ -28,13 +30,13 @@
 // to 16 keys (N of the first product, K of the second).
 //
 // What bounds it (GB300): a step of 128 keys for both q tiles is 2048 cycles of MMAs (heads
-// of 128) against 2420 measured in a long sequence; the difference is the chain S -> softmax
+// of 128) against 2420 measured in a long sequence (one q tile alone: 2200); the difference is the chain S -> softmax
 // (1150 cycles for a tile alone, 870 of them its instructions; exp2 runs at 4 cycles per warp
 // and SM quarter) -> P V -> next S, which the other tile's MMAs cover only in part. TMEM holds
-// no third tile. One sequence of 16384 tokens, 8 query heads, 2 key/value heads: 333 us, 1650
+// no third tile. One sequence of 16384 tokens, 8 query heads, 2 key/value heads: 330 us, 1660
 // TFLOP/s; tensor pipe active in 80 % of the cycles. Shorter prompts: the first item is known
-// 1.6 us after the grid ahead has finished, and the call ends with its longest item (8152
-// tokens in four sequences, 8 heads each way: 43 us, of which the 24 key tiles of the longest
+// 1.6 us after the grid ahead has finished, and the call ends with its longest item (8037
+// tokens in four sequences, 8 heads each way: 42 us, of which the 24 key tiles of the longest
 // item take 36). Heads of 64: half the MMAs, the same softmax: 2440 cycles a step.
 #include <cuda_bf16.h>
 #include <limits.h>
@@ -980,7 +982,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
         // The first item is looked up twice, at first in a call of made-up numbers and before the
         // grid ahead has finished: the code is in the instruction cache by the time that this
         // call's numbers may be read, and everything else waits for the first item.
-        Schedule sched{p, lane, 8 - p.pack_shift, 1, 0, 0, {0, lane == 0 ? 65536 : 0, lane == 0 ? 65536 : 0, 0}};
+        Schedule sched{p, lane, 0, 1, 0, 0, {0, lane == 0 ? 65536 : 0, lane == 0 ? 65536 : 0, 0}};
         Plan plan;
         Item it;
 #pragma unroll 1
@@ -991,7 +993,12 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                 sched.n_seqs = p.b.n_seqs;
                 sched.own = lane < p.b.n_seqs ? seq_info(p, lane) : SeqInfo{0, 0, 0, 0};
             }
-            sched.measure();
+            // Items of one q tile where those are no more than the CTAs, of two elsewhere.
+            sched.shift = 7 - p.pack_shift;
+            for (;; ++sched.shift) {
+                sched.measure();
+                if (static_cast<uint32_t>(sched.tiles) * p.units <= gridDim.x || sched.shift == 8 - p.pack_shift) break;
+            }
             plan = plan_of(sched, p.units, gridDim.x, p.slots);
             it = kNoItem;
             if (blockIdx.x < plan.total) it = item_of(sched, plan, p.units, blockIdx.x);
