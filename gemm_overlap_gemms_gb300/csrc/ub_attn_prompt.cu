@@ -30,14 +30,14 @@
 // to 16 keys (N of the first product, K of the second).
 //
 // What bounds it (GB300): a step of 128 keys for both q tiles is 2048 cycles of MMAs (heads
-// of 128) against 2420 measured in a long sequence (one q tile alone: 2200); the difference is the chain S -> softmax
-// (1150 cycles for a tile alone, 870 of them its instructions; exp2 runs at 4 cycles per warp
-// and SM quarter) -> P V -> next S, which the other tile's MMAs cover only in part. TMEM holds
-// no third tile. One sequence of 16384 tokens, 8 query heads, 2 key/value heads: 330 us, 1660
-// TFLOP/s; tensor pipe active in 80 % of the cycles. Shorter prompts: the first item is known
-// 1.6 us after the grid ahead has finished, and the call ends with its longest item (8037
-// tokens in four sequences, 8 heads each way: 42 us, of which the 24 key tiles of the longest
-// item take 36). Heads of 64: half the MMAs, the same softmax: 2440 cycles a step.
+// of 128) against 2420 measured in a long sequence (2200 for one q tile alone); the difference
+// is the chain S -> softmax (1150 cycles, 870 of them its instructions; exp2 runs at 4 cycles
+// per warp and SM quarter) -> P V -> next S, which the other tile's MMAs cover only in part.
+// TMEM holds no third tile. One sequence of 16384 tokens, 8 query heads, 2 key/value heads:
+// 330 us, 1660 TFLOP/s; tensor pipe active in 80 % of the cycles. Shorter prompts: the first
+// item is known 1.6 us after the grid ahead has finished, and the call ends with its longest
+// item (8037 tokens in four sequences, 8 heads each way: 42 us, of which the 24 key tiles of
+// the longest item take 36). Heads of 64: half the MMAs, the same softmax: 2440 cycles a step.
 #include <cuda_bf16.h>
 #include <limits.h>
 
