@@ -90,7 +90,8 @@ struct DecodeParams {
     int many_tiles;          // the table could hold 2^31 tiles or more over all heads
     float scale;
     float *ws;
-    uint32_t *counters;      // DECODE_COUNTERS words per CTA
+    uint32_t *counters;      // parts that have come, per item: zero between calls
+    uint32_t *times;         // how often all have come: never reset, so at the same place in every call
     uint32_t *abort_word;
     uint64_t timeout_ns;
     uint32_t epoch;
@@ -102,7 +103,7 @@ constexpr int DECODE_KEYS = 32;          // keys of one tile
 constexpr int DECODE_CTAS_PER_SM = 1;
 constexpr int DECODE_HEADS = 16;         // query heads of one pass over a key/value head, at most
 constexpr int DECODE_SLOTS = 2;          // workspace slots per CTA
-constexpr int DECODE_COUNTERS = 2;       // join counters per CTA
+constexpr int DECODE_COUNTERS = 2;       // words per CTA: `counters` and `times`
 __host__ __device__ constexpr int decode_slot_floats(int head_dim) { return DECODE_HEADS * (head_dim + 2); }
 
 struct PromptParams {

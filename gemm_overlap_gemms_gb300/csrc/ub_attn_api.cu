@@ -342,6 +342,7 @@ int ub_attn_decode(ub_handle_t h, const ub_attn_t *in, void *stream)
     p.scale = a.scale;
     p.ws = c.ws;
     p.counters = c.join_counters;
+    p.times = c.join_counters + c.join_words / DECODE_COUNTERS;
     p.abort_word = c.abort_word;
     p.timeout_ns = c.timeout_ns;
     p.epoch = c.epoch;

@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
 #pragma unroll
         for (int which = 0; which < 2; ++which)
             if (pend[which].tiles != 0)
-                before[which] = *static_cast<volatile uint32_t *>(p.counters + G + split.owner(pend[which].item0));
+                before[which] = *static_cast<volatile uint32_t *>(p.times + split.owner(pend[which].item0));
         bar_compute();                  // this CTA's parts are written
         if (warp < 2 && lane == 0) {    // a warp for each
             const Pending it = warp == 0 ? pend[0] : pend[1];
@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
                 const bool last = static_cast<int>(arrive_acq_rel(p.counters + a)) == parts - 1;
                 if (last) {
                     p.counters[a] = 0u;  // zero again for the next call
-                    if (parts > JOIN_MOST) st_release_u32(p.counters + G + a, (warp == 0 ? before[0] : before[1]) + 1u);
+                    if (parts > JOIN_MOST) st_release_u32(p.times + a, (warp == 0 ? before[0] : before[1]) + 1u);
                 }
                 sm_last[warp] = last ? 1 : 0;
             }
@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
             const bool last = sm_last[which] != 0;
             const int a = split.owner(it.item0), z = split.owner(it.item0 + it.tiles - 1);
             const int parts = z - a + 1;
-            const uint32_t *times = p.counters + G + a;
+            const uint32_t *times = p.times + a;
             // part i's slot: 1 for the CTA in which the item begins, 0 for the others
             auto part = [&](int i) { return slot_of(a + i, i == 0 ? 1 : 0); };
             const int units = it.g * (D / 4);  // of four outputs

@@ -84,6 +84,22 @@ def test_decode_many_short_items(buf, heads, kv_heads, kv):
     run_decode(buf, b, heads, 128)
 
 
+def test_decode_grids_of_different_sizes_share_the_counters(buf):
+    """A call's grid follows the table's width; what one call leaves counted must not meet another's."""
+    long = ref.Batch([1] * 20, [700 + 97 * i % 1900 for i in range(20)], page=64, kv_heads=2, dim=128, seed=1, fill=float("nan"))
+    buf.set_active_shape([20, 256])
+    ql = long.randn(20, 8, 128)
+    before = buf.attn_decode(ql, long.k_cache, long.v_cache, long.lens, long.table)
+    for pages in range(13, 76):
+        b = ref.Batch([1], [64 * pages], page=64, kv_heads=1, dim=64, seed=pages, fill=float("nan"))
+        buf.set_active_shape([1, 256])
+        buf.attn_decode(b.randn(1, 4, 64), b.k_cache, b.v_cache, b.lens, b.table)
+    buf.set_active_shape([20, 256])
+    after = buf.attn_decode(ql, long.k_cache, long.v_cache, long.lens, long.table)
+    ok(buf)
+    assert torch.equal(before, after)
+
+
 def test_decode_is_deterministic_and_leaves_its_counters_clean(buf):
     b = ref.Batch([1] * 3, [30000, 5000, 11], page=32, kv_heads=2, dim=64, seed=5)
     q, first = run_decode(buf, b, 8, 64)
