@@ -87,7 +87,7 @@ struct DecodeParams {
     int64_t q_row, q_head, o_row, o_head;
     int heads, kv_heads, head_dim, group;
     int head_blocks;         // blocks of up to 16 query heads per key/value head
-    int many_tiles;          // the table could hold 2^31 tiles or more over all heads
+    int many_tiles;          // the table could hold 2^31 units of work or more over all heads
     float scale;
     float *ws;
     uint32_t *counters;      // parts that have come, per item: zero between calls
@@ -99,6 +99,7 @@ struct DecodeParams {
     __host__ __device__ int32_t *status_word() const { return b.status; }
 };
 cudaError_t launch_attn_decode(const DecodeParams &p, int grid, cudaStream_t s);
+constexpr int DECODE_ITEM_COST = 12;     // tiles that the end of an item counts as in the split
 constexpr int DECODE_KEYS = 32;          // keys of one tile
 constexpr int DECODE_CTAS_PER_SM = 1;
 constexpr int DECODE_HEADS = 16;         // query heads of one pass over a key/value head, at most

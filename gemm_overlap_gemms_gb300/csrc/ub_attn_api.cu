@@ -350,7 +350,7 @@ int ub_attn_decode(ub_handle_t h, const ub_attn_t *in, void *stream)
     // As many CTAs as fit, and no more than there can be tiles.
     int64_t grid = static_cast<int64_t>(c.sms) * DECODE_CTAS_PER_SM;
     const int64_t most = ((a.table_width * a.page_size + DECODE_KEYS - 1) / DECODE_KEYS) * a.n_seqs * a.kv_heads * p.head_blocks;
-    p.many_tiles = most > INT32_MAX ? 1 : 0;
+    p.many_tiles = most > INT32_MAX / (1 + DECODE_ITEM_COST) ? 1 : 0;
     if (grid > most) grid = most;
     if (DECODE_COUNTERS * grid > c.join_words || DECODE_SLOTS * grid * decode_slot_floats(a.head_dim) > static_cast<int64_t>(c.ws_floats))
         return fail_call(UB_ERR_ARG, "%s: workspace too small for %lld CTAs", fn, (long long)grid);

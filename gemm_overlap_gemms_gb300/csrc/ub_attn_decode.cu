@@ -18,10 +18,14 @@
 // Work split: the (sequence, head, 32-key tile) triples of the whole call are laid end to
 // end and every CTA takes an equal, contiguous range, found on the device from kv_lens. So
 // ragged lengths, one long sequence and many short ones all load every SM alike, without
-// the host knowing a length. The parts of an item that spans CTAs go to the workspace and are
-// joined in CTA order (deterministic) once a counter per item says that all are there: up to
-// JOIN_MOST parts by the CTA that comes last, more by all their CTAs, a share of the outputs
-// each, so that no CTA reads all of a long sequence's parts.
+// the host knowing a length. The end of an item (its warps' partials joined and written, the
+// next queries loaded) counts as 12 tiles, which also keeps many items whole: 64 sequences of
+// 100 to 600 keys, 8 key/value heads 22.8 us, counted as 4 tiles 23.9, as none 28.9; 128
+// sequences of 20 to 400 keys, 4 heads 18.4, 19.5 and 30.9 us (6 to 16 tiles: within 3 %).
+// The parts of an item that spans CTAs go to the workspace and are joined in CTA order
+// (deterministic) once a counter per item says that all are there: up to JOIN_MOST parts by
+// the CTA that comes last, more by all their CTAs, a share of the outputs each, so that no
+// CTA reads all of a long sequence's parts.
 //
 // A CTA is four loading and four computing warps, one CTA on an SM. The loading warps fill a
 // ring of 128 KB (a stage is one tile's keys and values) with TMA boxes of one page or one
@@ -32,12 +36,12 @@
 // memory at the end of an item, while the ring goes on filling.
 //
 // Measured (GB300): 128 sequences, 583272 keys, 32 query heads, 8 key/value heads of 128 (2.39
-// GB): 350 us, 6.8 TB/s, HBM-bound (a ring of 192 KB: 360 us, SMs drift further apart; 64 KB:
-// 414 us). One sequence of 131071 keys, one key/value head (67 MB): 18.5 us, of which 10 us
-// stream; 3-4 us pass before the first tile lands, 5 us after the last (parts written, counted,
-// joined). 64 sequences, 127938 keys, 2 key/value heads (131 MB): 31 us, 18 of them streaming.
-// 15 sequences of 2900 keys, one key/value head, 8 query heads (22 MB, 10 parts each): 12.4 us.
-// Four sequences of 300 keys, 8 heads: 8 us a call, bound by the host's side of it.
+// GB): 345 us, 6.9 TB/s, HBM-bound (a ring of 192 KB: 3 % slower, SMs drift further apart; 64
+// KB: 18 % slower). One sequence of 131071 keys, one key/value head (67 MB): 18.7 us, of which
+// 10 us stream; 3-4 us pass before the first tile lands, 5 us after the last (parts written,
+// counted, joined). 64 sequences, 127938 keys, 2 key/value heads (131 MB): 29 us, 18 of them
+// streaming. 15 sequences of 2900 keys, one key/value head, 8 query heads (22 MB, 10 parts
+// each): 10.4 us. Four sequences of 300 keys, 8 heads: 7.5 us a call, bound by the host's side.
 #include <cuda_bf16.h>
 
 #include "ub_attn.h"
@@ -50,10 +54,11 @@ namespace {
 constexpr int KT = DECODE_KEYS;
 constexpr int WARPS = 4;
 constexpr int DEC_THREADS = 32 * 2 * WARPS;
-// Parts that one CTA joins: 2, 4 and 8 are within 1 us of one another at 2 to 10 parts (16
-// sequences of 500 to 1500 keys, 8 heads: 15.9, 14.8 and 15.6 us).
-constexpr int JOIN_MOST = 4;
-constexpr int MIN_TILES = 8;
+// Parts that one CTA joins (30 sequences of 2750 keys, 5 parts each: 12.1 us, joined by all
+// their CTAs 15.0; 15 sequences, 10 parts each: 10.4, joined by one 11.2), and how many it has
+// in flight.
+constexpr int JOIN_MOST = 8, JOIN_STEP = 4;
+constexpr int MIN_TILES = 4;             // of a CTA, on average (one sequence of 2000 keys: 7.8 us; 16: 10.9 us)
 constexpr int WHOLE_TILES = 32;
 
 template <int D, int NT>
@@ -140,13 +145,18 @@ __device__ __forceinline__ int clamped_len(const SeqBatch &b, int seq)
 }
 __device__ __forceinline__ int tiles_of(int len) { return len > 0 ? (len + KT - 1) / KT : 1; }
 
+// What an item counts in the split: its tiles and its end, which costs a CTA about as long as
+// DECODE_ITEM_COST tiles.
+__device__ __forceinline__ int cost_of(int len) { return tiles_of(len) + DECODE_ITEM_COST; }
+
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
 {
     if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
     return a / b;
 }
 
-// The equal split of `total` tiles over `ctas`: CTA c's first tile, and the CTA of a tile.
+// The equal split of `total` units (tiles and ends of items) over `ctas`: CTA c's first unit,
+// and the CTA of a unit.
 struct Split {
     int64_t base, rem;
     __device__ __forceinline__ int64_t first(int64_t c) const { return c * base + (c < rem ? c : rem); }
@@ -165,28 +175,28 @@ __device__ __forceinline__ int64_t warp_sum(int64_t v)
 }
 __device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
 
-// Sum and maximum of the sequences' tiles (one warp). I: a type that holds the sum over all heads.
+// Sum and maximum of the sequences' costs (one warp). I: a type that holds the sum over all heads.
 template <typename I>
-__device__ __forceinline__ I total_tiles(const SeqBatch &b, int lane, int own, int *most)
+__device__ __forceinline__ I total_cost(const SeqBatch &b, int lane, int own, int *most)
 {
     I sum = own;
     int top = own;
     for (int i = lane + 32; i < b.n_seqs; i += 32) {
-        const int n = tiles_of(clamped_len(b, i));
+        const int n = cost_of(clamped_len(b, i));
         sum += n;
         top = n > top ? n : top;
     }
     *most = __reduce_max_sync(0xffffffffu, top);
     return warp_sum(sum);
 }
-// The sequence that holds per-head tile `tile` over all heads, and the tiles before it. own:
-// the tiles of sequence `lane` (0 past the last).
+// The sequence that holds unit `unit` of the call, and the units before it. own: the cost of
+// sequence `lane` (0 past the last).
 template <typename I>
-__device__ __forceinline__ void find_seq(const SeqBatch &b, int lane, int own, I tile, int heads, int *seq, I *before)
+__device__ __forceinline__ void find_seq(const SeqBatch &b, int lane, int own, I unit, int heads, int *seq, I *before)
 {
-    I seen = 0;  // tiles of the sequences before this batch of 32, over all heads
+    I seen = 0;  // units of the sequences before this batch of 32, over all heads
     for (int i0 = 0; i0 < b.n_seqs; i0 += 32) {
-        I mine = i0 == 0 ? own : (i0 + lane < b.n_seqs ? tiles_of(clamped_len(b, i0 + lane)) : 0);
+        I mine = i0 == 0 ? own : (i0 + lane < b.n_seqs ? cost_of(clamped_len(b, i0 + lane)) : 0);
         mine *= heads;
         I upto = mine;
 #pragma unroll
@@ -194,7 +204,7 @@ __device__ __forceinline__ void find_seq(const SeqBatch &b, int lane, int own, I
             const I x = __shfl_up_sync(0xffffffffu, upto, o);
             if (lane >= o) upto += x;
         }
-        const uint32_t past = __ballot_sync(0xffffffffu, seen + upto > tile);
+        const uint32_t past = __ballot_sync(0xffffffffu, seen + upto > unit);
         if (past != 0u) {
             const int l = __ffs(static_cast<int>(past)) - 1;
             *seq = i0 + l;
@@ -207,23 +217,23 @@ __device__ __forceinline__ void find_seq(const SeqBatch &b, int lane, int own, I
     *before = seen;
 }
 
-// What a CTA does: its first item and tile, and how many tiles it takes (0: nothing).
+// What a CTA does: its first item and tile, and how many units it takes (none: nothing).
 struct Share {
     Split split;
-    int64_t x, left;  // first tile of the whole call (not counted for whole items), tiles
+    int64_t x, left;  // first unit of the whole call (not counted for whole items), units
     int seq, head, t0;
 };
 template <typename I>
 __device__ __forceinline__ Share share_of(const SeqBatch &b, int lane, int heads, int cta, int grid)
 {
     Share s{{0, 0}, 0, 0, 0, 0, 0};
-    const int own = lane < b.n_seqs ? tiles_of(clamped_len(b, lane)) : 0;
+    const int own = lane < b.n_seqs ? cost_of(clamped_len(b, lane)) : 0;
     int most;
-    const I total = total_tiles<I>(b, lane, own, &most) * heads;
+    const I total = total_cost<I>(b, lane, own, &most) * heads;
     // Few short items: one CTA each. Else equal shares, of at least MIN_TILES tiles, or one CTA
-    // per item where those are shorter (355 items of one tile: 8.7 against 18.4 us).
+    // per item where those are shorter (355 items of one tile: 8.7 us; 44 CTAs: 18.4).
     const int64_t n_items = static_cast<int64_t>(b.n_seqs) * heads;
-    const bool whole_items = most <= WHOLE_TILES && n_items <= grid;
+    const bool whole_items = most <= WHOLE_TILES + DECODE_ITEM_COST && n_items <= grid;
     I ctas = whole_items ? static_cast<I>(n_items) : total / MIN_TILES;
     if (!whole_items && ctas < n_items) ctas = n_items < total ? static_cast<I>(n_items) : total;
     ctas = ctas < 1 ? 1 : (ctas > grid ? grid : ctas);
@@ -239,11 +249,20 @@ __device__ __forceinline__ Share share_of(const SeqBatch &b, int lane, int heads
     const I x = static_cast<I>(s.split.first(cta));
     I before;
     find_seq<I>(b, lane, own, x, heads, &s.seq, &before);
-    const int tiles = tiles_of(clamped_len(b, s.seq));
+    const int cost = cost_of(clamped_len(b, s.seq)), tiles = cost - DECODE_ITEM_COST;
     s.x = x;
     s.left = s.split.first(cta + 1) - x;
-    s.head = static_cast<int>(quotient(x - before, tiles));
-    s.t0 = static_cast<int>(x - before - static_cast<I>(s.head) * tiles);
+    s.head = static_cast<int>(quotient(x - before, cost));
+    s.t0 = static_cast<int>(x - before - static_cast<I>(s.head) * cost);
+    if (s.t0 >= tiles) {  // behind the item's last tile: on to the next
+        s.x += cost - s.t0;
+        s.left -= cost - s.t0;
+        s.t0 = 0;
+        if (++s.head == heads) {
+            s.head = 0;
+            ++s.seq;
+        }
+    }
     return s;
 }
 
@@ -284,7 +303,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
     const int heads = p.kv_heads * p.head_blocks;  // items per sequence
     const Share sh = p.many_tiles ? share_of<int64_t>(b, lane, heads, blockIdx.x, gridDim.x)
                                   : share_of<int>(b, lane, heads, blockIdx.x, gridDim.x);
-    if (sh.left == 0) return;
+    if (sh.left <= 0) return;
     const Split split = sh.split;
     int seq = sh.seq, head = sh.head, t0 = sh.t0;
     int64_t x = sh.x, left = sh.left;
@@ -328,6 +347,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
         const int tiles = tiles_of(len);
         const int64_t item0 = x - t0;
         const int t1 = tiles - t0 < left ? tiles : t0 + static_cast<int>(left);
+        const int64_t units = tiles + DECODE_ITEM_COST - t0 < left ? tiles + DECODE_ITEM_COST - t0 : left;
         upto += t1 - t0;
         const int kvh = head / p.head_blocks, hb = head - kvh * p.head_blocks;
         const int h0 = kvh * p.group + hb * DECODE_HEADS;     // first query head
@@ -583,8 +603,8 @@ __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
             bar_compute();  // the shared partials are free again
         }
         if (!__all_sync(0xffffffffu, alive)) alive = false;
-        x += t1 - t0;
-        left -= t1 - t0;
+        x += units;
+        left -= units;
         t0 = 0;
         if (++head == heads) {
             head = 0;
@@ -631,30 +651,40 @@ __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
                 if (!last) continue;
                 for (int u = tid; u < units; u += 32 * WARPS) {
                     const int hh = u / (D / 4), d = (u - hh * (D / 4)) * 4;
-                    float4 v[JOIN_MOST];
-                    float m[JOIN_MOST], l[JOIN_MOST];
                     float M = -INFINITY, L = 0.f;
-#pragma unroll
-                    for (int i = 0; i < JOIN_MOST; ++i) {
-                        if (i >= parts) continue;
-                        v[i] = __ldcg(reinterpret_cast<const float4 *>(part(i) + hh * D + d));
-                        m[i] = __ldcg(part(i) + DECODE_HEADS * D + hh);
-                        l[i] = __ldcg(part(i) + DECODE_HEADS * (D + 1) + hh);
-                    }
-#pragma unroll
-                    for (int i = 0; i < JOIN_MOST; ++i)
-                        if (i < parts) M = fmaxf(M, m[i]);
-                    const float ref = M == -INFINITY ? 0.f : M;
                     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int i0 = 0; i0 < parts; i0 += JOIN_STEP) {
+                        float4 v[JOIN_STEP];
+                        float m[JOIN_STEP], l[JOIN_STEP], top = M;
 #pragma unroll
-                    for (int i = 0; i < JOIN_MOST; ++i) {
-                        if (i >= parts) continue;
-                        const float fw = ex2((m[i] - ref) * sl);
-                        L += l[i] * fw;
-                        acc.x += v[i].x * fw;
-                        acc.y += v[i].y * fw;
-                        acc.z += v[i].z * fw;
-                        acc.w += v[i].w * fw;
+                        for (int k = 0; k < JOIN_STEP; ++k) {
+                            m[k] = -INFINITY;
+                            l[k] = 0.f;
+                            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (i0 + k >= parts) continue;
+                            v[k] = __ldcg(reinterpret_cast<const float4 *>(part(i0 + k) + hh * D + d));
+                            m[k] = __ldcg(part(i0 + k) + DECODE_HEADS * D + hh);
+                            l[k] = __ldcg(part(i0 + k) + DECODE_HEADS * (D + 1) + hh);
+                        }
+#pragma unroll
+                        for (int k = 0; k < JOIN_STEP; ++k) top = fmaxf(top, m[k]);
+                        const float ref = top == -INFINITY ? 0.f : top;
+                        const float f0 = ex2((M - ref) * sl);
+                        L *= f0;
+                        acc.x *= f0;
+                        acc.y *= f0;
+                        acc.z *= f0;
+                        acc.w *= f0;
+                        M = top;
+#pragma unroll
+                        for (int k = 0; k < JOIN_STEP; ++k) {
+                            const float fw = ex2((m[k] - ref) * sl);
+                            L += l[k] * fw;
+                            acc.x += v[k].x * fw;
+                            acc.y += v[k].y * fw;
+                            acc.z += v[k].z * fw;
+                            acc.w += v[k].w * fw;
+                        }
                     }
                     finish(it.seq, it.h0, hh, d, acc, M, L);
                 }

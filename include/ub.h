@@ -441,7 +441,7 @@ typedef struct {
  *
  * One kernel each, on `stream`. Attention uses the handle's workspace for the parts of split
  * work, and counts finished parts there; results do not depend on which part finishes when.
- * A sequence that ub_attn_decode spreads over more than 4 SMs, and few new tokens over a long
+ * A sequence that ub_attn_decode spreads over more than 8 SMs, and few new tokens over a long
  * cache in ub_attn_prompt, are joined by CTAs that wait for one another (bounded,
  * UB_ERR_TIMEOUT), as split GEMM tiles are: see ag_gemm, Concurrency.
  * ub_clear_status also resets what such a call may have left counted.
