@@ -59,7 +59,10 @@ constexpr int DEC_THREADS = 32 * 2 * WARPS;
 // in flight.
 constexpr int JOIN_MOST = 8, JOIN_STEP = 4;
 constexpr int MIN_TILES = 4;             // of a CTA, on average (one sequence of 2000 keys: 7.8 us; 16: 10.9 us)
-constexpr int WHOLE_TILES = 32;
+// Tiles that a join costs: items of equal length, whole and split, 32 items of 16 tiles 7.0 and
+// 7.8 us, of 22 8.2 and 8.1, of 31 9.8 and 9.1; 8 items of 22 8.3 and 8.5, of 31 9.9 and 8.7; 64
+// items of 31 10.0 and 10.5; 128 of 31 10.2 and 13.6.
+constexpr int JOIN_TILES = 19;
 
 template <int D, int NT>
 struct DecShape {
@@ -230,10 +233,12 @@ __device__ __forceinline__ Share share_of(const SeqBatch &b, int lane, int heads
     const int own = lane < b.n_seqs ? cost_of(clamped_len(b, lane)) : 0;
     int most;
     const I total = total_cost<I>(b, lane, own, &most) * heads;
-    // Few short items: one CTA each. Else equal shares, of at least MIN_TILES tiles, or one CTA
-    // per item where those are shorter (355 items of one tile: 8.7 us; 44 CTAs: 18.4).
+    // A CTA per item where no item is much longer than an equal share would be: a share saves
+    // the difference and costs a join. Else equal shares, of at least MIN_TILES units, or one
+    // CTA per item where those are shorter (355 items of one tile: 8.7 us; on 44 CTAs 18.4).
     const int64_t n_items = static_cast<int64_t>(b.n_seqs) * heads;
-    const bool whole_items = most <= WHOLE_TILES + DECODE_ITEM_COST && n_items <= grid;
+    const bool whole_items = n_items <= grid && static_cast<int64_t>(most - DECODE_ITEM_COST - JOIN_TILES) * grid <=
+                                                    total - n_items * DECODE_ITEM_COST;
     I ctas = whole_items ? static_cast<I>(n_items) : total / MIN_TILES;
     if (!whole_items && ctas < n_items) ctas = n_items < total ? static_cast<I>(n_items) : total;
     ctas = ctas < 1 ? 1 : (ctas > grid ? grid : ctas);

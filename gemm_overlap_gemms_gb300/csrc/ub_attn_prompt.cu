@@ -993,11 +993,14 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                 sched.n_seqs = p.b.n_seqs;
                 sched.own = lane < p.b.n_seqs ? seq_info(p, lane) : SeqInfo{0, 0, 0, 0};
             }
-            // Items of one q tile where those are no more than the CTAs, of two elsewhere.
+            // Items of one q tile where those are no more than the CTAs and are not split, of two
+            // elsewhere.
             sched.shift = 7 - p.pack_shift;
             for (;; ++sched.shift) {
                 sched.measure();
-                if (static_cast<uint32_t>(sched.tiles) * p.units <= gridDim.x || sched.shift == 8 - p.pack_shift) break;
+                if (sched.shift == 8 - p.pack_shift ||
+                    (static_cast<uint32_t>(sched.tiles) * p.units <= gridDim.x && sched.cmax <= MIN_SPLIT))
+                    break;
             }
             plan = plan_of(sched, p.units, gridDim.x, p.slots);
             it = kNoItem;

@@ -77,9 +77,10 @@ def test_decode_lengths(buf, kv):
 
 
 @pytest.mark.parametrize("heads,kv_heads,kv", [(5, 5, [1 + 7 * i % 30 for i in range(71)]), (8, 8, [17 + 13 * i % 53 for i in range(49)]),
-                                               (12, 4, [0, 5, 0, 300, 33, 0] * 13), (12, 1, [2900 - i for i in range(15)])])
-def test_decode_many_short_items(buf, heads, kv_heads, kv):
-    """A CTA for about every short item, several CTAs for the longer ones."""
+                                               (12, 4, [0, 5, 0, 300, 33, 0] * 13), (12, 1, [2900 - i for i in range(15)]),
+                                               (4, 1, [1500 + i for i in range(140)]), (16, 2, [0] * 30 + [3000])])
+def test_decode_items_and_ctas(buf, heads, kv_heads, kv):
+    """A CTA for every item of about the same length or of a tile or two; equal shares of others."""
     b = ref.Batch([1] * len(kv), kv, page=64, kv_heads=kv_heads, dim=128, seed=heads, fill=float("nan"))
     run_decode(buf, b, heads, 128)
 
