@@ -101,6 +101,20 @@ def test_decode_grids_of_different_sizes_share_the_counters(buf):
     assert torch.equal(before, after)
 
 
+def test_a_page_table_as_wide_as_it_may_be(buf):
+    """The work that such a table could hold passes 32 bits; what the lengths ask for is small."""
+    b = ref.Batch([1] * 3, [5000, 0, 300], page=256, kv_heads=8, dim=64, seed=7, fill=float("nan"))
+    wide = torch.full((3, 8388600), -1, dtype=torch.int32, device="cuda")
+    wide[:, :b.table.shape[1]] = b.table
+    narrow, b.table = b.table, wide
+    q, out = run_decode(buf, b, 16, 64)
+    assert torch.equal(out, buf.attn_decode(q, b.k_cache, b.v_cache, b.lens, narrow))
+    out = sentinel(q.shape)
+    _, lse = buf.attn_prompt_paged(q, b.k_cache, b.v_cache, b.starts, b.lens, wide, out=out, lse=True)
+    ok(buf)
+    check_prompt(b, q, lambda s: (b.rows(b.k_cache, s), b.rows(b.v_cache, s)), out, lse)
+
+
 def test_decode_is_deterministic_and_leaves_its_counters_clean(buf):
     b = ref.Batch([1] * 3, [30000, 5000, 11], page=32, kv_heads=2, dim=64, seed=5)
     q, first = run_decode(buf, b, 8, 64)
