@@ -346,8 +346,8 @@ struct Schedule {
     __device__ __noinline__ Item at(int g, int *level) const
     {
         // The largest level lo with count(lo) > g, in strides that fall to 1; the last pass
-        // covers lo + 1 too (31 levels at most are left for it).
-        int lo = 0, stride = cmax <= 30 ? 1 : (cmax + 32) / 32, k, n;
+        // covers lo + 1 too, so that 31 levels at most may be left for it: level 31 takes two.
+        int lo = 0, stride = cmax <= 30 ? 1 : (cmax <= 62 ? 2 : (cmax + 32) / 32), k, n;
         for (;; stride = stride <= 31 ? 1 : (stride + 30) / 31) {
             n = counts(lo + lane * stride);
             k = 31 - __clz(static_cast<int>(__ballot_sync(0xffffffffu, n > g) | 1u));

@@ -275,6 +275,24 @@ def test_prompt_packed(buf, new, heads, kv_heads, dim):
     run_packed(buf, b, heads, kv_heads, dim)
 
 
+@pytest.mark.parametrize("tiles", [30, 31, 32, 62, 63, 64])
+def test_prompt_packed_longest_of_any_number_of_key_tiles(buf, tiles):
+    """The schedule looks items up by their number of key tiles, 32 numbers at a time."""
+    b = ref.Batch([128 * tiles - 5, 700, 300], [0] * 3, kv_heads=2, dim=64, seed=tiles)
+    run_packed(buf, b, 4, 2, 64)
+
+
+@pytest.mark.parametrize("tiles", [30, 31, 32, 62, 63, 961, 962, 991, 992, 993, 1023, 1024])
+def test_prompt_chunks_of_any_number_of_key_tiles(buf, tiles):
+    b = ref.Batch([3, 300, 9], [128 * tiles - 60, 128 * tiles - 128, 700], page=64, kv_heads=1, dim=64, seed=tiles, fill=float("nan"))
+    buf.set_active_shape([b.T, 256])
+    q = b.randn(b.T, 2, 64, std=1.5)
+    out = sentinel(q.shape)
+    _, lse = buf.attn_prompt_paged(q, b.k_cache, b.v_cache, b.starts, b.lens, b.table, out=out, lse=True)
+    ok(buf)
+    check_prompt(b, q, lambda s: (b.rows(b.k_cache, s), b.rows(b.v_cache, s)), out, lse)
+
+
 def test_prompt_packed_many_sequences(buf):
     new = [(7 * i) % 61 for i in range(300)]
     b = ref.Batch(new, [0] * len(new), kv_heads=2, dim=64, pad=3, seed=1)
