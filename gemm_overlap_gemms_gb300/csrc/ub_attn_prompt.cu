@@ -402,11 +402,12 @@ __device__ Plan plan_of(const Schedule &sc, int units, int ctas, int slots)
 {
     Plan pl{1, 0u, static_cast<uint32_t>(sc.tiles) * units, 0};
     if (pl.total >= static_cast<uint32_t>(ctas) || sc.cmax <= MIN_SPLIT) return pl;
-    // 32 limits at once, from an even share up; of those that give no more pieces than there
-    // are CTAs and slots, the one of the shortest longest piece.
+    // 32 limits at once, from an even share up to the longest item, closer together near the
+    // first; of those that give no more pieces than there are CTAs and slots, the one of the
+    // shortest longest piece.
     int limit = static_cast<int>(sc.work() * units / ctas) + 1;
     limit = limit < MIN_PIECE ? MIN_PIECE : limit;
-    limit += static_cast<int>(static_cast<uint32_t>(limit) * static_cast<uint32_t>(sc.lane) / 8u);
+    limit += static_cast<int>(static_cast<float>(sc.cmax - limit) * static_cast<float>(sc.lane * sc.lane) * (1.f / 1024.f));
     const int n = sc.counts(limit + 1), pieces = (sc.cmax + limit - 1) / limit;
     const float split = static_cast<float>(n) * units * pieces;
     const bool fits = limit < sc.cmax && split <= slots && split + static_cast<float>(sc.tiles - n) * units <= ctas;
