@@ -40,6 +40,13 @@ class AttentionBlock:
         self.cos, self.sin, self.interleaved = cos, sin, interleaved
 
     def _run(self, shards, seq_starts, kv_lens, page_table, attention, stream):
+        # Everything below allocates and clears on the current stream, so that has to be the
+        # call's: a clearing elsewhere could land after the attention has written, and memory
+        # dropped here could be reused while the call still reads it.
+        with torch.cuda.stream(stream):
+            return self._run_here(shards, seq_starts, kv_lens, page_table, attention, stream)
+
+    def _run_here(self, shards, seq_starts, kv_lens, page_table, attention, stream):
         buf, H, G, D = self.buf, self.heads, self.kv_heads, self.head_dim
         T = buf.active_shape[0]
         A = []
@@ -59,7 +66,8 @@ class AttentionBlock:
     def prompt(self, shards, seq_starts, kv_lens, page_table, stream=None):
         """Output shards for the active tokens: whole prompts, or chunks of prompts whose
         beginnings are cached; seq_starts [n + 1], kv_lens [n] with these tokens, page_table
-        [n, entries]."""
+        [n, entries]. With `stream` everything runs there, the inputs have to be ready there, and
+        the outputs belong to it."""
         return self._run(shards, seq_starts, kv_lens, page_table,
                          lambda q, k, v, a: self.buf.attn_prompt_paged(q, k, v, seq_starts, kv_lens, page_table, out=a,
                                                                        stream=stream), stream)

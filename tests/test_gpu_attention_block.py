@@ -108,3 +108,78 @@ def test_chunks_match_the_whole_prompt(block):
         torch.cuda.synchronize()
         assert buf.query_status() == ub.UB_OK
         close(got, want[done - chunk:done])
+
+
+def _busy(ms=30):
+    """Keep the current stream busy for some milliseconds."""
+    torch.cuda._sleep(int(ms * 1.5e6))
+
+
+def test_another_stream_beside_a_busy_current_one(block):
+    """prompt and step on a stream of their own, while the current stream is behind and allocates:
+    what they give on the current stream, bit for bit."""
+    buf = block.buf
+    dev = torch.device("cuda")
+    gen = synth.generator(dev, seed=5)
+    table = torch.randperm(40, device=dev)[:21].to(torch.int32).view(3, 7)
+    starts = torch.tensor([0, 37, 38, 128], dtype=torch.int32, device=dev)
+    lens = torch.tensor([37, 1, 90], dtype=torch.int32, device=dev)
+    one, longer = torch.arange(4, dtype=torch.int32, device=dev), lens + 1
+    x = [list(synth.normal_bf16((TP, n // TP, HIDDEN), 1.0, gen, dev)) for n in (128, 4)]
+
+    def both(stream=None):
+        buf.set_active_shape([128, HIDDEN])
+        first = block.prompt(x[0], starts, lens, table, stream=stream)
+        buf.set_active_shape([4, HIDDEN])
+        return first + block.step(x[1], one, longer, table, stream=stream)
+    want = both()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        side.wait_stream(torch.cuda.current_stream())
+        _busy()
+        got = both(side)
+        for _ in range(8):     # the current stream's own allocations, behind its work
+            torch.full((128, HEADS, D), float("nan"), dtype=torch.bfloat16, device=dev)
+        torch.cuda.synchronize()
+        assert buf.query_status() == ub.UB_OK
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_a_captured_step_with_new_lengths(block):
+    """A step captured into a graph and replayed with new tokens and lengths: what the same steps
+    give outside it."""
+    buf = block.buf
+    dev = torch.device("cuda")
+    gen = synth.generator(dev, seed=6)
+    table = torch.arange(21, dtype=torch.int32, device=dev).view(3, 7)
+    one = torch.arange(4, dtype=torch.int32, device=dev)
+    lens = torch.zeros(3, dtype=torch.int32, device=dev)
+    x = [torch.zeros(2, HIDDEN, dtype=torch.bfloat16, device=dev) for _ in range(TP)]
+    tokens = [synth.normal_bf16((TP, 2, HIDDEN), 1.0, gen, dev) for _ in range(6)]
+    counts = [torch.tensor(n, dtype=torch.int32, device=dev) for n in ([1, 1, 1], [2, 2, 2], [3, 2, 3], [4, 3, 4], [5, 4, 4], [6, 5, 5])]
+    buf.set_active_shape([4, HIDDEN])
+
+    def put(i):
+        for s, t in zip(x, tokens[i]):
+            s.copy_(t)
+        lens.copy_(counts[i])
+    want = []
+    for i in range(6):
+        put(i)
+        want.append([y.clone() for y in block.step(x, one, lens, table)])
+    torch.cuda.synchronize()
+    for c in block.caches:
+        for t in c:
+            t[:21] = float("nan")
+    graph = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        out = block.step(x, one, lens, table, stream=side)
+    for i in range(6):
+        put(i)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert buf.query_status() == ub.UB_OK
+        assert all(torch.equal(a, b) for a, b in zip(out, want[i])), i
