@@ -1690,19 +1690,30 @@ int ub_query_status(ub_handle_t h)
 {
     if (int rc = check_handle(h)) return rc;
     DeviceGuard g(h->device);
-    int32_t st = 0;
-    UB_CUDA(cudaMemcpyAsync(&st, status_of(h), sizeof st, cudaMemcpyDeviceToHost, h->side));
+    uint32_t w[2] = {0u, 0u};  // abort and status words
+    UB_CUDA(cudaMemcpyAsync(w, abort_of(h), sizeof w, cudaMemcpyDeviceToHost, h->side));
     UB_CUDA(cudaStreamSynchronize(h->side));
-    return st;
+    // A call that gave up while ub_clear_status ran may have lost its status, not its abort word.
+    return w[1] == 0u && w[0] != 0u ? static_cast<int>(UB_ERR_TIMEOUT) : static_cast<int32_t>(w[1]);
 }
 
 int ub_clear_status(ub_handle_t h)
 {
     if (int rc = check_handle(h)) return rc;
     DeviceGuard g(h->device);
-    UB_CUDA(cudaMemsetAsync(abort_of(h), 0, 2 * sizeof(uint32_t), h->side));  // abort and status words
-    // what a call whose wait ran out may have left counted
-    UB_CUDA(cudaMemsetAsync(join_counters_of(h), 0, (join_words(h) + kPromptWords) * sizeof(uint32_t), h->side));
+    // Only a call whose wait ran out (the abort word then holds its epoch) leaves the attention's
+    // join counters and tickets counted. Calls in flight count there too, so a reset between
+    // their counts would lose some: it waits for the device first. Without such a call nothing
+    // but the status word is written, and nothing is waited for.
+    uint32_t aborted = 0;
+    UB_CUDA(cudaMemcpyAsync(&aborted, abort_of(h), sizeof aborted, cudaMemcpyDeviceToHost, h->side));
+    UB_CUDA(cudaStreamSynchronize(h->side));
+    if (aborted != 0) {
+        UB_CUDA(cudaDeviceSynchronize());
+        UB_CUDA(cudaMemsetAsync(join_counters_of(h), 0, (join_words(h) + kPromptWords) * sizeof(uint32_t), h->side));
+        UB_CUDA(cudaMemsetAsync(abort_of(h), 0, sizeof(uint32_t), h->side));
+    }
+    UB_CUDA(cudaMemsetAsync(status_of(h), 0, sizeof(int32_t), h->side));
     UB_CUDA(cudaStreamSynchronize(h->side));
     return UB_OK;
 }

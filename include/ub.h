@@ -443,8 +443,8 @@ typedef struct {
  * work, and counts finished parts there; results do not depend on which part finishes when.
  * A sequence that ub_attn_decode spreads over more than 8 SMs, and few new tokens over a long
  * cache in ub_attn_prompt, are joined by CTAs that wait for one another (bounded,
- * UB_ERR_TIMEOUT), as split GEMM tiles are: see ag_gemm, Concurrency.
- * ub_clear_status also resets what such a call may have left counted.
+ * UB_ERR_TIMEOUT), as split GEMM tiles are: see ag_gemm, Concurrency. What such a call may
+ * have left counted is reset by ub_clear_status.
  *
  * Errors: UB_ERR_ARG (null pointers, size, heads not a multiple of kv_heads, head_dim,
  * page_size, rot_dim, scale), UB_ERR_ZERO (n_seqs, heads, kv_heads, num_pages or table_width
@@ -467,10 +467,14 @@ int ub_get_option(ub_handle_t h, int key, int64_t *val);
  * calls of interest has been synchronised. Returns UB_ERR_CUDA if the read fails.
  */
 int ub_query_status(ub_handle_t h);
-/* Reset the sticky device status to UB_OK, and the word through which a call whose wait
- * ran out stops the rest of its CTAs (stream-ordered on the side stream). A call replayed
- * from a CUDA graph keeps the epoch it was captured with, so after one replay has timed
- * out the later replays of that graph give up at once until this is called. */
+/* Reset the sticky device status to UB_OK and, where a wait has run out, also the word
+ * through which that call stops the rest of its CTAs and what it may have left counted
+ * (the attention's tickets and joins). In that case it waits for the device before the
+ * reset, so that no call in flight loses a count; no call of the handle may be made while
+ * it runs. After an attention call whose wait ran out, the results of further attention
+ * calls are undefined until then (nothing faults: their waits are bounded too). A call
+ * replayed from a CUDA graph keeps the epoch it was captured with, so after one replay has
+ * timed out the later replays of that graph give up at once until this is called. */
 int ub_clear_status(ub_handle_t h);
 
 /* Counters of the handle: calls made, device allocations made (constant after
