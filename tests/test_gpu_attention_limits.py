@@ -1,4 +1,5 @@
-"""The attention operators where a wait runs out, and beside ub_clear_status."""
+"""The attention operators where a wait runs out, beside ub_clear_status, and back to back on the
+same counters."""
 import pytest
 import torch
 
@@ -82,6 +83,14 @@ def first(buf, calls):
         ok(buf)
         c.check(outs[-1])
     return outs
+
+
+def test_calls_that_split_differently_back_to_back(buf, calls, first):
+    """Every launch keeps its own output and nothing is waited for in between: calls that share
+    workspace, tickets and counters are right although their launches overlap."""
+    got = rounds(calls, 20)
+    ok(buf)
+    same(got, calls, first)
 
 
 def test_clear_status_beside_calls_in_flight(buf, calls, first):
