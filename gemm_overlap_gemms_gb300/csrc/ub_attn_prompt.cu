@@ -331,6 +331,7 @@ struct Schedule {
     __device__ __noinline__ int counts(int c) const
     {
         int sum = 0;
+        c = c <= cmax ? c : cmax + 1;  // no item has more; the keys of c tiles stay within 32 bits
         for (int i0 = 0; i0 < n_seqs; i0 += 32) {
             const SeqInfo q = info(i0);
             const int m = n_seqs - i0 < 32 ? n_seqs - i0 : 32;

@@ -192,3 +192,42 @@ def test_a_wait_that_runs_out_after_another_error(buf, calls, first):
     got = rounds(calls, 2)
     ok(buf)
     same(got, calls, first)
+
+
+def test_a_sequence_as_long_as_a_table_may_hold(buf):
+    """Almost 2^31 keys: seven pages, named over and over by a table of 8388600 entries. Each distinct
+    key then counts as often as it is seen.
+
+    Bounds: those of attn_ref.attend, and the rounding of the fp32 sums over the key tiles of one SM's
+    part: a step of the sum of weights per tile, 2^-24, and eight of the weighted sum, 2^-23 (the
+    tensor core need not round to nearest)."""
+    page, pages, width, n, heads, dim = 256, 7, 8388600, 3, 2, 64
+    keys = page * width - 5
+    b = ref.Batch([n], [page * pages], page=page, kv_heads=1, dim=dim, free=0, seed=9)
+    table = (torch.arange(width, device="cuda") % pages).to(torch.int32).view(1, width)
+    lens = torch.tensor([keys], dtype=torch.int32, device="cuda")
+    q = b.randn(n, heads, dim, std=1.5)
+    k, v = (c.transpose(0, 1).flatten(1, 2)[0].double() for c in (b.k_cache, b.v_cache))  # in page order
+    s = torch.einsum("nhd,jd->nhj", q.double(), k) * dim ** -0.5
+    seen = torch.arange(keys - n + 1, keys + 1, device="cuda")[:, None]
+    times = seen // (page * pages) + (torch.arange(page * pages, device="cuda") < seen % (page * pages))
+    w = torch.exp(s - s.amax(-1, keepdim=True)) * times[:, None]
+    total = w.sum(-1)
+    want, mag = ((w @ x) / total[..., None] for x in (v, v.abs()))
+    want_lse = s.amax(-1) + total.log()
+    tiles = keys / 128 / torch.cuda.get_device_properties(0).multi_processor_count + 1
+    shift = 2.0 ** -19 * (1 + dim ** -0.5 * torch.einsum("nhd,jd->nhj", q.double().abs(), k.abs()).amax(-1))
+    bound = mag * (2.1 * ref.U + 2 * shift[..., None] + tiles * 9 * 2.0 ** -23)
+    for name in ("prompt", "decode"):
+        rows = n if name == "prompt" else 1
+        out = sentinel((rows, heads, dim))
+        buf.set_active_shape([rows, 256])
+        if name == "prompt":
+            _, lse = buf.attn_prompt_paged(q, b.k_cache, b.v_cache, b.starts, lens, table, out=out, lse=True)
+            rows = slice(0, n)
+        else:
+            _, lse = buf.attn_decode(q[n - 1:], b.k_cache, b.v_cache, lens, table, out=out, lse=True)
+            rows = slice(n - 1, n)
+        ok(buf)
+        ref.within(out, want[rows], bound[rows], name)
+        ref.within(lse, want_lse[rows], shift[rows] + tiles * 2.0 ** -23, name + ", lse")
