@@ -100,7 +100,8 @@ __global__ void __launch_bounds__(APPEND_THREADS) ub_kv_append_kernel(const __gr
         seq += __popc(__ballot_sync(0xffffffffu, past));
     }
     if (seq >= p.b.n_seqs) return;       // a row after the last sequence
-    const int64_t start = p.b.seq_starts[seq], end = p.b.seq_starts[seq + 1];
+    // A sequence ends at T at the latest, for the positions as for the attention over them.
+    const int64_t start = p.b.seq_starts[seq], end = min(p.b.seq_starts[seq + 1], p.T);
     if (t < start || t >= end) return;   // starts out of order: no sequence
     const int64_t pos = p.b.kv_lens[seq] - (end - start) + (t - start);
     if (pos < 0 || (p.rot > 0 && pos >= p.max_pos)) {

@@ -231,3 +231,21 @@ def test_a_sequence_as_long_as_a_table_may_hold(buf):
         ok(buf)
         ref.within(out, want[rows], bound[rows], name)
         ref.within(lse, want_lse[rows], shift[rows] + tiles * 2.0 ** -23, name + ", lse")
+
+
+@pytest.mark.parametrize("starts", [[0, 5, 12], [-3, 5, 8], [0, 5, 2 ** 31 - 1], [-2 ** 31, 5, 9]])
+def test_starts_past_the_active_tokens_are_cut_in_every_operator(buf, starts):
+    """The tokens' positions follow the cut starts: append stores where the attention looks."""
+    b = ref.Batch([5, 3], [25, 37], page=16, kv_heads=1, dim=64, seed=10)
+    buf.set_active_shape([8, 256])
+    q, k, v = b.randn(8, 2, 64), b.randn(8, 1, 64), b.randn(8, 1, 64)
+    given = torch.tensor(starts, dtype=torch.int32, device="cuda")
+    buf.kv_append(q, k, v, None, None, given, b.lens, b.table, b.k_cache, b.v_cache)
+    got = buf.attn_prompt_paged(q, b.k_cache, b.v_cache, given, b.lens, b.table)
+    ok(buf)
+    for s, (t0, t1) in enumerate(((0, 5), (5, 8))):
+        n = t1 - t0
+        assert torch.equal(b.rows(b.k_cache, s)[0, -n:], k[t0:t1, 0]) and torch.equal(b.rows(b.v_cache, s)[0, -n:], v[t0:t1, 0])
+        o, e, _, _ = ref.attend(q[t0:t1], b.rows(b.k_cache, s), b.rows(b.v_cache, s),
+                                torch.arange(b.kv[s] - n, b.kv[s], device="cuda"), 0.125)
+        ref.within(got[t0:t1], o, e, "sequence %d" % s)
