@@ -41,7 +41,7 @@
 // 10 us stream; 3-4 us pass before the first tile lands, 5 us after the last (parts written,
 // counted, joined). 64 sequences, 127938 keys, 2 key/value heads (131 MB): 29 us, 18 of them
 // streaming. 15 sequences of 2900 keys, one key/value head, 8 query heads (22 MB, 10 parts
-// each): 10.4 us. Four sequences of 300 keys, 8 heads: 7.5 us a call, bound by the host's side.
+// each): 10.4 us. Four sequences of 300 keys, 8 heads: 7.4-9.4 us a call, bound by the host's side.
 #include <cuda_bf16.h>
 
 #include "ub_attn.h"
@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
                         l[nt][c] = l[nt][c] * f[nt][c] + sum;
                     }
                 // Weights in BF16, the type of the values they multiply (their sum stays fp32):
-                // 2^-9 of each weight, as large as the rounding of the output.
+                // up to 2^-8 of each weight, as large as the rounding of the output.
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt)
 #pragma unroll

@@ -34,7 +34,7 @@
 // is the chain S -> softmax (1150 cycles, 870 of them its instructions; exp2 runs at 4 cycles
 // per warp and SM quarter) -> P V -> next S, which the other tile's MMAs cover only in part.
 // TMEM holds no third tile. One sequence of 16384 tokens, 8 query heads, 2 key/value heads:
-// 330 us, 1660 TFLOP/s; tensor pipe active in 80 % of the cycles. Shorter prompts: the first
+// 329-342 us, 1.61-1.67 PFLOP/s; tensor pipe active in 80 % of the cycles. Shorter prompts: the first
 // item is known 1.6 us after the grid ahead has finished, and the call ends with its longest
 // item (8037 tokens in four sequences, 8 heads each way: 42 us, of which the 24 key tiles of
 // the longest item take 36). Heads of 64: half the MMAs, the same softmax: 2440 cycles a step.
@@ -398,7 +398,13 @@ struct Plan {
     uint32_t total;      // ... then the whole items
     int n_split;         // token tiles (of each unit) that are split
 };
-constexpr int MIN_SPLIT = PROMPT_WHOLE_KEYS / PROMPT_KEYS, MIN_PIECE = 5;
+constexpr int MIN_SPLIT = PROMPT_WHOLE_KEYS / PROMPT_KEYS;
+// Key tiles of a piece, at least, where the CTAs would allow shorter ones. It matters to a few
+// rows over keys that just pay for a split; 16 tokens, 8 query heads on one of 128, pieces of at
+// least 3, 5 and 8 tiles: 2000 keys 13.8, 14.5 and 19.7 us, 3000 keys 13.8, 16.1 and 19.8, 6000
+// keys 15.4, 17.0 and 20.1; 300 and 1 tokens over 1409 and 3000 keys, heads of 64: 15.8, 15.9 and
+// 18.1; 20000 keys, 8 heads each way: 27.0 with any of them.
+constexpr int MIN_PIECE = 5;
 __device__ Plan plan_of(const Schedule &sc, int units, int ctas, int slots)
 {
     Plan pl{1, 0u, static_cast<uint32_t>(sc.tiles) * units, 0};
@@ -598,6 +604,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                 }
                 const float ref = m == -INFINITY ? 0.f : m * sl;  // no key yet: every weight is zero
                 const uint64_t sl2 = pair_of(sl, sl), ref2 = pair_of(-ref, -ref);
+                // Weights in BF16, the type of the values they multiply (kind::f16 wants one type for
+                // both): up to 2^-8 of each, as large as the rounding of the output. Their sum takes
+                // them unrounded, in fp32.
                 uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
                 for (int c0 = 0; c0 < 128; c0 += 32) {

@@ -21,7 +21,7 @@
 // 8 + 8 + 8 heads (104 MB): 20.4 us, 5.1 TB/s, of which about 4 us are launch and ramp. CTAs of
 // 128 threads (of 256: 68 us) and four heads in flight per lane (two: 66 us, eight: 73 us);
 // loading the first heads ahead of the token's place costs registers, and so warps: 77 us.
-// Four tokens: 2.4 us of GPU time, 9.5 us a call, bound by the host's side of it.
+// Four tokens: 2.4 us of GPU time, 9.5-10.8 us a call, bound by the host's side of it.
 #include <cuda_bf16.h>
 
 #include "ub_attn.h"

@@ -375,11 +375,13 @@ int ub_stream_read(ub_handle_t h, const void *src, int64_t bytes, void *stream);
  * What the device finds wrong with them faults nothing and is recorded in the sticky status
  * (ub_query_status: UB_ERR_ARG): a table entry outside [0, num_pages) or beyond the table's
  * width (its keys read as zeros, an append to it is dropped), a position below zero or
- * outside the rotation tables (the token is dropped). A kv_lens entry below zero counts as
- * zero, one beyond the table as the table's capacity; starts that run backwards or past T
- * are cut to [0, T]. What is past a sequence's length in its last page may hold anything,
- * NaN too; the keys and values of a sequence itself must be finite (a value that is not
- * may reach earlier rows of the same sequence, never another sequence).
+ * outside the rotation tables (the token is dropped). In the attention a kv_lens entry below
+ * zero counts as zero, one beyond the table as the table's capacity. Starts are cut to
+ * [0, T], and a sequence that would end before its start is empty (rows that two sequences
+ * then claim are undefined). What is past a sequence's length in its last page may hold
+ * anything, NaN too; the keys and values of a sequence itself must be finite: a key that is
+ * later than a row has the weight zero there, and zero times an infinite value or NaN is NaN,
+ * so such a value may reach earlier rows of the same sequence, never another sequence.
  *
  * Views: strides in elements, the head dimension contiguous (stride 1); pointers 16-byte
  * aligned, every stride of a dimension longer than 1 a positive multiple of 8. So q, k, v
@@ -427,7 +429,9 @@ typedef struct {
  * fp32 arithmetic, one BF16 rounding. Queries go to `out` (q itself is allowed), rotated
  * keys and unrotated values to the cache. One kernel.
  *
- * ub_attn_prompt: causal attention of the new tokens, fp32 scores and sums:
+ * ub_attn_prompt: causal attention of the new tokens. Scores, maxima and sums are fp32; the
+ * weights p_j are rounded to BF16, the type of the values, for their product with v_j (up to
+ * 2^-8 of a weight, as large as the rounding of the output), but not in the sum below it:
  *     out[t][h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q[t][h] . k_j[h / g] - max),
  * g = heads / kv_heads, over the keys j of t's sequence up to and including t's position.
  *  - page_size = 0: whole prompts; the keys and values are the packed rows k, v themselves.
