@@ -13,7 +13,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libubgemm.so")
 SOURCES = ["ub_gemm.cu", "ub_skinny.cu", "ub_api.cu", "ub_noalloc.cu", "ub_bulk.cu",
-           "ub_attn_api.cu", "ub_kv_append.cu", "ub_attn_decode.cu", "ub_attn_prompt.cu"]
+           "ub_attn_api.cu", "ub_kv_append.cu", "ub_attn_decode.cu", "ub_attn_prompt.cu", "ub_attn_tree.cu",
+           "ub_pages.cu", "ub_pages_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-I", INCLUDE, "-I", CSRC]
 

@@ -66,6 +66,7 @@ struct SeqBatch {
 
 struct AppendParams {
     SeqBatch b;
+    const int32_t *parents;  // of drafted tokens, or null: rotated by their depth
     const void *q, *k, *v;
     void *q_out, *k_cache, *v_cache;
     int64_t q_row, q_head, k_row, k_head, v_row, v_head, o_row, o_head;
@@ -88,6 +89,7 @@ struct DecodeParams {
     int heads, kv_heads, head_dim, group;
     int head_blocks;         // blocks of up to 16 query heads per key/value head
     int many_tiles;          // the table could hold 2^31 units of work or more over all heads
+    int window, sinks;       // keys in sight: the last `window` and the first `sinks`; window 0: all
     float scale;
     float *ws;
     uint32_t *counters;      // parts that have come, per item: zero between calls
@@ -118,6 +120,7 @@ struct PromptParams {
     int T, heads, kv_heads, head_dim, group;
     int pack_shift;          // 1 << pack_shift query heads of one key/value head share a q tile
     int units;               // kv_heads * (group >> pack_shift)
+    int window, sinks;       // as in DecodeParams
     float scale;
     uint32_t *tickets;       // work items drawn, CTAs done; zero between calls
     float *ws;               // parts of items split over their keys: `slots` of 256 rows
@@ -135,5 +138,77 @@ constexpr int PROMPT_WHOLE_KEYS = 1408;  // items of no more keys are never spli
 constexpr int PROMPT_ROWS = 128;         // rows (tokens x packed heads) of one q tile, two per CTA
 constexpr int PROMPT_KEYS = 128;         // keys of one tile
 cudaError_t launch_attn_prompt(const PromptParams &p, int grid, cudaStream_t s);
+
+
+struct TreeParams {
+    CUtensorMap tmQ;         // [T, heads, head_dim], boxes of one q tile's tokens and heads
+    CUtensorMap tmK, tmV;    // [pages, kv_heads, page_size, head_dim]
+    SeqBatch b;
+    const int32_t *parents;
+    void *out;
+    float *lse;
+    int64_t o_row, o_head;
+    int T, heads, kv_heads, head_dim, group;
+    int unit_heads;          // query heads of one key/value head that share a q tile
+    int blocks;              // ... and how many such sets a key/value head has
+    int units;               // kv_heads * blocks
+    int tokens;              // tokens of a q tile
+    int window, sinks;       // as in DecodeParams
+    float scale;
+    float *ws, *ws_rows;     // parts of split items: two slots per CTA of 256 rows; their maxima and sums
+    uint32_t *counters, *times;  // as in DecodeParams
+    uint32_t *abort_word;
+    uint64_t timeout_ns;
+    uint32_t epoch;
+    int pdl;
+};
+constexpr int TREE_ROWS = 128;           // rows (tokens x heads) of one q tile, two per item
+constexpr int TREE_KEYS = 128;           // keys of one tile
+constexpr int TREE_SLOTS = 2;            // workspace slots per CTA
+__host__ __device__ constexpr int tree_slot_floats(int head_dim) { return 2 * TREE_ROWS * head_dim; }
+cudaError_t launch_attn_tree(const TreeParams &p, int grid, cudaStream_t s);
+
+// The pages of a cache: tables and reference counts (see ub_pool_t).
+enum class PoolOp { take, free, fork, compact };
+struct PoolParams {
+    int32_t *refs, *refs_out;     // refs_out: compact
+    int32_t *table, *new_table;   // new_table: fork, compact
+    int64_t table_row, new_row, width;
+    int64_t n;                    // rows (take, free), children (fork), room for moves (compact)
+    int64_t pages;
+    int rows, page_shift;
+    const int32_t *begin, *end;   // take, free: rows of the cache; fork: begin holds the lengths
+    const int32_t *source;        // fork
+    int32_t *pairs;               // fork: copies, compact: moves
+    int32_t *used;                // compact
+    int32_t *list;                // workspace: `pages` words (compact: twice as many)
+    int32_t *status;
+    int pdl;
+};
+cudaError_t launch_pool(PoolOp op, const PoolParams &p, int sms, cudaStream_t s);
+
+struct PageCopyParams {
+    void *k_cache, *v_cache;
+    int64_t kc_page, kc_head, kc_row, vc_page, vc_head, vc_row;
+    const int32_t *pairs;         // [n, 2]: from, to
+    int64_t n, pages;
+    int kv_heads, head_dim, page_shift;
+    int32_t *status;
+    int pdl;
+};
+cudaError_t launch_kv_copy(const PageCopyParams &p, int sms, cudaStream_t s);
+
+struct AcceptParams {
+    SeqBatch b;
+    void *k_cache, *v_cache;
+    int64_t kc_page, kc_head, kc_row, vc_page, vc_head, vc_row;
+    const int32_t *parents, *leaves;
+    int32_t *new_lens;
+    int tokens;                   // entries of parents
+    int kv_heads, head_dim;
+    int parts;                    // CTAs per sequence
+    int pdl;
+};
+cudaError_t launch_kv_accept(AcceptParams p, cudaStream_t s);
 
 }  // namespace ubk

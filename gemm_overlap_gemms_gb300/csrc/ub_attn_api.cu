@@ -1,44 +1,19 @@
 // Host side of the attention operators declared in include/ub.h (ub_kv_append,
-// ub_attn_prompt, ub_attn_decode): argument checks, tensor maps, launches. Nothing of the
-// token batch (lengths, page table) is read on the host.
+// ub_attn_prompt, ub_attn_decode, ub_attn_tree and their forms for windows and drafts, and
+// ub_kv_accept, ub_kv_copy): argument checks, tensor maps, launches. Nothing of the token batch
+// (lengths, page table, drafts) is read on the host.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
-#include <nvtx3/nvToolsExt.h>
 #include <string.h>
 
 #include "ub_attn.h"
+#include "ub_attn_host.h"
 #include "ub_internal.h"
 
 using namespace ubk;
 
 namespace {
-
-struct DeviceScope {
-    int prev = -1;
-    bool ok = true;
-    explicit DeviceScope(int dev)
-    {
-        if (cudaGetDevice(&prev) != cudaSuccess || (prev != dev && cudaSetDevice(dev) != cudaSuccess)) ok = false;
-        if (prev == dev) prev = -1;
-    }
-    ~DeviceScope()
-    {
-        if (ok && prev >= 0) cudaSetDevice(prev);
-    }
-};
-
-struct Range {
-    explicit Range(const char *name) { nvtxRangePushA(name); }
-    ~Range() { nvtxRangePop(); }
-};
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int cuda_failed(cudaError_t e, const char *what)
-{
-    return fail_call(UB_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
-}
 
 // One stride of a dimension of `extent`: that of a dimension of length 1 is never used, and
 // is replaced by one that the tensor maps accept.
@@ -73,7 +48,45 @@ int check_pages(const char *fn, const char *name, ub_pages_t *x, const ub_attn_t
     return UB_OK;
 }
 
-// The checks all three operators share; *a becomes a copy with usable strides.
+int check_cache_sizes(const char *fn, const ub_attn_t *a)
+{
+    if (a->page_size < 8 || a->page_size > 256 || (a->page_size & (a->page_size - 1)) != 0)
+        return fail_call(UB_ERR_ARG, "%s: page size %d is not a power of two from 8 to 256", fn, a->page_size);
+    if (a->num_pages <= 0 || a->table_width <= 0)
+        return fail_call(UB_ERR_ZERO, "%s: %lld pages, %lld table entries per sequence", fn, (long long)a->num_pages,
+                         (long long)a->table_width);
+    if (a->num_pages > INT32_MAX || a->table_width * a->page_size > INT32_MAX - 256 || a->table_width > INT32_MAX)
+        return fail_call(UB_ERR_ARG, "%s: cache of %lld pages, table of %lld entries: too large", fn,
+                         (long long)a->num_pages, (long long)a->table_width);
+    return UB_OK;
+}
+
+int check_caches(const char *fn, ub_attn_t *a)
+{
+    if (int rc = check_pages(fn, "k_cache", &a->k_cache, *a)) return rc;
+    return check_pages(fn, "v_cache", &a->v_cache, *a);
+}
+
+int check_table(const char *fn, const ub_attn_t &a)
+{
+    if (!a.kv_lens || !a.page_table) return fail_call(UB_ERR_ARG, "%s: kv_lens or page_table is null", fn);
+    if (a.n_seqs > 1 && a.table_row < a.table_width)
+        return fail_call(UB_ERR_ARG, "%s: page_table rows of %lld entries, %lld apart", fn, (long long)a.table_width,
+                         (long long)a.table_row);
+    return UB_OK;
+}
+
+// What a row sees besides the causal rule, of at most `keys` keys: *window 0 if that is everything.
+int check_window(const char *fn, int32_t window, int32_t sinks, int64_t keys, int *out_window, int *out_sinks)
+{
+    if (window < 0 || sinks < 0) return fail_call(UB_ERR_ARG, "%s: window %d, sinks %d", fn, window, sinks);
+    const bool all = window == 0 || window >= keys || sinks >= keys;
+    *out_window = all ? 0 : window;
+    *out_sinks = all ? 0 : sinks;
+    return UB_OK;
+}
+
+// The checks the attention operators share; *a becomes a copy with usable strides.
 int check_common(const char *fn, ub_handle_t h, const ub_attn_t *in, bool cache, ub_attn_t *a)
 {
     if (!h) return fail_call(UB_ERR_ARG, "null handle");
@@ -88,20 +101,9 @@ int check_common(const char *fn, ub_handle_t h, const ub_attn_t *in, bool cache,
     if (a->head_dim != 64 && a->head_dim != 128)
         return fail_call(UB_ERR_ARG, "%s: head dimension %d is neither 64 nor 128", fn, a->head_dim);
     if (!cache) return UB_OK;
-    if (a->page_size < 8 || a->page_size > 256 || (a->page_size & (a->page_size - 1)) != 0)
-        return fail_call(UB_ERR_ARG, "%s: page size %d is not a power of two from 8 to 256", fn, a->page_size);
-    if (a->num_pages <= 0 || a->table_width <= 0)
-        return fail_call(UB_ERR_ZERO, "%s: %lld pages, %lld table entries per sequence", fn, (long long)a->num_pages,
-                         (long long)a->table_width);
-    if (a->num_pages > INT32_MAX || a->table_width * a->page_size > INT32_MAX - 256 || a->table_width > INT32_MAX)
-        return fail_call(UB_ERR_ARG, "%s: cache of %lld pages, table of %lld entries: too large", fn,
-                         (long long)a->num_pages, (long long)a->table_width);
-    if (!a->kv_lens || !a->page_table) return fail_call(UB_ERR_ARG, "%s: kv_lens or page_table is null", fn);
-    if (a->n_seqs > 1 && a->table_row < a->table_width)
-        return fail_call(UB_ERR_ARG, "%s: page_table rows of %lld entries, %lld apart", fn, (long long)a->table_width,
-                         (long long)a->table_row);
-    if (int rc = check_pages(fn, "k_cache", &a->k_cache, *a)) return rc;
-    return check_pages(fn, "v_cache", &a->v_cache, *a);
+    if (int rc = check_cache_sizes(fn, a)) return rc;
+    if (int rc = check_table(fn, *a)) return rc;
+    return check_caches(fn, a);
 }
 
 int check_scale(const char *fn, const ub_attn_t &a)
@@ -157,13 +159,8 @@ int encode_tokens(CUtensorMap *map, const ub_heads_t &x, int64_t T, int heads, i
     return encode_nd(map, x.data, 3, dims, strides, box);
 }
 
-}  // namespace
-
-extern "C" {
-
-int ub_kv_append(ub_handle_t h, const ub_attn_t *in, void *stream)
+int append_call(const char *fn, ub_handle_t h, const ub_attn_t *in, const int32_t *parents, void *stream)
 {
-    static const char *fn = "ub_kv_append";
     ub_attn_t a;
     if (int rc = check_common(fn, h, in, true, &a)) return rc;
     const int64_t T = handle_tokens(h);
@@ -189,6 +186,7 @@ int ub_kv_append(ub_handle_t h, const ub_attn_t *in, void *stream)
     AppendParams p;
     memset(&p, 0, sizeof p);
     p.b = batch_of(a, c);
+    p.parents = parents;
     p.q = a.q.data;
     p.k = a.k.data;
     p.v = a.v.data;
@@ -231,9 +229,8 @@ int ub_kv_append(ub_handle_t h, const ub_attn_t *in, void *stream)
     return handle_prof_stop(h, UB_OP_KV_APPEND, s, timed);
 }
 
-int ub_attn_prompt(ub_handle_t h, const ub_attn_t *in, void *stream)
+int prompt_call(const char *fn, ub_handle_t h, const ub_attn_t *in, int32_t window, int32_t sinks, void *stream)
 {
-    static const char *fn = "ub_attn_prompt";
     ub_attn_t a;
     const bool paged = in && in->page_size != 0;
     if (int rc = check_common(fn, h, in, paged, &a)) return rc;
@@ -246,14 +243,16 @@ int ub_attn_prompt(ub_handle_t h, const ub_attn_t *in, void *stream)
         if (int rc = check_heads(fn, "v", &a.v, T, a.kv_heads, a.head_dim)) return rc;
     }
     if (int rc = check_heads(fn, "out", &a.out, T, a.heads, a.head_dim)) return rc;
+    const int64_t keys = paged ? a.table_width * a.page_size : T;
+    PromptParams p;
+    memset(&p, 0, sizeof p);
+    if (int rc = check_window(fn, window, sinks, keys, &p.window, &p.sinks)) return rc;
     DeviceScope g(handle_device(h));
     if (!g.ok) return fail_call(UB_ERR_CUDA, "%s: cannot select the handle's device", fn);
     Range range(fn);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     HandleCall c;
     if (int rc = handle_call(h, s, &c)) return rc;
-    PromptParams p;
-    memset(&p, 0, sizeof p);
     p.group = a.heads / a.kv_heads;
     // The query heads of a key/value head are packed into the rows of a q tile, as many as a
     // power of two of the group allows: they share the tile's keys and values, and a tile of
@@ -295,7 +294,6 @@ int ub_attn_prompt(ub_handle_t h, const ub_attn_t *in, void *stream)
     // be split over their keys.
     const int64_t tokens = PROMPT_ROWS / pack;
     const int64_t most = (T / tokens + (a.n_seqs < T ? a.n_seqs : T)) * p.units;
-    const int64_t keys = paged ? a.table_width * a.page_size : T;
     const int64_t grid = most < c.sms && keys <= PROMPT_WHOLE_KEYS ? most : c.sms;
     bool timed = false;
     if (int rc = handle_prof_start(h, UB_OP_ATTN_PROMPT, s, &timed)) return rc;
@@ -304,9 +302,8 @@ int ub_attn_prompt(ub_handle_t h, const ub_attn_t *in, void *stream)
     return handle_prof_stop(h, UB_OP_ATTN_PROMPT, s, timed);
 }
 
-int ub_attn_decode(ub_handle_t h, const ub_attn_t *in, void *stream)
+int decode_call(const char *fn, ub_handle_t h, const ub_attn_t *in, int32_t window, int32_t sinks, void *stream)
 {
-    static const char *fn = "ub_attn_decode";
     ub_attn_t a;
     if (int rc = check_common(fn, h, in, true, &a)) return rc;
     const int64_t T = handle_tokens(h);
@@ -315,14 +312,15 @@ int ub_attn_decode(ub_handle_t h, const ub_attn_t *in, void *stream)
         return fail_call(UB_ERR_CAPACITY, "%s: %d sequences exceed the %lld active tokens", fn, a.n_seqs, (long long)T);
     if (int rc = check_heads(fn, "q", &a.q, T, a.heads, a.head_dim)) return rc;
     if (int rc = check_heads(fn, "out", &a.out, T, a.heads, a.head_dim)) return rc;
+    DecodeParams p;
+    memset(&p, 0, sizeof p);
+    if (int rc = check_window(fn, window, sinks, a.table_width * a.page_size, &p.window, &p.sinks)) return rc;
     DeviceScope g(handle_device(h));
     if (!g.ok) return fail_call(UB_ERR_CUDA, "%s: cannot select the handle's device", fn);
     Range range(fn);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     HandleCall c;
     if (int rc = handle_call(h, s, &c)) return rc;
-    DecodeParams p;
-    memset(&p, 0, sizeof p);
     if (int rc = encode_pages_whole(&p.tmK, a.k_cache, a, DECODE_KEYS)) return rc;
     if (int rc = encode_pages_whole(&p.tmV, a.v_cache, a, DECODE_KEYS)) return rc;
     handle_count_maps(h, 2);
@@ -359,6 +357,211 @@ int ub_attn_decode(ub_handle_t h, const ub_attn_t *in, void *stream)
     const cudaError_t e = launch_attn_decode(p, static_cast<int>(grid), s);
     if (e != cudaSuccess) return cuda_failed(e, "decode attention kernel launch");
     return handle_prof_stop(h, UB_OP_ATTN_DECODE, s, timed);
+}
+
+int tree_call(const char *fn, ub_handle_t h, const ub_attn_t *in, const int32_t *parents, int32_t window, int32_t sinks,
+              void *stream)
+{
+    ub_attn_t a;
+    if (int rc = check_common(fn, h, in, true, &a)) return rc;
+    const int64_t T = handle_tokens(h);
+    if (!a.seq_starts || !parents) return fail_call(UB_ERR_ARG, "%s: seq_starts or parents is null", fn);
+    if (int rc = check_scale(fn, a)) return rc;
+    if (int rc = check_heads(fn, "q", &a.q, T, a.heads, a.head_dim)) return rc;
+    if (int rc = check_heads(fn, "out", &a.out, T, a.heads, a.head_dim)) return rc;
+    const int64_t keys = a.table_width * a.page_size;
+    TreeParams p;
+    memset(&p, 0, sizeof p);
+    if (int rc = check_window(fn, window, sinks, keys, &p.window, &p.sinks)) return rc;
+    DeviceScope g(handle_device(h));
+    if (!g.ok) return fail_call(UB_ERR_CUDA, "%s: cannot select the handle's device", fn);
+    Range range(fn);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    HandleCall c;
+    if (int rc = handle_call(h, s, &c)) return rc;
+    // All query heads of a key/value head share a q tile, in even sets where they are more than
+    // its rows: they share its keys and values.
+    p.group = a.heads / a.kv_heads;
+    p.blocks = (p.group + TREE_ROWS - 1) / TREE_ROWS;
+    p.unit_heads = (p.group + p.blocks - 1) / p.blocks;
+    p.units = a.kv_heads * p.blocks;
+    p.tokens = TREE_ROWS / p.unit_heads;
+    if (int rc = encode_tokens(&p.tmQ, a.q, T, a.heads, a.head_dim, p.unit_heads, p.tokens)) return rc;
+    if (int rc = encode_pages(&p.tmK, a.k_cache, a, TREE_KEYS)) return rc;
+    if (int rc = encode_pages(&p.tmV, a.v_cache, a, TREE_KEYS)) return rc;
+    handle_count_maps(h, 3);
+    p.b = batch_of(a, c);
+    p.parents = parents;
+    p.out = a.out.data;
+    p.lse = a.lse;
+    p.o_row = a.out.row;
+    p.o_head = a.out.head;
+    p.T = static_cast<int>(T);
+    p.heads = a.heads;
+    p.kv_heads = a.kv_heads;
+    p.head_dim = a.head_dim;
+    p.scale = a.scale;
+    p.ws = c.ws;
+    p.ws_rows = c.ws_rows;
+    p.counters = c.join_counters;
+    p.times = c.join_counters + c.join_words / DECODE_COUNTERS;
+    p.abort_word = c.abort_word;
+    p.timeout_ns = c.timeout_ns;
+    p.epoch = c.epoch;
+    p.pdl = c.pdl;
+    // As many CTAs as fit, and no more than there can be key tiles.
+    int64_t grid = c.sms;
+    const int64_t items = (T / (2 * p.tokens) + (a.n_seqs < T ? a.n_seqs : T)) * p.units;
+    const int64_t tiles = (keys + TREE_KEYS - 1) / TREE_KEYS;
+    if (items <= grid && items * tiles < grid) grid = items * tiles;
+    if (DECODE_COUNTERS * grid > c.join_words || TREE_SLOTS * grid > PROMPT_SLOTS ||
+        TREE_SLOTS * grid * tree_slot_floats(a.head_dim) > static_cast<int64_t>(c.ws_floats))
+        return fail_call(UB_ERR_ARG, "%s: workspace too small for %lld CTAs", fn, (long long)grid);
+    bool timed = false;
+    if (int rc = handle_prof_start(h, UB_OP_ATTN_TREE, s, &timed)) return rc;
+    const cudaError_t e = launch_attn_tree(p, static_cast<int>(grid), s);
+    if (e != cudaSuccess) return cuda_failed(e, "tree attention kernel launch");
+    return handle_prof_stop(h, UB_OP_ATTN_TREE, s, timed);
+}
+
+// The caches of ub_kv_copy and ub_kv_accept: the fields of ub_attn_t that describe them.
+int check_cache_call(const char *fn, ub_handle_t h, const ub_attn_t *in, ub_attn_t *a)
+{
+    if (!h) return fail_call(UB_ERR_ARG, "null handle");
+    if (!in) return fail_call(UB_ERR_ARG, "%s: null arguments", fn);
+    if (in->size != sizeof(ub_attn_t))
+        return fail_call(UB_ERR_ARG, "%s: argument struct of %u bytes, %zu expected", fn, in->size, sizeof(ub_attn_t));
+    *a = *in;
+    if (a->kv_heads <= 0) return fail_call(UB_ERR_ZERO, "%s: %d key/value heads", fn, a->kv_heads);
+    if (a->kv_heads > 65536) return fail_call(UB_ERR_ARG, "%s: %d key/value heads", fn, a->kv_heads);
+    if (a->head_dim != 64 && a->head_dim != 128)
+        return fail_call(UB_ERR_ARG, "%s: head dimension %d is neither 64 nor 128", fn, a->head_dim);
+    return UB_OK;
+}
+
+int log2_of(int x)
+{
+    int shift = 0;
+    while ((1 << shift) < x) ++shift;
+    return shift;
+}
+
+template <typename P>
+void set_caches(P *p, const ub_attn_t &a)
+{
+    p->k_cache = a.k_cache.data;
+    p->v_cache = a.v_cache.data;
+    p->kc_page = a.k_cache.page;
+    p->kc_head = a.k_cache.head;
+    p->kc_row = a.k_cache.row;
+    p->vc_page = a.v_cache.page;
+    p->vc_head = a.v_cache.head;
+    p->vc_row = a.v_cache.row;
+    p->kv_heads = a.kv_heads;
+    p->head_dim = a.head_dim;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ub_kv_append(ub_handle_t h, const ub_attn_t *a, void *stream) { return append_call("ub_kv_append", h, a, nullptr, stream); }
+
+int ub_kv_append_tree(ub_handle_t h, const ub_attn_t *a, const int32_t *parents, void *stream)
+{
+    if (h && a && !parents) return fail_call(UB_ERR_ARG, "ub_kv_append_tree: parents is null");
+    return append_call("ub_kv_append_tree", h, a, parents, stream);
+}
+
+int ub_attn_prompt(ub_handle_t h, const ub_attn_t *a, void *stream) { return prompt_call("ub_attn_prompt", h, a, 0, 0, stream); }
+
+int ub_attn_prompt_window(ub_handle_t h, const ub_attn_t *a, int32_t window, int32_t sinks, void *stream)
+{
+    return prompt_call("ub_attn_prompt_window", h, a, window, sinks, stream);
+}
+
+int ub_attn_decode(ub_handle_t h, const ub_attn_t *a, void *stream) { return decode_call("ub_attn_decode", h, a, 0, 0, stream); }
+
+int ub_attn_decode_window(ub_handle_t h, const ub_attn_t *a, int32_t window, int32_t sinks, void *stream)
+{
+    return decode_call("ub_attn_decode_window", h, a, window, sinks, stream);
+}
+
+int ub_attn_tree(ub_handle_t h, const ub_attn_t *a, const int32_t *parents, int32_t window, int32_t sinks, void *stream)
+{
+    return tree_call("ub_attn_tree", h, a, parents, window, sinks, stream);
+}
+
+int ub_kv_copy(ub_handle_t h, const ub_attn_t *in, const int32_t *pairs, int64_t n_pairs, void *stream)
+{
+    static const char *fn = "ub_kv_copy";
+    ub_attn_t a;
+    if (int rc = check_cache_call(fn, h, in, &a)) return rc;
+    a.table_width = 1;  // no table
+    if (int rc = check_cache_sizes(fn, &a)) return rc;
+    if (int rc = check_caches(fn, &a)) return rc;
+    if (n_pairs < 0 || n_pairs > INT32_MAX) return fail_call(UB_ERR_ARG, "%s: %lld pairs", fn, (long long)n_pairs);
+    if (n_pairs == 0) return UB_OK;
+    if (!pairs) return fail_call(UB_ERR_ARG, "%s: pairs is null", fn);
+    DeviceScope g(handle_device(h));
+    if (!g.ok) return fail_call(UB_ERR_CUDA, "%s: cannot select the handle's device", fn);
+    Range range(fn);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    HandleCall c;
+    if (int rc = handle_call(h, s, &c)) return rc;
+    PageCopyParams p;
+    memset(&p, 0, sizeof p);
+    set_caches(&p, a);
+    p.pairs = pairs;
+    p.n = n_pairs;
+    p.pages = a.num_pages;
+    p.page_shift = log2_of(a.page_size);
+    p.status = c.status;
+    p.pdl = c.pdl;
+    bool timed = false;
+    if (int rc = handle_prof_start(h, UB_OP_KV_COPY, s, &timed)) return rc;
+    const cudaError_t e = launch_kv_copy(p, c.sms, s);
+    if (e != cudaSuccess) return cuda_failed(e, "page copy kernel launch");
+    return handle_prof_stop(h, UB_OP_KV_COPY, s, timed);
+}
+
+int ub_kv_accept(ub_handle_t h, const ub_attn_t *in, const int32_t *parents, int64_t n_tokens, const int32_t *leaves,
+                 int32_t *new_lens, void *stream)
+{
+    static const char *fn = "ub_kv_accept";
+    ub_attn_t a;
+    if (int rc = check_cache_call(fn, h, in, &a)) return rc;
+    if (a.n_seqs <= 0) return fail_call(UB_ERR_ZERO, "%s: %d sequences", fn, a.n_seqs);
+    if (!a.seq_starts || !parents || !leaves || !new_lens) return fail_call(UB_ERR_ARG, "%s: a null array", fn);
+    if (n_tokens < 0 || n_tokens > INT32_MAX) return fail_call(UB_ERR_ARG, "%s: %lld tokens", fn, (long long)n_tokens);
+    if (int rc = check_cache_sizes(fn, &a)) return rc;
+    if (int rc = check_table(fn, a)) return rc;
+    if (int rc = check_caches(fn, &a)) return rc;
+    const uintptr_t from = reinterpret_cast<uintptr_t>(a.kv_lens), to = reinterpret_cast<uintptr_t>(new_lens);
+    const uintptr_t bytes = sizeof(int32_t) * static_cast<uintptr_t>(a.n_seqs);
+    if (from < to + bytes && to < from + bytes) return fail_call(UB_ERR_ARG, "%s: new_lens overlaps kv_lens", fn);
+    if (static_cast<int64_t>(a.n_seqs) * ((2 * static_cast<int64_t>(a.kv_heads) * a.head_dim / 8 + 127) / 128) > INT32_MAX)
+        return fail_call(UB_ERR_ARG, "%s: %d sequences of %d heads are too many", fn, a.n_seqs, a.kv_heads);
+    DeviceScope g(handle_device(h));
+    if (!g.ok) return fail_call(UB_ERR_CUDA, "%s: cannot select the handle's device", fn);
+    Range range(fn);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    HandleCall c;
+    if (int rc = handle_call(h, s, &c)) return rc;
+    AcceptParams p;
+    memset(&p, 0, sizeof p);
+    p.b = batch_of(a, c);
+    set_caches(&p, a);
+    p.parents = parents;
+    p.leaves = leaves;
+    p.new_lens = new_lens;
+    p.tokens = static_cast<int>(n_tokens);
+    p.pdl = c.pdl;
+    bool timed = false;
+    if (int rc = handle_prof_start(h, UB_OP_KV_ACCEPT, s, &timed)) return rc;
+    const cudaError_t e = launch_kv_accept(p, s);
+    if (e != cudaSuccess) return cuda_failed(e, "accept kernel launch");
+    return handle_prof_stop(h, UB_OP_KV_ACCEPT, s, timed);
 }
 
 }  // extern "C"

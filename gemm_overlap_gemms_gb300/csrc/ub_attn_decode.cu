@@ -140,17 +140,38 @@ __device__ __forceinline__ uint32_t arrive_acq_rel(uint32_t *counter)
 
 __device__ __forceinline__ void bar_compute() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-__device__ __forceinline__ int clamped_len(const SeqBatch &b, int seq)
+// The keys that the new token of a sequence sees: all of them, or (WINDOW) the last `window` and
+// the first `sinks`. Its tiles are those that hold such a key, in rising order.
+template <bool WINDOW>
+struct Keys {
+    int len;
+    int lo;     // first key of the window
+    int near;   // its tile
+    int far;    // tiles before it that hold sinks
+    __device__ __forceinline__ int tiles() const
+    {
+        const int all = len > 0 ? (len + KT - 1) / KT : 1;
+        return WINDOW ? all - near + far : all;
+    }
+    __device__ __forceinline__ int tile(int t) const { return !WINDOW || t < far ? t : t - far + near; }
+    // What an item counts in the split: its tiles and its end, which costs a CTA about as long as
+    // DECODE_ITEM_COST tiles.
+    __device__ __forceinline__ int cost() const { return tiles() + DECODE_ITEM_COST; }
+};
+template <bool WINDOW>
+__device__ __forceinline__ Keys<WINDOW> keys_of(const DecodeParams &p, int seq)
 {
-    const int len = b.kv_lens[seq];
-    const int64_t most = static_cast<int64_t>(b.table_width) << b.page_shift;
-    return len < 0 ? 0 : (len > most ? static_cast<int>(most) : len);
+    const int len = p.b.kv_lens[seq];
+    const int64_t most = static_cast<int64_t>(p.b.table_width) << p.b.page_shift;
+    Keys<WINDOW> k{len < 0 ? 0 : (len > most ? static_cast<int>(most) : len), 0, 0, 0};
+    if (WINDOW) {
+        k.lo = k.len > p.window ? k.len - p.window : 0;
+        k.near = k.lo / KT;
+        const int sunk = (p.sinks + KT - 1) / KT;
+        k.far = sunk < k.near ? sunk : k.near;
+    }
+    return k;
 }
-__device__ __forceinline__ int tiles_of(int len) { return len > 0 ? (len + KT - 1) / KT : 1; }
-
-// What an item counts in the split: its tiles and its end, which costs a CTA about as long as
-// DECODE_ITEM_COST tiles.
-__device__ __forceinline__ int cost_of(int len) { return tiles_of(len) + DECODE_ITEM_COST; }
 
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
 {
@@ -179,13 +200,13 @@ __device__ __forceinline__ int64_t warp_sum(int64_t v)
 __device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
 
 // Sum and maximum of the sequences' costs (one warp). I: a type that holds the sum over all heads.
-template <typename I>
-__device__ __forceinline__ I total_cost(const SeqBatch &b, int lane, int own, int *most)
+template <bool WINDOW, typename I>
+__device__ __forceinline__ I total_cost(const DecodeParams &p, int lane, int own, int *most)
 {
     I sum = own;
     int top = own;
-    for (int i = lane + 32; i < b.n_seqs; i += 32) {
-        const int n = cost_of(clamped_len(b, i));
+    for (int i = lane + 32; i < p.b.n_seqs; i += 32) {
+        const int n = keys_of<WINDOW>(p, i).cost();
         sum += n;
         top = n > top ? n : top;
     }
@@ -194,12 +215,12 @@ __device__ __forceinline__ I total_cost(const SeqBatch &b, int lane, int own, in
 }
 // The sequence that holds unit `unit` of the call, and the units before it. own: the cost of
 // sequence `lane` (0 past the last).
-template <typename I>
-__device__ __forceinline__ void find_seq(const SeqBatch &b, int lane, int own, I unit, int heads, int *seq, I *before)
+template <bool WINDOW, typename I>
+__device__ __forceinline__ void find_seq(const DecodeParams &p, int lane, int own, I unit, int heads, int *seq, I *before)
 {
     I seen = 0;  // units of the sequences before this batch of 32, over all heads
-    for (int i0 = 0; i0 < b.n_seqs; i0 += 32) {
-        I mine = i0 == 0 ? own : (i0 + lane < b.n_seqs ? cost_of(clamped_len(b, i0 + lane)) : 0);
+    for (int i0 = 0; i0 < p.b.n_seqs; i0 += 32) {
+        I mine = i0 == 0 ? own : (i0 + lane < p.b.n_seqs ? keys_of<WINDOW>(p, i0 + lane).cost() : 0);
         mine *= heads;
         I upto = mine;
 #pragma unroll
@@ -216,7 +237,7 @@ __device__ __forceinline__ void find_seq(const SeqBatch &b, int lane, int own, I
         }
         seen += __shfl_sync(0xffffffffu, upto, 31);
     }
-    *seq = b.n_seqs;
+    *seq = p.b.n_seqs;
     *before = seen;
 }
 
@@ -226,17 +247,17 @@ struct Share {
     int64_t x, left;  // first unit of the whole call (not counted for whole items), units
     int seq, head, t0;
 };
-template <typename I>
-__device__ __forceinline__ Share share_of(const SeqBatch &b, int lane, int heads, int cta, int grid)
+template <bool WINDOW, typename I>
+__device__ __forceinline__ Share share_of(const DecodeParams &p, int lane, int heads, int cta, int grid)
 {
     Share s{{0, 0}, 0, 0, 0, 0, 0};
-    const int own = lane < b.n_seqs ? cost_of(clamped_len(b, lane)) : 0;
+    const int own = lane < p.b.n_seqs ? keys_of<WINDOW>(p, lane).cost() : 0;
     int most;
-    const I total = total_cost<I>(b, lane, own, &most) * heads;
+    const I total = total_cost<WINDOW, I>(p, lane, own, &most) * heads;
     // A CTA per item where no item is much longer than an equal share would be: a share saves
     // the difference and costs a join. Else equal shares, of at least MIN_TILES units, or one
     // CTA per item where those are shorter (355 items of one tile: 8.7 us; on 44 CTAs 18.4).
-    const int64_t n_items = static_cast<int64_t>(b.n_seqs) * heads;
+    const int64_t n_items = static_cast<int64_t>(p.b.n_seqs) * heads;
     const bool whole_items = n_items <= grid && static_cast<int64_t>(most - DECODE_ITEM_COST - JOIN_TILES) * grid <=
                                                     total - n_items * DECODE_ITEM_COST;
     I ctas = whole_items ? static_cast<I>(n_items) : total / MIN_TILES;
@@ -248,13 +269,13 @@ __device__ __forceinline__ Share share_of(const SeqBatch &b, int lane, int heads
     if (whole_items) {
         s.seq = cta / heads;
         s.head = cta - s.seq * heads;
-        s.left = tiles_of(clamped_len(b, s.seq));
+        s.left = keys_of<WINDOW>(p, s.seq).tiles();
         return s;
     }
     const I x = static_cast<I>(s.split.first(cta));
     I before;
-    find_seq<I>(b, lane, own, x, heads, &s.seq, &before);
-    const int cost = cost_of(clamped_len(b, s.seq)), tiles = cost - DECODE_ITEM_COST;
+    find_seq<WINDOW, I>(p, lane, own, x, heads, &s.seq, &before);
+    const int cost = keys_of<WINDOW>(p, s.seq).cost(), tiles = cost - DECODE_ITEM_COST;
     s.x = x;
     s.left = s.split.first(cta + 1) - x;
     s.head = static_cast<int>(quotient(x - before, cost));
@@ -271,7 +292,7 @@ __device__ __forceinline__ Share share_of(const SeqBatch &b, int lane, int heads
     return s;
 }
 
-template <int D, int NT>
+template <int D, int NT, bool WINDOW>
 __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
     ub_attn_decode_kernel(const __grid_constant__ DecodeParams p)
 {
@@ -306,8 +327,8 @@ __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
 
     const SeqBatch &b = p.b;
     const int heads = p.kv_heads * p.head_blocks;  // items per sequence
-    const Share sh = p.many_tiles ? share_of<int64_t>(b, lane, heads, blockIdx.x, gridDim.x)
-                                  : share_of<int>(b, lane, heads, blockIdx.x, gridDim.x);
+    const Share sh = p.many_tiles ? share_of<WINDOW, int64_t>(p, lane, heads, blockIdx.x, gridDim.x)
+                                  : share_of<WINDOW, int>(p, lane, heads, blockIdx.x, gridDim.x);
     if (sh.left <= 0) return;
     const Split split = sh.split;
     int seq = sh.seq, head = sh.head, t0 = sh.t0;
@@ -348,8 +369,8 @@ __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
         v_row[mt] = row_at(mt * 16 + (lane & 7) + ((lane >> 4) << 3));
     }
     while (left > 0 && seq < b.n_seqs) {
-        const int len = clamped_len(b, seq);
-        const int tiles = tiles_of(len);
+        const Keys<WINDOW> keys = keys_of<WINDOW>(p, seq);
+        const int len = keys.len, tiles = keys.tiles();
         const int64_t item0 = x - t0;
         const int t1 = tiles - t0 < left ? tiles : t0 + static_cast<int>(left);
         const int64_t units = tiles + DECODE_ITEM_COST - t0 < left ? tiles + DECODE_ITEM_COST - t0 : left;
@@ -371,15 +392,19 @@ __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
                 if (count >= S) alive = mbar_wait(empty0 + 8 * stage, ((count / S) - 1) & 1, wc);
                 alive = __all_sync(0xffffffffu, alive);
                 if (!alive) break;
-                const int key0 = t * KT;
+                const int key0 = keys.tile(t) * KT;
                 const int page0 = key0 >> b.page_shift;
                 const int valid = len - key0;
                 const int n_box = valid <= 0 ? 0 : ((valid < KT ? valid : KT) + box - 1) / box;
                 if (page0 + boxes > cached0 + cached_n) {
                     cached0 = page0;
                     cached_n = 32;
-                    ids = cached0 + lane < pages ? table[cached0 + lane] : -1;
-                    if (cached0 + lane < pages && (ids < 0 || ids >= b.num_pages)) {
+                    // a page that the token does not see may be another sequence's by now, or nobody's
+                    const int64_t first = static_cast<int64_t>(cached0 + lane) << b.page_shift;
+                    const bool seen = cached0 + lane < pages &&
+                                      (!WINDOW || first + (int64_t(1) << b.page_shift) > keys.lo || first < p.sinks);
+                    ids = seen ? table[cached0 + lane] : -1;
+                    if (seen && (ids < 0 || ids >= b.num_pages)) {
                         atomicCAS(p.status_word(), 0, UB_ERR_ARG);
                         ids = -1;  // outside the tensor: the box is filled with zeros
                     }
@@ -435,7 +460,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
                 alive = __all_sync(0xffffffffu, alive);
                 if (!alive) break;
                 const uint32_t kb = smem_u32(base) + stage * Sh::STAGE_BYTES, vb = kb + Sh::TILE_BYTES;
-                const int valid = len - t * KT;
+                const int key0 = keys.tile(t) * KT, valid = len - key0;
                 if (valid < KT) {
                     // Rows past the length hold another call's bytes, perhaps not even numbers:
                     // their weight is zero, so their values must be finite.
@@ -495,7 +520,8 @@ __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
 #pragma unroll
                             for (int r = 0; r < 2; ++r) {
                                 float &v = s[mt][nt][r * 2 + c];
-                                if (mt * 16 + r * 8 + lane / 4 >= valid) v = -INFINITY;
+                                const int key = mt * 16 + r * 8 + lane / 4;
+                                if (key >= valid || (WINDOW && key0 + key < keys.lo && key0 + key >= p.sinks)) v = -INFINITY;
                                 mx = fmaxf(mx, v);
                             }
 #pragma unroll
@@ -775,13 +801,18 @@ __global__ void __launch_bounds__(DEC_THREADS, DECODE_CTAS_PER_SM)
 
 }  // namespace
 
+template <int D, int NT, bool WINDOW>
+static cudaError_t launch_decode(const DecodeParams &p, int grid, cudaStream_t s)
+{
+    const cudaError_t e = raise_smem_limit(reinterpret_cast<const void *>(ub_attn_decode_kernel<D, NT, WINDOW>),
+                                           DecShape<D, NT>::SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_ex(ub_attn_decode_kernel<D, NT, WINDOW>, p, grid, DEC_THREADS, DecShape<D, NT>::SMEM, 1, p.pdl != 0, s);
+}
 template <int D, int NT>
 static cudaError_t launch_decode(const DecodeParams &p, int grid, cudaStream_t s)
 {
-    const cudaError_t e = raise_smem_limit(reinterpret_cast<const void *>(ub_attn_decode_kernel<D, NT>),
-                                           DecShape<D, NT>::SMEM);
-    if (e != cudaSuccess) return e;
-    return launch_ex(ub_attn_decode_kernel<D, NT>, p, grid, DEC_THREADS, DecShape<D, NT>::SMEM, 1, p.pdl != 0, s);
+    return p.window > 0 ? launch_decode<D, NT, true>(p, grid, s) : launch_decode<D, NT, false>(p, grid, s);
 }
 
 cudaError_t launch_attn_decode(const DecodeParams &p, int grid, cudaStream_t s)

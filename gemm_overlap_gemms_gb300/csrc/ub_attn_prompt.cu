@@ -42,6 +42,7 @@
 #include <limits.h>
 
 #include "ub_attn.h"
+#include "ub_attn_mma.cuh"
 #include "ub_device.cuh"
 #include "ub_internal.h"
 
@@ -79,7 +80,7 @@ struct Item {
     int len;     // keys of the sequence
     int src;     // first key row (packed) or sequence (paged)
     int unit;
-    int j0, j1;  // its key tiles (a piece of a split item: a part of them)
+    int j0, j1;  // its key tiles, of those in sight (a piece of a split item: a part of them)
     int slot;    // first workspace slot of a split item; -1: not split
     int piece, pieces;
     int n;       // key tiles of the whole item
@@ -92,6 +93,31 @@ __device__ __forceinline__ int piece_begin(int n, int i, int pieces)
     return i * base + (i < rem ? i : rem);
 }
 
+// The keys that the rows of an item see together: all up to the last row, or (WINDOW) from the
+// window of the first row on, and the first `sinks`. Key tiles are counted along those that hold
+// such a key.
+template <bool WINDOW>
+struct Sight {
+    int lo;    // first key of the first row's window
+    int near;  // its key tile
+    int far;   // key tiles before it that hold sinks
+    __device__ __forceinline__ int gap() const { return WINDOW ? near - far : 0; }
+    // The key tile that is the j-th in sight.
+    __device__ __forceinline__ int tile(int j) const { return WINDOW && j >= far ? j + (near - far) : j; }
+};
+template <bool WINDOW>
+__device__ __forceinline__ Sight<WINDOW> sight(const PromptParams &p, int off)
+{
+    Sight<WINDOW> s{0, 0, 0};
+    if (WINDOW) {
+        s.lo = off >= p.window ? off - p.window + 1 : 0;
+        s.near = s.lo / PROMPT_KEYS;
+        const int sunk = (p.sinks + PROMPT_KEYS - 1) / PROMPT_KEYS;
+        s.far = sunk < s.near ? sunk : s.near;
+    }
+    return s;
+}
+
 struct Range2 {
     int lim[2];  // keys that q tile i reaches
     int n[2];    // its key tiles, of those of the item or piece
@@ -99,7 +125,8 @@ struct Range2 {
     int nmax;
     int limmax;
 };
-__device__ __forceinline__ Range2 ranges(const Item &it, int tpt)
+// gap: key tiles out of sight before the last ones
+__device__ __forceinline__ Range2 ranges(const Item &it, int tpt, int gap)
 {
     Range2 r;
 #pragma unroll
@@ -110,7 +137,7 @@ __device__ __forceinline__ Range2 ranges(const Item &it, int tpt)
         lim = lim < 0 ? 0 : (lim > it.len ? it.len : lim);
         r.tok[i] = tok;
         r.lim[i] = lim;
-        const int n = (lim + PROMPT_KEYS - 1) / PROMPT_KEYS, most = it.j1 - it.j0;
+        const int n = (lim + PROMPT_KEYS - 1) / PROMPT_KEYS - (lim > 0 ? gap : 0), most = it.j1 - it.j0;
         r.n[i] = n - it.j0 < 0 ? 0 : (n - it.j0 > most ? most : n - it.j0);
     }
     r.nmax = r.n[0] > r.n[1] ? r.n[0] : r.n[1];
@@ -128,126 +155,6 @@ __device__ __forceinline__ Range2 uniform(Range2 r)
     r.nmax = r.n[0] > r.n[1] ? r.n[0] : r.n[1];
     return r;
 }
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t e;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
-    return e != 0;
-}
-// Keys of tile j that are multiplied, for a q tile that reaches `lim` keys: a multiple of 16.
-__device__ __forceinline__ int extent(int lim, int j)
-{
-    const int left = lim - j * PROMPT_KEYS;
-    return left >= PROMPT_KEYS ? PROMPT_KEYS : (left + 15) & ~15;
-}
-
-template <int N>
-__device__ __forceinline__ void more_registers()
-{
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void fewer_registers()
-{
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-__device__ __forceinline__ float max3(float a, float b, float c)
-{
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-// Two fp32 operations in one instruction, on a register pair.
-__device__ __forceinline__ uint64_t pair_of(float lo, float hi)
-{
-    return static_cast<uint64_t>(__float_as_uint(lo)) | (static_cast<uint64_t>(__float_as_uint(hi)) << 32);
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ float low(uint64_t a) { return __uint_as_float(static_cast<uint32_t>(a)); }
-__device__ __forceinline__ float high(uint64_t a) { return __uint_as_float(static_cast<uint32_t>(a >> 32)); }
-
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
-        : "memory");
-}
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z, int w)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
-        : "memory");
-}
-
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
-}
-// A from TMEM: 128 lanes x 8 columns, two bf16 of K per column.
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
-}
-
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *v)
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(v[0]),
-        "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
-        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(taddr)
-        : "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// kind::f16, fp32 accumulator, bf16 operands, M = 128.
-__device__ __forceinline__ constexpr uint32_t prompt_idesc(int n, bool b_mn)
-{
-    return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? (1u << 16) : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
-           (static_cast<uint32_t>(128 >> 4) << 24);
-}
-
-// V tile, MN-major (the head dimension contiguous): atoms of 8 keys x 64 columns, 1024
-// bytes apart along the keys, the second 64 columns `half` bytes further.
-__device__ __forceinline__ uint64_t smem_desc_v(uint32_t saddr, uint32_t half)
-{
-    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(half >> 4) << 16) |
-           (static_cast<uint64_t>(1024u >> 4) << 32) | (static_cast<uint64_t>(1u) << 46) | (static_cast<uint64_t>(2u) << 61);
-}
-
 // ---------------------------------------------------------------- schedule
 
 struct SeqInfo {
@@ -405,20 +312,25 @@ constexpr int MIN_SPLIT = PROMPT_WHOLE_KEYS / PROMPT_KEYS;
 // keys 15.4, 17.0 and 20.1; 300 and 1 tokens over 1409 and 3000 keys, heads of 64: 15.8, 15.9 and
 // 18.1; 20000 keys, 8 heads each way: 27.0 with any of them.
 constexpr int MIN_PIECE = 5;
-__device__ Plan plan_of(const Schedule &sc, int units, int ctas, int slots)
+// With a window the key tiles of an item are at most `cap`, whatever it reaches.
+template <bool WINDOW>
+__device__ Plan plan_of(const Schedule &sc, int units, int ctas, int slots, int cap)
 {
     Plan pl{1, 0u, static_cast<uint32_t>(sc.tiles) * units, 0};
-    if (pl.total >= static_cast<uint32_t>(ctas) || sc.cmax <= MIN_SPLIT) return pl;
+    const int cmax = WINDOW && sc.cmax > cap ? cap : sc.cmax;
+    if (pl.total >= static_cast<uint32_t>(ctas) || cmax <= MIN_SPLIT) return pl;
     // 32 limits at once, from an even share up to the longest item, closer together near the
     // first; of those that give no more pieces than there are CTAs and slots, the one of the
     // shortest longest piece.
-    int limit = static_cast<int>(sc.work() * units / ctas) + 1;
+    float work = sc.work();
+    if (WINDOW) work = fminf(work, static_cast<float>(sc.tiles) * cap);
+    int limit = static_cast<int>(work * units / ctas) + 1;
     limit = limit < MIN_PIECE ? MIN_PIECE : limit;
-    limit += static_cast<int>(static_cast<float>(sc.cmax - limit) * static_cast<float>(sc.lane * sc.lane) * (1.f / 1024.f));
-    const int n = sc.counts(limit + 1), pieces = (sc.cmax + limit - 1) / limit;
+    limit += static_cast<int>(static_cast<float>(cmax - limit) * static_cast<float>(sc.lane * sc.lane) * (1.f / 1024.f));
+    const int n = sc.counts(limit + 1), pieces = (cmax + limit - 1) / limit;
     const float split = static_cast<float>(n) * units * pieces;
-    const bool fits = limit < sc.cmax && split <= slots && split + static_cast<float>(sc.tiles - n) * units <= ctas;
-    const int longest = (sc.cmax + pieces - 1) / pieces;
+    const bool fits = limit < cmax && split <= slots && split + static_cast<float>(sc.tiles - n) * units <= ctas;
+    const int longest = (cmax + pieces - 1) / pieces;
     const int best = __reduce_min_sync(0xffffffffu, fits ? longest : INT_MAX);
     if (best == INT_MAX) return pl;
     const int pick = __ffs(static_cast<int>(__ballot_sync(0xffffffffu, fits && longest == best))) - 1;
@@ -428,6 +340,7 @@ __device__ Plan plan_of(const Schedule &sc, int units, int ctas, int slots)
     pl.total += static_cast<uint32_t>(pl.n_split * units * (pl.pieces - 1));
     return pl;
 }
+template <bool WINDOW>
 __device__ Item item_of(const Schedule &sc, const Plan &pl, int units, uint32_t g)
 {
     uint32_t rank = g;   // among the items; fewer than 2^32: T * heads rows
@@ -444,6 +357,7 @@ __device__ Item item_of(const Schedule &sc, const Plan &pl, int units, uint32_t 
     Item it = sc.at(static_cast<int>(tile), &level);
     it.unit = static_cast<int>(rank - tile * units);
     it.j0 = 0;
+    if (WINDOW && level > 0) level -= sight<WINDOW>(sc.p, it.off).gap();
     it.j1 = it.n = level;
     if (pieces > 1) {
         it.j0 = piece_begin(level, piece, pieces);
@@ -457,7 +371,7 @@ __device__ Item item_of(const Schedule &sc, const Plan &pl, int units, uint32_t 
 
 // ---------------------------------------------------------------- kernel
 
-template <int D>
+template <int D, bool WINDOW>
 __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __grid_constant__ PromptParams p)
 {
     using Sh = PromptShape<D>;
@@ -558,7 +472,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
         uint32_t n_s = 0, n_l = 0;                     // phases used
         Item it;
         for (uint32_t k = 0; next_item(k, it); ++k) {
-            const Range2 r = ranges(it, tpt);
+            const Sight<WINDOW> in = sight<WINDOW>(p, it.off);
+            const Range2 r = ranges(it, tpt, in.gap());
             if (r.n[i] == 0) continue;
             const int token = i * tpt + (row >> p.pack_shift);
             int reach = it.off + token + 1;            // keys this row sees
@@ -572,11 +487,19 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, reinterpret_cast<uint32_t *>(s) + c * 32);
                 tmem_wait_ld();
-                const int cols = reach - (it.j0 + j) * PROMPT_KEYS;
+                const int key0 = in.tile(it.j0 + j) * PROMPT_KEYS, cols = reach - key0;
                 if (cols < PROMPT_KEYS) {
 #pragma unroll
                     for (int c = 0; c < 128; ++c)
                         if (c >= cols) s[c] = -INFINITY;
+                }
+                if (WINDOW) {  // columns between the sinks and the row's window
+                    const int from = p.sinks - key0, to = it.off + token - p.window + 1 - key0;
+                    if (to > 0 && from < PROMPT_KEYS) {
+#pragma unroll
+                        for (int c = 0; c < 128; ++c)
+                            if (c >= from && c < to) s[c] = -INFINITY;
+                    }
                 }
                 float mx[4] = {m, m, m, m};
 #pragma unroll
@@ -663,13 +586,15 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                 arrive(join_go);
             }
             if (alive && wait(join_go, 0)) {
-                const Range2 r = ranges(it, tpt);
+                const int gap = sight<WINDOW>(p, it.off).gap();
+                const Range2 r = ranges(it, tpt, gap);
                 const int per = D / 16;                // units of a q tile
                 for (int u = it.piece + it.pieces * i; u < 2 * per; u += 2 * it.pieces) {
                     const int t = u / per, c = (u - t * per) * 16;
                     const int rows_tok = t == 0 ? r.tok[0] : r.tok[1], lim = t == 0 ? r.lim[0] : r.lim[1];
                     if (rows_tok == 0) continue;
-                    const int n = (lim + PROMPT_KEYS - 1) / PROMPT_KEYS;  // key tiles that q tile t reaches
+                    // key tiles that q tile t reaches
+                    const int n = (lim + PROMPT_KEYS - 1) / PROMPT_KEYS - (lim > 0 ? gap : 0);
                     const float *rows = p.ws_rows + static_cast<int64_t>(it.slot) * 512 + t * 128 + row;
                     const float4 *cols = reinterpret_cast<const float4 *>(p.ws) + static_cast<int64_t>(it.slot) * (64 * D) +
                                          c / 4 * 256 + t * 128 + row;
@@ -740,7 +665,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
         uint32_t n_o[2] = {0, 0};
         Item it;
         for (uint32_t k = 0; next_item(k, it); ++k) {
-            const Range2 r = ranges(it, tpt);
+            const Range2 r = ranges(it, tpt, sight<WINDOW>(p, it.off).gap());
             // A split item's part: [columns / 4][256 rows][4] fp32 and the rows' maxima and sums.
             float4 *part_o = reinterpret_cast<float4 *>(p.ws) + static_cast<int64_t>(it.slot + it.piece) * (64 * D) + row;
             float *part_m = p.ws_rows + static_cast<int64_t>(it.slot + it.piece) * 512 + row;
@@ -823,7 +748,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
         for (uint32_t k = 0;; ++k) {
             if (k >= 2) arrive(want);                  // every load of item k - 1 has been issued
             if (!next_item(k, it)) break;
-            const Range2 r = ranges(it, tpt);
+            const Sight<WINDOW> in = sight<WINDOW>(p, it.off);
+            const Range2 r = ranges(it, tpt, in.gap());
             const int kvh = (it.unit << p.pack_shift) / p.group;
             const int32_t *table = p.paged ? p.b.page_table + it.src * p.b.table_row : nullptr;
             const int pages = p.paged ? (it.len + (1 << p.b.page_shift) - 1) >> p.b.page_shift : 0;
@@ -842,16 +768,20 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
             };
             load_q(0);
             for (int j = 0; j < r.nmax && alive; ++j) {
-                const int key0 = (it.j0 + j) * PROMPT_KEYS;
+                const int kt = in.tile(it.j0 + j), key0 = kt * PROMPT_KEYS;
                 // every key that is multiplied is loaded (pages past the length as zeros)
-                const int n_box = p.paged ? (extent(r.limmax, it.j0 + j) + box - 1) / box : 1;
+                const int n_box = p.paged ? (extent(r.limmax, kt) + box - 1) / box : 1;
                 const int page0 = key0 >> p.b.page_shift;
                 const int boxes = PROMPT_KEYS / box;
                 if (p.paged && page0 + boxes > cached0 + cached_n) {
                     cached0 = page0;
                     cached_n = 32;
-                    ids = cached0 + lane < pages ? table[cached0 + lane] : -1;
-                    if (cached0 + lane < pages && (ids < 0 || ids >= p.b.num_pages)) {
+                    // a page that no row sees may be another sequence's by now, or nobody's
+                    const int64_t first = static_cast<int64_t>(cached0 + lane) << p.b.page_shift;
+                    const bool seen = cached0 + lane < pages &&
+                                      (!WINDOW || first + (int64_t(1) << p.b.page_shift) > in.lo || first < p.sinks);
+                    ids = seen ? table[cached0 + lane] : -1;
+                    if (seen && (ids < 0 || ids >= p.b.num_pages)) {
                         atomicCAS(p.b.status, 0, UB_ERR_ARG);
                         ids = -1;                      // outside the tensor: filled with zeros
                     }
@@ -870,7 +800,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                         two = (two & ~(1u << at)) | (static_cast<uint32_t>(kind == 0 && j > 0) << at);
                     }
                     // The last tile of V goes through the zeroing warp when it ends inside 16 keys.
-                    const bool fix = kind == 1 && j == r.nmax - 1 && extent(r.limmax, it.j0 + j) > it.len - key0;
+                    const bool fix = kind == 1 && j == r.nmax - 1 && extent(r.limmax, kt) > it.len - key0;
                     const uint32_t bar = (fix ? v_raw : kv_full) + 8 * st;
                     const CUtensorMap *map = kind == 0 ? &p.tmK : &p.tmV;
                     const uint32_t dst = sm_kv + st * Sh::TILE_BYTES;
@@ -919,7 +849,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
         };
         Item it;
         for (uint32_t k = 0; next_item(k, it); ++k) {
-            const Range2 r = uniform(ranges(it, tpt));
+            Sight<WINDOW> in = sight<WINDOW>(p, it.off);
+            if (WINDOW) in.near = __shfl_sync(0xffffffffu, in.near, 0), in.far = __shfl_sync(0xffffffffu, in.far, 0);
+            const Range2 r = uniform(ranges(it, tpt, in.gap()));
             const int n = i == 0 ? r.n[0] : r.n[1], lim = i == 0 ? r.lim[0] : r.lim[1];
             const int j0 = __shfl_sync(0xffffffffu, it.j0, 0);
             if (n > 0) {
@@ -938,9 +870,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                 if (!in_turn(step - 1 + i)) break;
                 const uint64_t v = v_desc + ((c - 1) % NST) * (Sh::TILE_BYTES / 16);
                 const uint64_t kk = k_desc + (c % NST) * (Sh::TILE_BYTES / 16);
-                const int steps = pv ? extent(lim, j0 + j) / 16 : 0;
-                const uint32_t s_idesc = prompt_idesc(s_next ? extent(lim, j0 + j + 1) : 16, false);
-                constexpr uint32_t o_idesc = prompt_idesc(D, true);
+                const int steps = pv ? extent(lim, in.tile(j0 + j)) / 16 : 0;
+                const uint32_t s_idesc = attn_idesc(s_next ? extent(lim, in.tile(j0 + j + 1)) : 16, false);
+                constexpr uint32_t o_idesc = attn_idesc(D, true);
                 if (pv) {
                     if (EARLY) {
                         if (!wait(p_part + 8 * i, n_p & 1)) break;
@@ -1007,15 +939,20 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
             // Items of one q tile where those are no more than the CTAs and are not split, of two
             // elsewhere.
             sched.shift = 7 - p.pack_shift;
+            int cap = INT_MAX;
             for (;; ++sched.shift) {
                 sched.measure();
+                // key tiles in sight of an item: its rows' windows, and the sinks
+                if (WINDOW)
+                    cap = static_cast<int>((static_cast<int64_t>(p.window) + (1 << sched.shift) + 2 * PROMPT_KEYS - 3) / PROMPT_KEYS) +
+                          (p.sinks + PROMPT_KEYS - 1) / PROMPT_KEYS;
                 if (sched.shift == 8 - p.pack_shift ||
-                    (static_cast<uint32_t>(sched.tiles) * p.units <= gridDim.x && sched.cmax <= MIN_SPLIT))
+                    (static_cast<uint32_t>(sched.tiles) * p.units <= gridDim.x && (sched.cmax <= MIN_SPLIT || cap <= MIN_SPLIT)))
                     break;
             }
-            plan = plan_of(sched, p.units, gridDim.x, p.slots);
+            plan = plan_of<WINDOW>(sched, p.units, gridDim.x, p.slots, cap);
             it = kNoItem;
-            if (blockIdx.x < plan.total) it = item_of(sched, plan, p.units, blockIdx.x);
+            if (blockIdx.x < plan.total) it = item_of<WINDOW>(sched, plan, p.units, blockIdx.x);
         }
         // Longest first. The first two items of each CTA are dealt forth and back over the CTAs,
         // the rest by tickets, drawn when the loads of the item before have been issued.
@@ -1032,7 +969,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                 g = 2 * gridDim.x + __shfl_sync(0xffffffffu, ticket, 0);
             }
             Item drawn = kNoItem;
-            if (g < plan.total) drawn = item_of(sched, plan, p.units, g);
+            if (g < plan.total) drawn = item_of<WINDOW>(sched, plan, p.units, g);
             publish(k, drawn);
             return drawn;
         };
@@ -1047,9 +984,10 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                 it1 = draw(k + 1);
                 if (!alive) break;
             }
-            const Range2 r = ranges(it, tpt);
-            const int j = r.nmax - 1, valid = it.len - (it.j0 + j) * PROMPT_KEYS;
-            const int ext = r.nmax > 0 ? extent(r.limmax, it.j0 + j) : 0;
+            const Sight<WINDOW> in = sight<WINDOW>(p, it.off);
+            const Range2 r = ranges(it, tpt, in.gap());
+            const int j = r.nmax - 1, kt = in.tile(it.j0 + j), valid = it.len - kt * PROMPT_KEYS;
+            const int ext = r.nmax > 0 ? extent(r.limmax, kt) : 0;
             if (ext > valid) {
                 const uint32_t st = (c + 2 * j + 1) % NST;
                 if (!wait(v_raw + 8 * st, (used >> st) & 1)) break;
@@ -1077,19 +1015,21 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
     if (threadIdx.x == 0 && atomicAdd(p.tickets + 1, 1u) == gridDim.x - 1) p.tickets[0] = p.tickets[1] = 0u;
 }
 
-template <int D>
+template <int D, bool WINDOW>
 cudaError_t launch_prompt(const PromptParams &p, int grid, cudaStream_t s)
 {
-    const cudaError_t e = raise_smem_limit(reinterpret_cast<const void *>(ub_attn_prompt_kernel<D>), PromptShape<D>::SMEM);
+    const cudaError_t e =
+        raise_smem_limit(reinterpret_cast<const void *>(ub_attn_prompt_kernel<D, WINDOW>), PromptShape<D>::SMEM);
     if (e != cudaSuccess) return e;
-    return launch_ex(ub_attn_prompt_kernel<D>, p, grid, PR_THREADS, PromptShape<D>::SMEM, 1, p.pdl != 0, s);
+    return launch_ex(ub_attn_prompt_kernel<D, WINDOW>, p, grid, PR_THREADS, PromptShape<D>::SMEM, 1, p.pdl != 0, s);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_prompt(const PromptParams &p, int grid, cudaStream_t s)
 {
-    return p.head_dim == 128 ? launch_prompt<128>(p, grid, s) : launch_prompt<64>(p, grid, s);
+    if (p.window > 0) return p.head_dim == 128 ? launch_prompt<128, true>(p, grid, s) : launch_prompt<64, true>(p, grid, s);
+    return p.head_dim == 128 ? launch_prompt<128, false>(p, grid, s) : launch_prompt<64, false>(p, grid, s);
 }
 
 }  // namespace ubk

@@ -7,7 +7,9 @@
 // the pair j being elements (j, j + rot/2) of the head, or (2j, 2j + 1) when interleaved;
 // elements from rot on are copied. The query goes to q_out, the key and the value to row
 // pos % page_size of page page_table[s][pos / page_size]. The arithmetic is fp32, with one
-// rounding to BF16.
+// rounding to BF16. A draft of ub_kv_append_tree is stored at pos, but turned by the position that
+// it has on its path: the text's length and the number of its ancestors, which the warp counts
+// along the parents (neighbouring words, so a step costs a hit in L1).
 //
 // Bound by HBM: every byte is read once and written once. A warp owns a token: it finds
 // the token's sequence with one round of loads (each lane compares some of the starts and
@@ -104,7 +106,21 @@ __global__ void __launch_bounds__(APPEND_THREADS) ub_kv_append_kernel(const __gr
     const int64_t start = p.b.seq_starts[seq], end = min(p.b.seq_starts[seq + 1], p.T);
     if (t < start || t >= end) return;   // starts out of order: no sequence
     const int64_t pos = p.b.kv_lens[seq] - (end - start) + (t - start);
-    if (pos < 0 || (p.rot > 0 && pos >= p.max_pos)) {
+    int64_t turn = pos;                  // row of the rotation tables
+    if (p.parents != nullptr) {          // a draft: as many positions past the text as it has ancestors
+        const int64_t first = start < 0 ? 0 : start;
+        turn = pos - (t - first);
+        int64_t at = t - first;
+        for (int64_t up = p.parents[t]; up != -1; up = p.parents[first + at]) {
+            if (up < 0 || up >= at) {
+                if (lane == 0) atomicCAS(p.b.status, 0, UB_ERR_ARG);
+                break;
+            }
+            at = up;
+            ++turn;
+        }
+    }
+    if (pos < 0 || turn < 0 || (p.rot > 0 && turn >= p.max_pos)) {
         if (lane == 0) atomicCAS(p.b.status, 0, UB_ERR_ARG);
         return;
     }
@@ -122,8 +138,8 @@ __global__ void __launch_bounds__(APPEND_THREADS) ub_kv_append_kernel(const __gr
     const int v1 = turns && !p.interleaved ? slot + half : 2 * slot + 1;
     float c[8], s[8];
     if (turns) {
-        const float4 *cp = reinterpret_cast<const float4 *>(p.cos + pos * (p.rot / 2) + slot * 8);
-        const float4 *sp = reinterpret_cast<const float4 *>(p.sin + pos * (p.rot / 2) + slot * 8);
+        const float4 *cp = reinterpret_cast<const float4 *>(p.cos + turn * (p.rot / 2) + slot * 8);
+        const float4 *sp = reinterpret_cast<const float4 *>(p.sin + turn * (p.rot / 2) + slot * 8);
         *reinterpret_cast<float4 *>(c) = cp[0];
         *reinterpret_cast<float4 *>(c + 4) = cp[1];
         *reinterpret_cast<float4 *>(s) = sp[0];

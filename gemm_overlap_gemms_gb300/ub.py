@@ -32,7 +32,7 @@ OPTIONS = {"sm_margin": 1, "timeout_ns": 2, "self_rank": 3, "drop_flag": 4, "pro
            "cta_pair": 6, "streamk": 7, "copy_streams": 8, "gather_kernel": 9, "skinny": 10, "pdl": 11,
            "bulk_beside": 12, "gather_chain": 13}
 OPS = {"ag": 0, "rs": 1, "ag_swiglu": 2, "ag_kn": 3, "rs_kn": 4, "wgrad": 5, "reduce_scatter": 6, "kv_append": 7,
-       "attn_prompt": 8, "attn_decode": 9}
+       "attn_prompt": 8, "attn_decode": 9, "attn_tree": 10, "kv_accept": 11, "kv_pages": 12, "kv_copy": 13}
 MAX_TP = 8
 EXPORTS = [
     "ub_create", "ub_destroy", "ub_set_active_shape", "ub_set_active_shape_nd",
@@ -43,8 +43,11 @@ EXPORTS = [
     "ub_allgather", "ub_reduce_scatter", "ub_plan_tail_split", "ub_plan_path",
     "ub_plan_ag_self_head", "ag_gemm_from_buffer", "ub_plan_gather_parts", "ub_stream_read",
     "ub_plan_ag_group_m", "ub_kv_append", "ub_attn_prompt", "ub_attn_decode",
+    "ub_attn_prompt_window", "ub_attn_decode_window", "ub_kv_append_tree", "ub_attn_tree", "ub_kv_accept",
+    "ub_kv_take", "ub_kv_free", "ub_kv_fork", "ub_kv_compact", "ub_kv_copy",
 ]
 NOALLOC_MAX_ELEMS = 16 * 1024 * 1024
+ACCEPT_MOST = 2048  # drafts of a sequence in kv_accept
 
 
 class UbError(RuntimeError):
@@ -115,6 +118,16 @@ def load():
         "ub_kv_append": [P, ctypes.c_char_p, P],
         "ub_attn_prompt": [P, ctypes.c_char_p, P],
         "ub_attn_decode": [P, ctypes.c_char_p, P],
+        "ub_attn_prompt_window": [P, ctypes.c_char_p, I, I, P],
+        "ub_attn_decode_window": [P, ctypes.c_char_p, I, I, P],
+        "ub_kv_append_tree": [P, ctypes.c_char_p, P, P],
+        "ub_attn_tree": [P, ctypes.c_char_p, P, I, I, P],
+        "ub_kv_accept": [P, ctypes.c_char_p, P, I64, P, P, P],
+        "ub_kv_take": [P, ctypes.c_char_p, P, P, P],
+        "ub_kv_free": [P, ctypes.c_char_p, P, P, P],
+        "ub_kv_fork": [P, ctypes.c_char_p, P, P, I64, P, I64, P, P],
+        "ub_kv_compact": [P, ctypes.c_char_p, P, P, I64, P, I64, P, P],
+        "ub_kv_copy": [P, ctypes.c_char_p, P, I64, P],
         "ub_plan_gather_parts": [I, I, I64, I64, ctypes.POINTER(I), ctypes.POINTER(I64), ctypes.POINTER(I64),
                                  ctypes.POINTER(I)],
     }
@@ -221,6 +234,8 @@ def _bf16_cuda(t: torch.Tensor, name: str, shape=None, device=None):
 # decoding step's call takes microseconds): 8 ints, scale, reserved, 4 sizes, four
 # [data, row, head], two [data, page, head, row], six pointers.
 _ATTN = struct.Struct("=I7ifI4q" + "Q2q" * 4 + "Q3q" * 2 + "6Q")
+# ub_pool_t: four ints, three sizes, two pointers.
+_POOL = struct.Struct("=I2iI3q2Q")
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 # What a wrong argument raises while its view is read; the checks below are on the path of
 # every decoding step, so each argument is read once and its faults are named afterwards.
@@ -289,7 +304,7 @@ def _ints(t: torch.Tensor, name: str, n: int | None, device: int):
     _attn_error(t, name, _I32, device, "[%s] and contiguous" % ("n" if n is None else n))
 
 
-def _table(t: torch.Tensor, n: int, device: int):
+def _table(t: torch.Tensor, n: int, device: int, name: str = "page_table"):
     """(data, entries, row) of a page table."""
     try:
         rows, width = t.shape
@@ -298,7 +313,33 @@ def _table(t: torch.Tensor, n: int, device: int):
             return t.data_ptr(), width, row
     except _UNREADABLE:
         pass
-    _attn_error(t, "page_table", _I32, device, "[%d, entries] with a contiguous last dimension" % n)
+    _attn_error(t, name, _I32, device, "[%d, entries] with a contiguous last dimension" % n)
+
+
+def _tall(t, name: str) -> int:
+    """The rows of a table (what else is wrong with it _table says)."""
+    try:
+        return t.shape[0]
+    except _UNREADABLE + (IndexError,):
+        raise TypeError("%s must be a torch.Tensor [rows, entries]" % name) from None
+
+
+def _pairs(t: torch.Tensor, name: str, n: int | None, device: int):
+    """(data, pairs) of a contiguous int32 [pairs, 2]."""
+    try:
+        length, two = t.shape
+        if two == 2 and (n is None or length == n) and t.is_contiguous() and t.dtype is _I32 and t.get_device() == device:
+            return t.data_ptr(), length
+    except _UNREADABLE:
+        pass
+    _attn_error(t, name, _I32, device, "[%s, 2] and contiguous" % ("n" if n is None else n))
+
+
+def _sight(window, sinks) -> bool:
+    """Whether a window is asked for; window and sinks are checked here, for struct and ctypes do not."""
+    if window is None or window < 0 or sinks < 0 or window > 0x7fffffff or sinks > 0x7fffffff:
+        raise ValueError("window %r, sinks %r: counts of tokens are needed (window 0: all)" % (window, sinks))
+    return window > 0
 
 
 def _rotations(t: torch.Tensor, name: str, shape, device: int):
@@ -645,7 +686,7 @@ class UserBuffer:
         return lse, lse.data_ptr()
 
     def kv_append(self, q, k, v, cos, sin, seq_starts, kv_lens, page_table, k_cache, v_cache, q_out=None,
-                  interleaved: bool = False, stream=None):
+                  interleaved: bool = False, stream=None, parents=None):
         """Rotate q and k of the active tokens by their positions and store k and v in the paged
         cache (ub_kv_append). Returns the rotated queries.
 
@@ -653,7 +694,9 @@ class UserBuffer:
         strides that are multiples of 8; D 64 or 128. cos, sin: fp32 [positions, rot / 2], rot a
         multiple of 16 up to D (None: no rotation). seq_starts int32 [n + 1], kv_lens int32 [n]
         (the tokens of this call included), page_table int32 [n, entries], on the device.
-        k_cache, v_cache [pages, kv_heads, page_size, D]. q_out: like q, q itself allowed."""
+        k_cache, v_cache [pages, kv_heads, page_size, D]. q_out: like q, q itself allowed.
+        parents: int32 [T], the tokens are drafts (ub_kv_append_tree; see attn_tree), each rotated
+        by its position along its path."""
         dev = self._dev
         T, _ = self._active or self.active_shape
         D = _head_dim(q)
@@ -673,16 +716,23 @@ class UserBuffer:
         q_out, op, o0, o1 = self._out(q_out, "q_out", T, H, D, stream)
         a = _ATTN.pack(_ATTN.size, n, H, G, D, page, rot, 1 if interleaved else 0, 1.0, 0, pages, width, table_row,
                        positions, qp, q0, q1, kp, k0, k1, vp, v0, v1, op, o0, o1, *caches, starts, lens, table, cp, sp, 0)
-        rc = (_lib or load()).ub_kv_append(self._h, a, self._raw_stream(stream))
+        if parents is None:
+            rc = (_lib or load()).ub_kv_append(self._h, a, self._raw_stream(stream))
+        else:
+            rc = (_lib or load()).ub_kv_append_tree(self._h, a, _ints(parents, "parents", T, dev)[0], self._raw_stream(stream))
         if rc:
             _check(rc)
         return q_out
 
-    def attn_prompt(self, q, k, v, seq_starts, out=None, lse=None, scale: float | None = None, stream=None):
+    def attn_prompt(self, q, k, v, seq_starts, out=None, lse=None, scale: float | None = None, stream=None,
+                    window: int = 0, sinks: int = 0):
         """Causal attention of whole packed prompts (ub_attn_prompt): sequence s is rows
         [seq_starts[s], seq_starts[s + 1]) of q [T, heads, D] and of k, v [T, kv_heads, D].
         scale: 1 / sqrt(D) if None. lse: an fp32 [T, heads] tensor, or True for a new one.
-        Returns out, or (out, lse) where lse is asked for. Rows of no sequence stay as they are."""
+        Returns out, or (out, lse) where lse is asked for. Rows of no sequence stay as they are.
+        window > 0: a token sees the last `window` tokens, itself included, and the first `sinks`
+        of its sequence (ub_attn_prompt_window)."""
+        near = _sight(window, sinks)
         dev = self._dev
         T, _ = self._active or self.active_shape
         D = _head_dim(q)
@@ -696,15 +746,20 @@ class UserBuffer:
         lse, lp = self._lse(lse, T, H, stream)
         a = _ATTN.pack(_ATTN.size, n - 1, H, G, D, 0, 0, 0, D ** -0.5 if scale is None else scale, 0, 0, 0, 0, 0,
                        qp, q0, q1, kp, k0, k1, vp, v0, v1, op, o0, o1, 0, 0, 0, 0, 0, 0, 0, 0, starts, 0, 0, 0, 0, lp)
-        rc = (_lib or load()).ub_attn_prompt(self._h, a, self._raw_stream(stream))
+        if near:
+            rc = (_lib or load()).ub_attn_prompt_window(self._h, a, window, sinks, self._raw_stream(stream))
+        else:
+            rc = (_lib or load()).ub_attn_prompt(self._h, a, self._raw_stream(stream))
         if rc:
             _check(rc)
         return out if lse is None else (out, lse)
 
     def attn_prompt_paged(self, q, k_cache, v_cache, seq_starts, kv_lens, page_table, out=None, lse=None,
-                          scale: float | None = None, stream=None):
+                          scale: float | None = None, stream=None, window: int = 0, sinks: int = 0):
         """Causal attention of prompts, or of chunks of prompts, over the paged cache that holds
-        their keys and values (after kv_append); arguments as there and in attn_prompt."""
+        their keys and values (after kv_append); arguments as there and in attn_prompt. With a
+        window, entries of page_table whose pages no token sees are not looked at."""
+        near = _sight(window, sinks)
         dev = self._dev
         T, _ = self._active or self.active_shape
         D = _head_dim(q)
@@ -719,16 +774,20 @@ class UserBuffer:
         lse, lp = self._lse(lse, T, H, stream)
         a = _ATTN.pack(_ATTN.size, n, H, G, D, page, 0, 0, D ** -0.5 if scale is None else scale, 0, pages, width,
                        table_row, 0, qp, q0, q1, 0, 0, 0, 0, 0, 0, op, o0, o1, *caches, starts, lens, table, 0, 0, lp)
-        rc = (_lib or load()).ub_attn_prompt(self._h, a, self._raw_stream(stream))
+        if near:
+            rc = (_lib or load()).ub_attn_prompt_window(self._h, a, window, sinks, self._raw_stream(stream))
+        else:
+            rc = (_lib or load()).ub_attn_prompt(self._h, a, self._raw_stream(stream))
         if rc:
             _check(rc)
         return out if lse is None else (out, lse)
 
     def attn_decode(self, q, k_cache, v_cache, kv_lens, page_table, out=None, lse=None, scale: float | None = None,
-                    stream=None):
+                    stream=None, window: int = 0, sinks: int = 0):
         """Attention of one new token per sequence over the paged cache (ub_attn_decode): row s of
         q [T, heads, D] is sequence s, n = kv_lens.shape[0] <= T; arguments as in kv_append and
-        attn_prompt. Rows from n on stay as they are."""
+        attn_prompt (window and sinks: ub_attn_decode_window). Rows from n on stay as they are."""
+        near = _sight(window, sinks)
         dev = self._dev
         T, _ = self._active or self.active_shape
         D = _head_dim(q)
@@ -740,10 +799,153 @@ class UserBuffer:
         lse, lp = self._lse(lse, T, H, stream)
         a = _ATTN.pack(_ATTN.size, n, H, G, D, page, 0, 0, D ** -0.5 if scale is None else scale, 0, pages, width,
                        table_row, 0, qp, q0, q1, 0, 0, 0, 0, 0, 0, op, o0, o1, *caches, 0, lens, table, 0, 0, lp)
-        rc = (_lib or load()).ub_attn_decode(self._h, a, self._raw_stream(stream))
+        if near:
+            rc = (_lib or load()).ub_attn_decode_window(self._h, a, window, sinks, self._raw_stream(stream))
+        else:
+            rc = (_lib or load()).ub_attn_decode(self._h, a, self._raw_stream(stream))
         if rc:
             _check(rc)
         return out if lse is None else (out, lse)
+
+    def attn_tree(self, q, k_cache, v_cache, seq_starts, kv_lens, page_table, parents, out=None, lse=None,
+                  scale: float | None = None, stream=None, window: int = 0, sinks: int = 0):
+        """Attention of drafted tokens over the paged cache that holds the text and them
+        (ub_attn_tree): rows [seq_starts[s], seq_starts[s + 1]) of q are the drafts of sequence s,
+        the last of its kv_lens[s] cached tokens. parents int32 [T]: the draft that each token
+        follows, counted within its sequence and before it, or -1: the text. A draft sees the text,
+        its ancestors and itself. Other arguments as in attn_prompt_paged."""
+        near = _sight(window, sinks)
+        dev = self._dev
+        T, _ = self._active or self.active_shape
+        D = _head_dim(q)
+        qp, q0, q1, H = _heads_view(q, "q", T, D, dev)
+        caches, pages, G, page = _caches(k_cache, v_cache, D, dev)
+        lens, n = _ints(kv_lens, "kv_lens", None, dev)
+        starts, _ = _ints(seq_starts, "seq_starts", n + 1, dev)
+        up, _ = _ints(parents, "parents", T, dev)
+        table, width, table_row = _table(page_table, n, dev)
+        out, op, o0, o1 = self._out(out, "out", T, H, D, stream)
+        lse, lp = self._lse(lse, T, H, stream)
+        a = _ATTN.pack(_ATTN.size, n, H, G, D, page, 0, 0, D ** -0.5 if scale is None else scale, 0, pages, width,
+                       table_row, 0, qp, q0, q1, 0, 0, 0, 0, 0, 0, op, o0, o1, *caches, starts, lens, table, 0, 0, lp)
+        rc = (_lib or load()).ub_attn_tree(self._h, a, up, window, sinks if near else 0, self._raw_stream(stream))
+        if rc:
+            _check(rc)
+        return out if lse is None else (out, lse)
+
+    def kv_accept(self, k_cache, v_cache, seq_starts, kv_lens, page_table, parents, leaves, new_lens=None, stream=None):
+        """Keep the accepted drafts (ub_kv_accept): leaves int32 [n] names the last accepted draft of
+        each sequence, -1 for none; the cached rows of its path move together behind the text.
+        Returns new_lens int32 [n], the lengths with the accepted drafts. parents has an entry per
+        draft, whatever the active shape is now; kv_lens stays as it is, for the other layers'
+        caches."""
+        dev = self._dev
+        try:
+            D = k_cache.shape[3]
+        except (AttributeError, IndexError, TypeError):
+            D = -1
+        caches, pages, G, page = _caches(k_cache, v_cache, D, dev)
+        lens, n = _ints(kv_lens, "kv_lens", None, dev)
+        starts, _ = _ints(seq_starts, "seq_starts", n + 1, dev)
+        up, tokens = _ints(parents, "parents", None, dev)
+        last, _ = _ints(leaves, "leaves", n, dev)
+        table, width, table_row = _table(page_table, n, dev)
+        if new_lens is None:
+            new_lens = self._new((n,), _I32, stream)
+        to, _ = _ints(new_lens, "new_lens", n, dev)
+        a = _ATTN.pack(_ATTN.size, n, G, G, D, page, 0, 0, 1.0, 0, pages, width, table_row, 0, *[0] * 12, *caches,
+                       starts, lens, table, 0, 0, 0)
+        rc = (_lib or load()).ub_kv_accept(self._h, a, up, tokens, last, to, self._raw_stream(stream))
+        if rc:
+            _check(rc)
+        return new_lens
+
+    # -- pages of the cache
+    def _pool(self, refs, page_table, page_size: int, n: int):
+        refs_p, pages = _ints(refs, "refs", None, self._dev)
+        table, width, row = _table(page_table, n, self._dev)
+        return _POOL.pack(_POOL.size, n, page_size, 0, pages, width, row, refs_p, table), pages, width
+
+    def kv_take(self, refs, page_table, begin, end, page_size: int, stream=None):
+        """Pages for the cache rows [begin[s], end[s]) of every sequence (ub_kv_take): each missing
+        entry (-1) of page_table int32 [n, entries] among them gets a free page, the lowest first.
+        refs int32 [pages]: how many table entries name a page, 0: free. In place."""
+        n = _tall(page_table, "page_table")
+        pool, _, _ = self._pool(refs, page_table, page_size, n)
+        b, _ = _ints(begin, "begin", n, self._dev)
+        e, _ = _ints(end, "end", n, self._dev)
+        rc = (_lib or load()).ub_kv_take(self._h, pool, b, e, self._raw_stream(stream))
+        if rc:
+            _check(rc)
+
+    def kv_free(self, refs, page_table, begin, end, page_size: int, stream=None):
+        """Give up the pages that lie wholly within the cache rows [begin[s], end[s]) of every sequence
+        (ub_kv_free): their entries become -1, their counts go down. `end` may lie past the table."""
+        n = _tall(page_table, "page_table")
+        pool, _, _ = self._pool(refs, page_table, page_size, n)
+        b, _ = _ints(begin, "begin", n, self._dev)
+        e, _ = _ints(end, "end", n, self._dev)
+        rc = (_lib or load()).ub_kv_free(self._h, pool, b, e, self._raw_stream(stream))
+        if rc:
+            _check(rc)
+
+    def kv_fork(self, refs, page_table, kv_lens, source, new_table, page_size: int, copies=None, stream=None):
+        """Fork sequences (ub_kv_fork): row i of new_table int32 [children, entries] becomes row
+        source[i] of page_table, whole pages shared, a last page that is filled in part replaced by
+        a free one. Returns copies int32 [children, 2], (from, to) of those or (-1, -1): the data to
+        copy with kv_copy, in every layer's cache. new_table overlaps page_table nowhere."""
+        dev = self._dev
+        pool, _, width = self._pool(refs, page_table, page_size, _tall(page_table, "page_table"))
+        lens, _ = _ints(kv_lens, "kv_lens", page_table.shape[0], dev)
+        src, m = _ints(source, "source", None, dev)
+        to, new_width, new_row = _table(new_table, m, dev, "new_table")
+        if new_width != width:
+            raise ValueError("new_table has %d entries per row, page_table %d" % (new_width, width))
+        if copies is None:
+            copies = self._new((m, 2), _I32, stream)
+        pairs, _ = _pairs(copies, "copies", m, dev)
+        rc = (_lib or load()).ub_kv_fork(self._h, pool, lens, src, m, to, new_row, pairs, self._raw_stream(stream))
+        if rc:
+            _check(rc)
+        return copies
+
+    def kv_compact(self, refs, page_table, refs_out=None, table_out=None, moves=None, used=None, stream=None):
+        """Move the pages in use together into the first ones (ub_kv_compact). Returns (moves, used):
+        moves int32 [>= pages / 2, 2], (from, to) and then (-1, -1), for kv_copy; used int32 [1],
+        the number of pages in use. refs and page_table change in place unless refs_out and
+        table_out are given. Every table on the pool has to be rows of page_table."""
+        dev = self._dev
+        n = _tall(page_table, "page_table")
+        pool, pages, width = self._pool(refs, page_table, 8, n)  # the page size plays no part
+        r, _ = _ints(refs if refs_out is None else refs_out, "refs_out", pages, dev)
+        t, new_width, row = _table(page_table if table_out is None else table_out, n, dev, "table_out")
+        if new_width != width:
+            raise ValueError("table_out has %d entries per row, page_table %d" % (new_width, width))
+        if moves is None:
+            moves = self._new((pages // 2, 2), _I32, stream)
+        if used is None:
+            used = self._new((1,), _I32, stream)
+        m, room = _pairs(moves, "moves", None, dev)
+        u, _ = _ints(used, "used", 1, dev)
+        rc = (_lib or load()).ub_kv_compact(self._h, pool, r, t, row, m, room, u, self._raw_stream(stream))
+        if rc:
+            _check(rc)
+        return moves, used
+
+    def kv_copy(self, k_cache, v_cache, pairs, stream=None):
+        """Copy pages (ub_kv_copy): page pairs[i, 0] of both caches to page pairs[i, 1]; pairs int32
+        [n, 2] on the device, (-1, -1) is skipped."""
+        dev = self._dev
+        try:
+            D = k_cache.shape[3]
+        except (AttributeError, IndexError, TypeError):
+            D = -1
+        caches, pages, G, page = _caches(k_cache, v_cache, D, dev)
+        p, n = _pairs(pairs, "pairs", None, dev)
+        a = _ATTN.pack(_ATTN.size, 1, G, G, D, page, 0, 0, 1.0, 0, pages, 1, 1, 0, *[0] * 12, *caches, *[0] * 6)
+        rc = (_lib or load()).ub_kv_copy(self._h, a, p, n, self._raw_stream(stream))
+        if rc:
+            _check(rc)
 
 
 def ag_gemm_noalloc(shards, Wt: torch.Tensor, Y: torch.Tensor | None = None, stream=None):

@@ -137,7 +137,11 @@ enum {
     UB_OP_KV_APPEND = 7,
     UB_OP_ATTN_PROMPT = 8,
     UB_OP_ATTN_DECODE = 9,
-    UB_NUM_OPS = 10
+    UB_OP_ATTN_TREE = 10,
+    UB_OP_KV_ACCEPT = 11,
+    UB_OP_KV_PAGES = 12, /* ub_kv_take, ub_kv_free, ub_kv_fork, ub_kv_compact */
+    UB_OP_KV_COPY = 13,
+    UB_NUM_OPS = 14
 };
 
 /*
@@ -457,6 +461,113 @@ typedef struct {
 int ub_kv_append(ub_handle_t h, const ub_attn_t *a, void *stream);
 int ub_attn_prompt(ub_handle_t h, const ub_attn_t *a, void *stream);
 int ub_attn_decode(ub_handle_t h, const ub_attn_t *a, void *stream);
+
+/*
+ * Attention with a sliding window and a few first tokens that stay visible (sinks):
+ * ub_attn_prompt and ub_attn_decode as above, but a row at position `pos` sees only the keys
+ *     j <= pos  with  j > pos - window  or  j < sinks.
+ * window = 0: all keys (sinks then mean nothing). The key tiles that no row of a work item sees
+ * are not loaded, and a page that no row of it sees is not looked at: its table entry may be -1
+ * or another sequence's page (ub_kv_free hands it on). A page of which a row sees a part has to
+ * be the sequence's, its rows up to kv_lens finite.
+ * Errors: as ub_attn_prompt and ub_attn_decode; UB_ERR_ARG for window or sinks below zero.
+ */
+int ub_attn_prompt_window(ub_handle_t h, const ub_attn_t *a, int32_t window, int32_t sinks, void *stream);
+int ub_attn_decode_window(ub_handle_t h, const ub_attn_t *a, int32_t window, int32_t sinks, void *stream);
+
+/*
+ * Drafted tokens. The new tokens of sequence s, at most as many as its rows, are drafts that form
+ * a tree (or several) on top of the text, the first L_s = kv_lens[s] - n_s tokens of the cache:
+ * parents[t] is the draft that token t follows, counted within its sequence, or -1 where it
+ * follows the text. A parent comes before its children. Draft i is stored at place L_s + i of the
+ * cache; its position, by which it is rotated, is L_s + (number of its ancestors).
+ *
+ * ub_kv_append_tree: ub_kv_append, each draft rotated by its position and stored at its place.
+ *
+ * ub_attn_tree: attention of the drafts over the cache that holds the text and them. Draft i sees
+ * the text, its ancestors and itself; with window > 0 of those only the keys whose position lies
+ * within `window` positions of its own, itself included, or below `sinks`. Types, outputs, lse and
+ * arguments as ub_attn_prompt over a cache. The drafts of a sequence may be many or one. A place
+ * below zero (kv_lens[s] < n_s) is no key; a row without any key gives 0 and lse -inf.
+ * The (sequence, heads, 128 keys) tiles are split evenly over the GPU and joined in a fixed
+ * order; the CTAs of an item that is split wait for one another (bounded, UB_ERR_TIMEOUT).
+ *
+ * ub_kv_accept: leaves[s] is the last accepted draft of sequence s, -1: none. The rows of its
+ * path a_0 < a_1 < .. < a_m = leaves[s] move from their places L_s + a_d to L_s + d, keys and
+ * values, and new_lens[s] = L_s + m + 1 (L_s for no draft); other rows of the cache stay as they
+ * are. It reads seq_starts, kv_lens, page_table and the cache's fields of ub_attn_t; `parents` has
+ * n_tokens entries, whatever the active shape is now. new_lens must not overlap kv_lens: with a
+ * cache for each layer, every layer's call takes the same lengths.
+ *
+ * Recorded in the sticky status (UB_ERR_ARG), besides what ub_kv_append lists: a parent outside
+ * [-1, own place) (taken as -1), and in ub_kv_accept a leaf outside [-1, n_s), starts out of order
+ * or past n_tokens, a length below its drafts or past the table, and more than UB_ACCEPT_MOST
+ * drafts of a sequence (nothing of that sequence is moved then, and new_lens[s] is L_s).
+ */
+#define UB_ACCEPT_MOST 2048
+int ub_kv_append_tree(ub_handle_t h, const ub_attn_t *a, const int32_t *parents, void *stream);
+int ub_attn_tree(ub_handle_t h, const ub_attn_t *a, const int32_t *parents, int32_t window, int32_t sinks, void *stream);
+int ub_kv_accept(ub_handle_t h, const ub_attn_t *a, const int32_t *parents, int64_t n_tokens, const int32_t *leaves,
+                 int32_t *new_lens, void *stream);
+
+/*
+ * The pages of a cache, shared out on the device: a table row for each sequence, as in ub_attn_t,
+ * and refs[p], the number of table entries that name page p. A page of count <= 0 is free (a
+ * page that is to stay out of use gets a count of its own). Entries below zero name none. The
+ * tables serve every layer's cache; only ub_kv_copy moves data, and takes one layer's.
+ *
+ * ub_kv_take: pages for the cache rows [begin[s], end[s]) of every sequence: each missing entry
+ * among the pages that hold a part of them gets a free page, of count 1. Entries in the order of
+ * the table (by sequence, then by place) get the free pages in rising order. Too few: the last
+ * ones stay missing, UB_ERR_CAPACITY in the sticky status.
+ *
+ * ub_kv_free: the entries of pages that lie wholly within [begin[s], end[s]) become -1 and their
+ * pages' counts go down by one. `end` may lie past the table: a row is given up with 0 and its
+ * capacity, the rest of rejected drafts with the new length and the capacity, what a window has
+ * left behind with the sinks and the first key still in sight.
+ *
+ * ub_kv_fork: row i of new_table becomes a copy of row source[i] of page_table, of whose sequence
+ * kv_lens[source[i]] rows are in the cache: the whole pages are shared (their counts go up by
+ * one); a last page that is filled in part is copied, into a free page of count 1 (the children,
+ * in order, get the free pages in rising order), and copies[i] = (from, to) says so; (-1, -1)
+ * where there is none. Then ub_kv_copy copies the data, for every layer. new_table has the width
+ * of page_table and overlaps it nowhere; what its rows held is not given up first (ub_kv_free).
+ *
+ * ub_kv_compact: the U pages in use move together into pages 0 .. U - 1: the k-th page in use at
+ * or above U goes to the k-th free page below it, moves[k] = (from, to), rest (-1, -1), and
+ * *used = U. refs_out and table_out, which may be refs and page_table, get the new counts and
+ * tables; all tables on the pool have to be rows of page_table. n_moves >= num_pages / 2.
+ *
+ * ub_kv_copy: page pairs[i][0] of k_cache and v_cache is copied to page pairs[i][1], all heads;
+ * pairs of two negative pages are skipped. It reads the cache's fields of ub_attn_t. A page that
+ * two pairs write, or one writes and another reads, gets either content, in any mix.
+ *
+ * Recorded in the sticky status (UB_ERR_ARG): an entry at or past num_pages (dropped; ub_kv_compact
+ * leaves it), freeing or sharing a page whose count is not above zero, rows to take outside the
+ * table (cut), a source or a length out of range, a pair with one page outside the cache (skipped).
+ *
+ * One kernel each, on `stream`; take, fork and compact use the handle's workspace, so the
+ * calls of a handle are ordered as the attention's are. Host errors: UB_ERR_ARG, UB_ERR_ZERO,
+ * UB_ERR_ALIGN, UB_ERR_CUDA.
+ */
+typedef struct {
+    uint32_t size;       /* sizeof(ub_pool_t) */
+    int32_t n_seqs;      /* rows of page_table */
+    int32_t page_size;   /* a power of two, 8..256 */
+    uint32_t reserved;   /* 0 */
+    int64_t num_pages;
+    int64_t table_width; /* entries per row */
+    int64_t table_row;   /* elements between rows */
+    int32_t *refs;       /* [num_pages] */
+    int32_t *page_table; /* [n_seqs, table_width] */
+} ub_pool_t;
+int ub_kv_take(ub_handle_t h, const ub_pool_t *pool, const int32_t *begin, const int32_t *end, void *stream);
+int ub_kv_free(ub_handle_t h, const ub_pool_t *pool, const int32_t *begin, const int32_t *end, void *stream);
+int ub_kv_fork(ub_handle_t h, const ub_pool_t *pool, const int32_t *kv_lens, const int32_t *source, int64_t n_children,
+               int32_t *new_table, int64_t new_row, int32_t *copies, void *stream);
+int ub_kv_compact(ub_handle_t h, const ub_pool_t *pool, int32_t *refs_out, int32_t *table_out, int64_t out_row,
+                  int32_t *moves, int64_t n_moves, int32_t *used, void *stream);
+int ub_kv_copy(ub_handle_t h, const ub_attn_t *a, const int32_t *pairs, int64_t n_pairs, void *stream);
 
 /* Options (UB_OPT_*). UB_ERR_ARG for an unknown key or an out-of-range value. */
 int ub_set_option(ub_handle_t h, int key, int64_t val);
