@@ -30,7 +30,7 @@ struct HandleCall {
     int join_words;
     uint32_t *tickets;       // two words, zero between calls
     uint32_t *piece_counters; // of the prompt attention's split items: PROMPT_SLOTS words
-    float *ws_rows;          // PROMPT_SLOTS * 512
+    float *ws_rows;          // PROMPT_SLOTS * 512, behind the floats of ws
 
 };
 
@@ -153,9 +153,10 @@ struct TreeParams {
     int blocks;              // ... and how many such sets a key/value head has
     int units;               // kv_heads * blocks
     int tokens;              // tokens of a q tile
+    int many_units;          // the call could hold 2^31 units of work or more
     int window, sinks;       // as in DecodeParams
     float scale;
-    float *ws, *ws_rows;     // parts of split items: two slots per CTA of 256 rows; their maxima and sums
+    float *ws;               // parts of split items: two slots per CTA
     uint32_t *counters, *times;  // as in DecodeParams
     uint32_t *abort_word;
     uint64_t timeout_ns;
@@ -165,7 +166,10 @@ struct TreeParams {
 constexpr int TREE_ROWS = 128;           // rows (tokens x heads) of one q tile, two per item
 constexpr int TREE_KEYS = 128;           // keys of one tile
 constexpr int TREE_SLOTS = 2;            // workspace slots per CTA
-__host__ __device__ constexpr int tree_slot_floats(int head_dim) { return 2 * TREE_ROWS * head_dim; }
+__host__ __device__ constexpr int tree_part_row(int head_dim) { return head_dim + 4; }  // floats of a row of a part
+__host__ __device__ constexpr int tree_slot_floats(int head_dim) { return 2 * TREE_ROWS * tree_part_row(head_dim); }
+constexpr int TREE_MOST_CTAS = 176;      // of a grid
+constexpr int TREE_MOST_UNITS = 64;      // of a key tile or the end of an item, at most
 cudaError_t launch_attn_tree(const TreeParams &p, int grid, cudaStream_t s);
 
 // The pages of a cache: tables and reference counts (see ub_pool_t).

@@ -401,8 +401,7 @@ int tree_call(const char *fn, ub_handle_t h, const ub_attn_t *in, const int32_t 
     p.kv_heads = a.kv_heads;
     p.head_dim = a.head_dim;
     p.scale = a.scale;
-    p.ws = c.ws;
-    p.ws_rows = c.ws_rows;
+    p.ws = c.ws;  // and on into ws_rows
     p.counters = c.join_counters;
     p.times = c.join_counters + c.join_words / DECODE_COUNTERS;
     p.abort_word = c.abort_word;
@@ -410,12 +409,13 @@ int tree_call(const char *fn, ub_handle_t h, const ub_attn_t *in, const int32_t 
     p.epoch = c.epoch;
     p.pdl = c.pdl;
     // As many CTAs as fit, and no more than there can be key tiles.
-    int64_t grid = c.sms;
+    int64_t grid = c.sms < TREE_MOST_CTAS ? c.sms : TREE_MOST_CTAS;
     const int64_t items = (T / (2 * p.tokens) + (a.n_seqs < T ? a.n_seqs : T)) * p.units;
     const int64_t tiles = (keys + TREE_KEYS - 1) / TREE_KEYS;
     if (items <= grid && items * tiles < grid) grid = items * tiles;
-    if (DECODE_COUNTERS * grid > c.join_words || TREE_SLOTS * grid > PROMPT_SLOTS ||
-        TREE_SLOTS * grid * tree_slot_floats(a.head_dim) > static_cast<int64_t>(c.ws_floats))
+    p.many_units = items > INT32_MAX / TREE_MOST_UNITS / (tiles + 1) ? 1 : 0;
+    const int64_t room = static_cast<int64_t>(c.ws_floats) + 512 * PROMPT_SLOTS;
+    if (DECODE_COUNTERS * grid > c.join_words || TREE_SLOTS * grid * tree_slot_floats(a.head_dim) > room)
         return fail_call(UB_ERR_ARG, "%s: workspace too small for %lld CTAs", fn, (long long)grid);
     bool timed = false;
     if (int rc = handle_prof_start(h, UB_OP_ATTN_TREE, s, &timed)) return rc;

@@ -27,7 +27,8 @@
 //   warps 0-3, 4-7   softmax of pipeline 0 and 1, one thread per row; the item's end; joins
 //   warp 8           loads (TMA): Q, then K and V tiles in a ring
 //   warps 9, 10      MMA issue for pipeline 0 and 1
-//   warp 11          zeroes the rows of V past a sequence's end in its last tile
+//   warp 11          schedule: this CTA's items; and zeroes the rows of V past a sequence's end in
+//                    its last tile (their weights are zero, their values may be anything)
 #include <cuda_bf16.h>
 
 #include "ub_attn.h"
@@ -41,13 +42,20 @@ namespace {
 constexpr int TR_THREADS = 384;
 constexpr int KEYS = TREE_KEYS, ROWS = TREE_ROWS;
 // Registers per thread by role; their sum is what the block is launched with (384 x 168).
-constexpr int SOFTMAX_REGS = 200, SINGLE_REGS = 104;
+constexpr int SOFTMAX_REGS = 216, SINGLE_REGS = 72;
 static_assert(2 * SOFTMAX_REGS + SINGLE_REGS == 3 * 168, "register split");
-constexpr int TM_S = 0, TM_O = 256;      // TMEM columns: S_i at 128 i, O_i at 256 + 128 i
+constexpr int ITEMS = 4;                 // items published ahead
+constexpr int TM_S = 0, TM_O = 256;      // TMEM columns: S_i at 128 i (and P_i in its place), O_i at 256 + 128 i
+constexpr int PART = 4;                  // steps of 16 keys whose weights are handed over early (heads of 128)
 constexpr float RESCALE_LOG2 = 8.f;      // growth of the maximum (log2) that is put off
-// What the end of an item (O joined and written, the next queries loaded) counts in the split, in
-// key tiles; what a join costs; key tiles of a CTA, at least.
-constexpr int ITEM_COST = 3, JOIN_TILES = 5, MIN_TILES = 2;
+// Units of the split, about 0.08 us: what a key tile takes in an item of one q tile and of two, heads
+// of 64 and of 128; the end of an item (the pipelines run empty, O joined and written, the next
+// queries loaded); a join. From the times of CTAs of calls of mixed items: key tiles 0.5-0.6 and
+// 1.1 us with heads of 64, 0.6-1.0 and 1.2 with heads of 128, ends 2-4 us, a join 6.
+__host__ __device__ constexpr int tile_units(int head_dim, bool two) { return two ? 15 : (head_dim == 64 ? 7 : 9); }
+constexpr int ITEM_COST = 42, JOIN_COST = 80;
+constexpr int MIN_UNITS = 24;            // of a CTA, at least: no less than any tile
+static_assert(ITEM_COST <= TREE_MOST_UNITS && tile_units(128, true) <= MIN_UNITS, "units");
 
 template <int D>
 struct TreeShape {
@@ -56,6 +64,8 @@ struct TreeShape {
     static constexpr int STAGES = D == 128 ? 5 : 10;
     static constexpr int CONTROL = 2048 + 768;            // (m, l) of two tiles; barriers
     static constexpr int SMEM = (2 + STAGES) * TILE_BYTES + CONTROL;
+    // The rows that a CTA joins: those of an item and one more of each part at most.
+    static_assert((2 * ROWS + TREE_MOST_CTAS) * 4 * tree_part_row(D) <= (2 + STAGES) * TILE_BYTES, "memory of a join");
     static_assert(SMEM <= 232448, "shared memory");
 };
 
@@ -65,18 +75,17 @@ struct Seq {
     int len, text;  // keys; those before the drafts (below zero: some drafts have no key)
     int lo;         // first key in the window of a draft that follows the text
     int near, far;  // its key tile; key tiles before it that hold sinks
-    int tiles;      // key tiles in sight
+    int tiles;      // key tiles in sight, at least one
     int blocks;     // items of a key/value head
+    int per;        // units of a key tile
     __device__ __forceinline__ int tile(int t) const { return t < far ? t : t - far + near; }
-    // Units of an item in the split.
-    __device__ __forceinline__ int span() const { return tiles > 1 ? tiles : 1; }
+    // Units of an item (2^24 tiles at most).
+    __device__ __forceinline__ int span() const { return tiles * per; }
     __device__ __forceinline__ int cost() const { return span() + ITEM_COST; }
 };
-__device__ __forceinline__ Seq seq_of(const TreeParams &p, int s)
+__device__ __forceinline__ Seq seq_from(const TreeParams &p, int a, int z, int len)
 {
     Seq q;
-    int a = p.b.seq_starts[s], z = p.b.seq_starts[s + 1];
-    const int len = p.b.kv_lens[s];
     a = a < 0 ? 0 : (a > p.T ? p.T : a);
     z = z < a ? a : (z > p.T ? p.T : z);
     const int64_t most = static_cast<int64_t>(p.b.table_width) << p.b.page_shift;
@@ -88,9 +97,30 @@ __device__ __forceinline__ Seq seq_of(const TreeParams &p, int s)
     q.near = q.lo / KEYS;
     const int sunk = (p.sinks + KEYS - 1) / KEYS;
     q.far = sunk < q.near ? sunk : q.near;
-    q.tiles = (q.len + KEYS - 1) / KEYS - q.near + q.far;
-    q.blocks = (q.n + 2 * p.tokens - 1) / (2 * p.tokens);
+    q.tiles = q.len > 0 ? (q.len + KEYS - 1) / KEYS - q.near + q.far : 1;
+    q.blocks = static_cast<int>(static_cast<uint32_t>(q.n + 2 * p.tokens - 1) / static_cast<uint32_t>(2 * p.tokens));
+    q.per = tile_units(p.head_dim, q.n > p.tokens);
     return q;
+}
+__device__ __forceinline__ Seq seq_of(const TreeParams &p, int s)
+{
+    return seq_from(p, p.b.seq_starts[s], p.b.seq_starts[s + 1], p.b.kv_lens[s]);
+}
+// Lane l's sequence.
+__device__ __forceinline__ Seq from_lane(const Seq &q, int l)
+{
+    Seq r;
+    r.start = __shfl_sync(0xffffffffu, q.start, l);
+    r.n = __shfl_sync(0xffffffffu, q.n, l);
+    r.len = __shfl_sync(0xffffffffu, q.len, l);
+    r.text = __shfl_sync(0xffffffffu, q.text, l);
+    r.lo = __shfl_sync(0xffffffffu, q.lo, l);
+    r.near = __shfl_sync(0xffffffffu, q.near, l);
+    r.far = __shfl_sync(0xffffffffu, q.far, l);
+    r.tiles = __shfl_sync(0xffffffffu, q.tiles, l);
+    r.blocks = __shfl_sync(0xffffffffu, q.blocks, l);
+    r.per = __shfl_sync(0xffffffffu, q.per, l);
+    return r;
 }
 
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
@@ -98,12 +128,14 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
     if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
     return a / b;
 }
+__device__ __forceinline__ int quotient(int a, int b) { return static_cast<int>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)); }
 __device__ __forceinline__ int64_t warp_sum(int64_t v)
 {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
+__device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
 
 // The equal split of `total` units over CTAs: CTA c's first unit, and the CTA of a unit.
 struct Split {
@@ -116,18 +148,25 @@ struct Split {
     }
 };
 
-// A CTA's way through its share of the call: the current item, and its key tiles [t0, t1).
+// A CTA's way through its share of the call: the current item, and its key tiles [t0, t1), those
+// whose first unit lies in the share.
 struct Walk {
     const TreeParams &p;
     Split split;
-    int64_t x, left;  // unit of the whole call at t0 (not counted for whole items), units to go
+    int64_t x, left;  // first unit of the item here (not counted for whole items), units to go
+    int off;          // units of the item that are others' (before x)
     int s, item;      // sequence, item of it
     int t0, t1;
     Seq q;
 
     __device__ __forceinline__ explicit Walk(const TreeParams &params) : p(params) {}
     __device__ __forceinline__ bool more() const { return left > 0 && s < p.b.n_seqs; }
-    __device__ __forceinline__ void cut() { t1 = q.span() - t0 < left ? q.span() : t0 + static_cast<int>(left); }
+    __device__ __forceinline__ void cut()
+    {
+        const uint32_t per = q.per, end = off + left < q.span() ? static_cast<int>(off + left) : q.span();
+        t0 = static_cast<int>((off + per - 1) / per);
+        t1 = static_cast<int>((end + per - 1) / per);
+    }
     __device__ __forceinline__ void settle_on()  // an item of sequence s, or of the next that has one
     {
         while (s < p.b.n_seqs) {
@@ -140,10 +179,10 @@ struct Walk {
     }
     __device__ __forceinline__ void next()
     {
-        const int64_t units = q.cost() - t0 < left ? q.cost() - t0 : left;
+        const int units = q.cost() - off < left ? q.cost() - off : static_cast<int>(left);
         x += units;
         left -= units;
-        t0 = 0;
+        off = 0;
         if (++item < q.blocks * p.units) {
             cut();
         } else if (left > 0) {
@@ -160,125 +199,152 @@ struct Walk {
         return n < 2 * p.tokens ? n : 2 * p.tokens;
     }
     // Whole in this CTA; and how many key tiles of it there are to do (an item without keys: none).
-    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == q.span(); }
-    __device__ __forceinline__ int todo() const { return q.tiles > 0 ? t1 - t0 : 0; }
+    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == q.tiles; }
+    __device__ __forceinline__ int todo() const { return q.len > 0 ? t1 - t0 : 0; }
 };
 
-// Sets out CTA `cta` of `grid` (one warp, all lanes alike).
-__device__ void begin(Walk &w, int lane, int cta, int grid)
+// Sets out CTA `cta` of `grid` (one warp, all lanes alike). I: a type that holds the units of the
+// call. (It runs cold, and everything waits for it: 32-bit where they fit.)
+template <typename I>
+__device__ __forceinline__ void begin(Walk &w, int lane, int cta, int grid)
 {
     const TreeParams &p = w.p;
-    w.left = 0;
-    w.s = w.item = w.t0 = w.t1 = 0;
-    w.x = 0;
+    w.left = w.x = 0;
+    w.off = w.s = w.item = w.t0 = w.t1 = 0;
     w.split = Split{0, 0};
+    const int n_seqs = p.b.n_seqs;
+    Seq own = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+    if (lane < n_seqs) own = seq_of(p, lane);
     // Sums over the sequences: items, and units of the split.
-    Seq own;
-    own.n = own.blocks = own.tiles = 0;
-    if (lane < p.b.n_seqs) own = seq_of(p, lane);
-    int64_t items = own.blocks, total = static_cast<int64_t>(own.blocks) * (own.blocks > 0 ? own.cost() : 0);
+    I items = own.blocks, total = static_cast<I>(own.blocks) * own.cost();
     int most = own.blocks > 0 ? own.span() : 0;
-    for (int i = lane + 32; i < p.b.n_seqs; i += 32) {
+#pragma unroll 1
+    for (int i = lane + 32; i < n_seqs; i += 32) {
         const Seq q = seq_of(p, i);
-        if (q.blocks == 0) continue;
         items += q.blocks;
-        total += static_cast<int64_t>(q.blocks) * q.cost();
-        most = q.span() > most ? q.span() : most;
+        total += static_cast<I>(q.blocks) * q.cost();
+        most = q.blocks > 0 && q.span() > most ? q.span() : most;
     }
     items = warp_sum(items) * p.units;
     total = warp_sum(total) * p.units;
     most = __reduce_max_sync(0xffffffffu, most);
     if (items == 0) return;
     // A CTA per item where no item is much longer than an equal share would be: a share saves the
-    // difference and costs a join. Else equal shares, of at least MIN_TILES units, or a CTA per
+    // difference and costs a join. Else equal shares, of at least MIN_UNITS units, or a CTA per
     // item where those are shorter.
-    const bool whole = items <= grid && static_cast<int64_t>(most - JOIN_TILES) * grid <= total - items * ITEM_COST;
-    int64_t ctas = whole ? items : total / MIN_TILES;
+    const bool whole = items <= grid && static_cast<int64_t>(most - JOIN_COST) * grid <= total - items * ITEM_COST;
+    I ctas = whole ? items : total / MIN_UNITS;
     if (!whole && ctas < items) ctas = items;
     ctas = ctas > grid ? grid : ctas;
     if (cta >= ctas) return;
-    const int64_t base = quotient(total, ctas);
+    const I base = quotient(total, ctas);
     w.split = Split{base, total - base * ctas};
-    const int64_t at = whole ? cta : w.split.first(cta);
+    const I at = whole ? cta : static_cast<I>(w.split.first(cta));
     // The sequence that holds item or unit `at`, and those before it.
-    int64_t seen = 0, before = 0;
-    for (int i0 = 0; i0 < p.b.n_seqs; i0 += 32) {
+    I seen = 0;
+#pragma unroll 1
+    for (int i0 = 0; i0 < n_seqs; i0 += 32) {
         Seq q = own;
-        if (i0 > 0 && i0 + lane < p.b.n_seqs) q = seq_of(p, i0 + lane);
-        int64_t mine = 0;
-        if (i0 + lane < p.b.n_seqs && q.blocks > 0) mine = static_cast<int64_t>(q.blocks) * p.units * (whole ? 1 : q.cost());
-        int64_t upto = mine;
+        if (i0 > 0) q = seq_of(p, i0 + lane < n_seqs ? i0 + lane : n_seqs - 1);
+        I mine = i0 + lane < n_seqs ? static_cast<I>(q.blocks) * p.units * (whole ? 1 : q.cost()) : 0, upto = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+            const I y = __shfl_up_sync(0xffffffffu, upto, o);
             if (lane >= o) upto += y;
         }
         const uint32_t past = __ballot_sync(0xffffffffu, seen + upto > at);
         if (past != 0u) {
             const int l = __ffs(static_cast<int>(past)) - 1;
             w.s = i0 + l;
-            before = seen + __shfl_sync(0xffffffffu, upto - mine, l);
+            w.q = from_lane(q, l);
+            seen += __shfl_sync(0xffffffffu, upto - mine, l);
             break;
         }
         seen += __shfl_sync(0xffffffffu, upto, 31);
     }
-    w.q = seq_of(p, w.s);
     if (whole) {
-        w.item = static_cast<int>(at - before);
+        w.item = static_cast<int>(at - seen);
         w.left = w.q.span();
     } else {
         w.x = at;
         w.left = w.split.first(cta + 1) - at;
-        w.item = static_cast<int>(quotient(at - before, w.q.cost()));
-        w.t0 = static_cast<int>(at - before - static_cast<int64_t>(w.item) * w.q.cost());
-        if (w.t0 >= w.q.span()) {  // behind the item's last tile: on to the next
-            w.x += w.q.cost() - w.t0;
-            w.left -= w.q.cost() - w.t0;
-            w.t0 = 0;
-            ++w.item;
-        }
+        w.item = static_cast<int>(quotient(at - seen, static_cast<I>(w.q.cost())));
+        w.off = static_cast<int>(at - seen - static_cast<I>(w.item) * w.q.cost());
     }
-    w.settle_on();
+    w.cut();
+    if (w.t0 >= w.q.tiles) w.next();  // behind the first unit of the item's last tile: on to the next
 }
+
+// One item of a CTA as the schedule warp publishes it. The other warps read it where they use it,
+// so that it takes no registers beside a row's scores.
+struct Item {
+    int seq;         // sequence; -1: no more items
+    int row0, ntok;  // first token of the call, tokens
+    int first;       // first draft
+    int unit;        // heads
+    int len, text;   // as in Seq
+    int lo, near, far;
+    int t0, todo;    // key tiles in sight: the first one, how many (0: the item has no keys)
+    int whole;       // all of the item's
+    __device__ __forceinline__ int tile(int j) const { return t0 + j < far ? t0 + j : t0 + j - far + near; }
+};
+// An item that other CTAs have parts of, for the join.
+struct Pending {
+    int row0, n, unit;  // first token and tokens, heads
+    int a, parts;       // the CTA in which it begins, and how many have parts; 0: no such item
+};
 
 // The low `n` bits (n may be below zero or past 32).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
 
 // The draft that draft i of a sequence follows, -1: the text.
-__device__ __forceinline__ int parent_of(const TreeParams &p, const Seq &q, int i)
+__device__ __forceinline__ int parent_of(const TreeParams &p, int start, int i)
 {
-    const int up = p.parents[q.start + i];
+    const int up = p.parents[start + i];
     if (up >= -1 && up < i) return up;
     atomicCAS(p.b.status, 0, UB_ERR_ARG);
     return -1;
 }
 
-// Which of the 128 keys from key0 on draft `i` at position `pos` sees (i < 0: a row of no draft).
-__device__ void keys_seen(const TreeParams &p, const Seq &q, int i, int pos, int key0, uint32_t *bits)
+// Which of the 128 keys from key0 on draft `i` at position `pos` sees (i < 0: a row of no draft);
+// start: the token of the sequence's first draft, text: keys before the drafts.
+__device__ __forceinline__ void keys_seen(const TreeParams &p, int start, int text, int i, int pos, int key0, uint32_t *bits)
 {
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
         const int first = key0 + 32 * w;
-        bits[w] = low_bits(q.text - first);
+        bits[w] = low_bits(text - first);
         if (p.window > 0) bits[w] &= ~low_bits(pos - p.window + 1 - first) | low_bits(p.sinks - first);
     }
-    const int gone = key0 - q.text;  // drafts before this tile, or before the cache
-    const int least = gone > -q.text ? gone : -q.text;
+    const int gone = key0 - text;  // drafts before this tile, or before the cache
+    const int least = gone > -text ? gone : -text;
     for (int d = 0; i >= 0 && i >= least; ++d) {
         const int c = i - gone;
         const bool seen = c < KEYS && (p.window == 0 || d < p.window || pos - d < p.sinks);
 #pragma unroll
         for (int w = 0; w < 4; ++w)
             if (seen && (c >> 5) == w) bits[w] |= 1u << (c & 31);
-        i = parent_of(p, q, i);
+        i = parent_of(p, start, i);
     }
     __syncwarp();
 }
 
-// An item that other CTAs have parts of, as its CTA keeps it for the join.
-struct Pending {
-    int64_t item0;            // its first unit
-    int span, row0, n, unit;  // units, first token and tokens, unit of heads
+__device__ __forceinline__ void store_lse(const TreeParams &p, int64_t token, int head, float m, float l)
+{
+    if (p.lse) p.lse[token * p.heads + head] = l > 0.f ? m * p.scale + logf(l) : (l == 0.f ? -INFINITY : l);
+}
+
+// 16 bytes from global to shared memory, past L1.
+__device__ __forceinline__ void copy16(uint32_t to, const void *from)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+
+// A part of a split item in the workspace: 256 rows of D columns, maximum and sum (and two words).
+template <int D>
+struct PartRow {
+    static constexpr int FLOATS = tree_part_row(D);
+    static constexpr int BYTES = 4 * FLOATS;
 };
 
 template <int D>
@@ -286,6 +352,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
 {
     using Sh = TreeShape<D>;
     constexpr int NST = Sh::STAGES, HALVES = D / 64;
+    constexpr bool EARLY = D == 128;
     extern __shared__ __align__(1024) uint8_t base[];
     const uint32_t sm_q = smem_u32(base), sm_kv = sm_q + 2 * Sh::TILE_BYTES;
     float *sm_max = reinterpret_cast<float *>(base + (2 + NST) * Sh::TILE_BYTES);  // [2][128]
@@ -294,10 +361,15 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
     const uint32_t kv_full = smem_u32(bars), v_raw = kv_full + 8 * NST, kv_empty = kv_full + 16 * NST,
                    misc = kv_full + 24 * NST;
     const uint32_t q_full = misc, q_empty = misc + 8, s_full = misc + 16, p_full = misc + 32, o_full = misc + 48,
-                   o_empty = misc + 64, both = misc + 80, parts_done = misc + 88, join_go = misc + 96, drain = misc + 112;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(reinterpret_cast<uint8_t *>(bars) + 24 * NST + 128);
+                   o_empty = misc + 64, both = misc + 80, parts_done = misc + 88, join_go = misc + 96, drain = misc + 112,
+                   p_part = misc + 128, joined = misc + 144;
+    const uint32_t it_full = misc + 152, it_empty = it_full + 8 * ITEMS;
+    Item *items = reinterpret_cast<Item *>(reinterpret_cast<uint8_t *>(bars) + 24 * NST + 152 + 16 * ITEMS);
+    Pending *pend = reinterpret_cast<Pending *>(items + ITEMS);  // begun before this CTA; going on after it
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(pend + 2);
     volatile uint32_t *issued = tmem_slot + 1;   // ring positions whose loads have been issued
-    static_assert(24 * NST + 136 <= 768, "barrier area");
+    volatile uint32_t *turn = issued + 1;        // steps that the issuer of each pipeline has done
+    static_assert(24 * NST + 152 + 16 * ITEMS + sizeof(Item) * ITEMS + sizeof(Pending) * 2 + 16 <= 768, "barrier area");
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     if ((sm_q & 1023u) != 0u) {  // the swizzled tiles need what the declaration asks for
@@ -314,15 +386,22 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
         mbar_init(q_empty, 2);               // both issuing warps
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full + 8 * i, 1);
+            mbar_init(p_part + 8 * i, 4);    // heads of 128: the first PART steps of P written, O rescaled
             mbar_init(p_full + 8 * i, 4);
             mbar_init(o_full + 8 * i, 1);
             mbar_init(o_empty + 8 * i, 8);   // all softmax warps
             mbar_init(join_go + 8 * i, 1);
             mbar_init(drain + 8 * i, 1);
         }
-        *issued = 0u;
+        for (int i = 0; i < ITEMS; ++i) {
+            mbar_init(it_full + 8 * i, 1);
+            mbar_init(it_empty + 8 * i, 11);  // every warp but the schedule's
+        }
+        pend[0].parts = pend[1].parts = 0;
+        *issued = turn[0] = turn[1] = 0u;
         mbar_init(both, 8);
         mbar_init(parts_done, 8);
+        mbar_init(joined, 8);
         fence_mbar_init();
         prefetch_tmap(&p.tmQ);
         prefetch_tmap(&p.tmK);
@@ -351,8 +430,10 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
     };
-    Walk w(p);
-    begin(w, lane, blockIdx.x, gridDim.x);
+    // Waits for the k-th item of this CTA; false at the end, or when a wait ran out.
+    auto there = [&](uint32_t k) {
+        return wait(it_full + 8 * (k % ITEMS), (k / ITEMS) & 1) && *static_cast<volatile int *>(&items[k % ITEMS].seq) >= 0;
+    };
 
     if (warp < 8) {
         // ------------------------------------------------------------ softmax
@@ -365,28 +446,19 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
         const float sl = p.scale * 1.4426950408889634f;
         const int G = gridDim.x;
         uint32_t n_s = 0, n_o[2] = {0, 0};             // phases used
-        Pending pend[2] = {{0, 0, 0, 0, 0}, {0, 0, 0, 0, 0}};  // begun before this CTA; going on after it
-        auto store_lse = [&](int64_t token, int head, float m, float l) {
-            if (p.lse) p.lse[token * p.heads + head] = l > 0.f ? m * p.scale + logf(l) : (l == 0.f ? -INFINITY : l);
-        };
-        for (uint32_t k = 0; w.more() && alive; ++k, w.next()) {
-            const Seq &q = w.q;
-            const int ntok = w.tokens(), todo = w.todo();
-            const bool two = ntok > p.tokens;
+        for (uint32_t k = 0; there(k); ++k) {
+            const Item &it = items[k % ITEMS];
+            const int todo = it.todo;
+            const bool two = it.ntok > p.tokens;
             const int token = (two ? i * p.tokens : 0) + row_token;  // of the item
-            const bool real = row_token < p.tokens && token < ntok;
-            const int draft = real ? w.first_token() + token : -1;
-            int pos = q.text;
+            const bool real = row_token < p.tokens && token < it.ntok;
+            const int draft = real ? it.first + token : -1;
+            int pos = it.text;
             if (p.window > 0 && draft >= 0)
-                for (int up = parent_of(p, q, draft); up >= 0; up = parent_of(p, q, up)) ++pos;
+                for (int up = parent_of(p, it.row0 - it.first, draft); up >= 0; up = parent_of(p, it.row0 - it.first, up)) ++pos;
             __syncwarp();
             float m = -INFINITY, l = 0.f;
             for (int j = two ? 0 : i; j < todo; j += two ? 1 : 2) {
-                const int key0 = q.tile(w.t0 + j) * KEYS;
-                uint32_t bits[4];
-                // some row does not see all of the tile: drafts, or keys left of a window
-                const bool edge = key0 + KEYS > q.text || (p.window > 0 && key0 <= q.len - p.window && key0 + KEYS > p.sinks);
-                if (edge) keys_seen(p, q, draft, pos, key0, bits);
                 if (!wait(s_full + 8 * i, n_s & 1)) break;
                 ++n_s;
                 tc_fence_after();
@@ -394,7 +466,11 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, reinterpret_cast<uint32_t *>(s) + c * 32);
                 tmem_wait_ld();
-                if (edge) {
+                // Some row does not see all of the tile: drafts, or keys left of a window.
+                const int key0 = it.tile(j) * KEYS;
+                if (key0 + KEYS > it.text || (p.window > 0 && key0 <= it.len - p.window && key0 + KEYS > p.sinks)) {
+                    uint32_t bits[4];
+                    keys_seen(p, it.row0 - it.first, it.text, draft, pos, key0, bits);
 #pragma unroll
                     for (int c = 0; c < 128; ++c)
                         if (((bits[c >> 5] >> (c & 31)) & 1u) == 0u) s[c] = -INFINITY;
@@ -439,10 +515,12 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
                         pk[c / 2] = pack_bf16x2(__float_as_uint(e0), __float_as_uint(e1));
                     }
                     tmem_st16(ts + c0 / 2, pk);
+                    if ((EARLY && c0 + 32 == PART * 16) || c0 == 96) {
+                        tmem_wait_st();
+                        tc_fence_before();
+                        arrive((c0 == 96 ? p_full : p_part) + 8 * i);
+                    }
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                arrive(p_full + 8 * i);
                 const uint64_t all = add2(sum[0], sum[1]);
                 l = l * f + (low(all) + high(all));
             }
@@ -457,14 +535,14 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
             if (todo > (two ? 0 : 1) && !wait(o_full + 8, n_o[1]++ & 1)) break;
             if (!wait(both, k & 1)) break;
             tc_fence_after();
-            const bool whole = w.whole();
-            const int64_t out_token = static_cast<int64_t>(q.start) + w.first_token() + token;
-            const int unit = w.unit(), kvh = unit / p.blocks;
-            const int in_group = (unit - kvh * p.blocks) * p.unit_heads + row_head;
+            const bool whole = it.whole != 0;
+            const int64_t out_token = static_cast<int64_t>(it.row0) + token;
+            const int kvh = it.unit / p.blocks;
+            const int in_group = (it.unit - kvh * p.blocks) * p.unit_heads + row_head;
             const int head = kvh * p.group + in_group;
             const bool mine = real && in_group < p.group;
             // One q tile: the two pipelines' O of a row, joined; half of the columns each.
-            float f0 = 1.f, f1 = 0.f, M = m, L = l;
+            float f0 = 1.f, f1 = 1.f, M = m, L = l;
             if (!two) {
                 const float m0 = sm_max[row], m1 = sm_max[128 + row];
                 M = fmaxf(m0, m1);
@@ -474,34 +552,20 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
                 L = sm_sum[row] * f0 + sm_sum[128 + row] * f1;
             }
             const int c0 = two || i == 0 ? 0 : D / 2, c1 = two || i == 1 ? D : D / 2;
-            const int which = w.t0 == 0 ? 1 : 0, part_row = two ? i * 128 + row : row;
+            const int which = it.t0 == 0 ? 1 : 0, part_row = two ? i * 128 + row : row;
             const int64_t slot = static_cast<int64_t>(which) * G + blockIdx.x;
-            float4 *part = reinterpret_cast<float4 *>(p.ws) + slot * (64 * D) + part_row;
+            float *part = p.ws + (slot * 256 + part_row) * PartRow<D>::FLOATS;
             const float inv = 1.f / L;
+            // a pipeline without a key tile has nothing there
+            const bool has0 = two ? i == 0 : todo > 0, has1 = two ? i == 1 : todo > 1;
 #pragma unroll 1
             for (int c = c0; c < c1; c += 16) {
-                float v[16];
-                if (two) {
-                    tmem_ld16(to + c, reinterpret_cast<uint32_t *>(v));
-                    tmem_wait_ld();
-                } else {
+                float v[16], u[16];
+                if (has0) tmem_ld16(tmem + TM_O + lanes + c, reinterpret_cast<uint32_t *>(v));
+                if (has1) tmem_ld16(tmem + TM_O + 128 + lanes + c, reinterpret_cast<uint32_t *>(u));
+                tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) v[e] = 0.f;
-                    float u[16];
-                    // a pipeline without a key tile has nothing there
-                    if (todo > 0) {
-                        tmem_ld16(tmem + TM_O + lanes + c, reinterpret_cast<uint32_t *>(u));
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) v[e] = u[e] * f0;
-                    }
-                    if (todo > 1) {
-                        tmem_ld16(tmem + TM_O + 128 + lanes + c, reinterpret_cast<uint32_t *>(u));
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) v[e] += u[e] * f1;
-                    }
-                }
+                for (int e = 0; e < 16; ++e) v[e] = (has0 ? v[e] * f0 : 0.f) + (has1 ? u[e] * f1 : 0.f);
                 if (mine && whole) {
                     __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + out_token * p.o_row + head * p.o_head + c;
 #pragma unroll
@@ -515,41 +579,40 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
                     }
                 } else if (mine) {
 #pragma unroll
-                    for (int e = 0; e < 16; e += 4) part[(c + e) / 4 * 256] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                    for (int e = 0; e < 16; e += 4)
+                        *reinterpret_cast<float4 *>(part + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
                 }
                 __syncwarp();
             }
             tc_fence_before();
             if (mine && (two || i == 0)) {
                 if (whole) {
-                    store_lse(out_token, head, M, L);
+                    store_lse(p, out_token, head, M, L);
                 } else {
-                    p.ws_rows[slot * 512 + part_row] = M;
-                    p.ws_rows[slot * 512 + 256 + part_row] = L;
+                    *reinterpret_cast<float2 *>(part + D) = make_float2(M, L);
                 }
             }
             arrive(o_empty);
             arrive(o_empty + 8);
-            if (!whole && w.t0 != 0) pend[0] = Pending{w.x - w.t0, q.span(), q.start + w.first_token(), ntok, unit};
-            if (!whole && w.t0 == 0) pend[1] = Pending{w.x, q.span(), q.start + w.first_token(), ntok, unit};
+            arrive(it_empty + 8 * (k % ITEMS));
         }
 
         // The parts of split items, joined when the CTA's own tiles are done: a CTA says that its
         // parts are there for both its items before it waits for either, so that no two items
-        // wait for one another (all CTAs are resident: one per SM, no more than SMs).
-        if ((pend[0].span | pend[1].span) != 0 && alive) {
+        // wait for one another (all CTAs are resident: one per SM, no more than SMs). Each CTA
+        // joins its share of the item's rows, of all parts, which it copies into the ring's memory.
+        if (alive && (pend[0].parts | pend[1].parts) != 0) {
             arrive(parts_done);
             if (warp < 2) {  // a warp for each
-                const Pending it = warp == 0 ? pend[0] : pend[1];
-                if (it.span != 0) {
-                    const int a = w.split.owner(it.item0), parts = w.split.owner(it.item0 + it.span - 1) - a + 1;
+                const Pending it = pend[warp];
+                if (it.parts != 0) {
                     // a count of the item's parts, and one, never reset, of how often all have come
-                    uint32_t *counter = p.counters + a, *times = p.times + a;
+                    uint32_t *counter = p.counters + it.a, *times = p.times + it.a;
                     if (wait(parts_done, 0) && lane == 0) {
                         const uint32_t before = *static_cast<volatile uint32_t *>(times);
                         uint32_t come;
                         asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(come) : "l"(counter) : "memory");
-                        if (come == static_cast<uint32_t>(parts - 1)) {
+                        if (come == static_cast<uint32_t>(it.parts - 1)) {
                             *counter = 0u;             // zero again for the next call
                             st_release_u32(times, before + 1u);
                         } else {
@@ -566,90 +629,109 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
                     arrive(join_go + 8 * warp);
                 }
             }
-#pragma unroll
-            for (int which = 0; which < 2; ++which) {
-                const Pending it = pend[which];
-                if (it.span == 0) continue;
-                if (!alive || !wait(join_go + 8 * which, 0)) break;
-                const int a = w.split.owner(it.item0), parts = w.split.owner(it.item0 + it.span - 1) - a + 1;
-                const int kvh = it.unit / p.blocks, h0 = (it.unit - kvh * p.blocks) * p.unit_heads;
-                const int rows = it.n * p.unit_heads, tile_rows = p.tokens * p.unit_heads;
-                const int units = rows * (D / 4);      // of four outputs, rows fastest
-                // Units of this CTA: `width` lanes each, as few as have all parts in flight at once.
-                constexpr int U = 5;                   // parts in flight per lane
-                int width_shift = 0;
-                while (width_shift < 5 && (U << width_shift) < parts) ++width_shift;
-                const int width = 1 << width_shift, at_once = 256 >> width_shift;
-                const int per = (units + parts - 1) / parts, i_cta = static_cast<int>(blockIdx.x) - a;
-                const int end = (i_cta + 1) * per < units ? (i_cta + 1) * per : units;
-                for (int u0 = i_cta * per; u0 < end; u0 += at_once) {
-                    const int u = u0 + (static_cast<int>(threadIdx.x) >> width_shift);
-                    const int c4 = u / rows, r = u - c4 * rows;
-                    const int part_row = r < tile_rows ? r : 128 + r - tile_rows;
-                    float MM = -INFINITY, LL = 0.f;
-                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int i0 = lane & (width - 1); i0 < parts && u < end; i0 += width * U) {
-                        float4 v[U];
-                        float mm[U], ll[U], top = MM;
-#pragma unroll
-                        for (int e = 0; e < U; ++e) {
-                            const int part = i0 + width * e;
-                            mm[e] = -INFINITY;
-                            ll[e] = 0.f;
-                            v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-                            if (part >= parts) continue;
-                            // slot 1 for the CTA in which the item begins, 0 for the others
-                            const int64_t slot = static_cast<int64_t>(part == 0 ? G : 0) + a + part;
-                            v[e] = __ldcg(reinterpret_cast<const float4 *>(p.ws) + slot * (64 * D) + c4 * 256 + part_row);
-                            mm[e] = __ldcg(p.ws_rows + slot * 512 + part_row);
-                            ll[e] = __ldcg(p.ws_rows + slot * 512 + 256 + part_row);
-                        }
-#pragma unroll
-                        for (int e = 0; e < U; ++e) top = fmaxf(top, mm[e]);
-                        const float ref = top == -INFINITY ? 0.f : top;
-                        const float g0 = ex2((MM - ref) * sl);
-                        LL *= g0;
-                        acc.x *= g0;
-                        acc.y *= g0;
-                        acc.z *= g0;
-                        acc.w *= g0;
-                        MM = top;
-#pragma unroll
-                        for (int e = 0; e < U; ++e) {
-                            const float g = ex2((mm[e] - ref) * sl);
-                            LL += ll[e] * g;
-                            acc.x += v[e].x * g;
-                            acc.y += v[e].y * g;
-                            acc.z += v[e].z * g;
-                            acc.w += v[e].w * g;
+            // This CTA's rows of an item: [first, first + n), and where they are in shared memory, part
+            // after part. Those of both items at once, where there is room.
+            auto share = [&](const Pending &it, int &first, int &n) {
+                const int rows = it.n * p.unit_heads, per = it.parts > 0 ? (rows + it.parts - 1) / it.parts : 0;
+                first = (static_cast<int>(blockIdx.x) - it.a) * per;
+                n = it.parts == 0 || first >= rows ? 0 : (rows - first < per ? rows - first : per);
+            };
+            int first0, n0, first1, n1;
+            share(pend[0], first0, n0);
+            share(pend[1], first1, n1);
+            const int size0 = n0 * pend[0].parts * PartRow<D>::BYTES, size1 = n1 * pend[1].parts * PartRow<D>::BYTES;
+            uint32_t n_joined = 0;
+            const bool at_once = size0 + size1 <= (2 + NST) * Sh::TILE_BYTES;
+#pragma unroll 1
+            for (int round = 0; round < (at_once ? 1 : 2) && alive; ++round) {
+#pragma unroll 1
+                for (int which = at_once ? 0 : round; which < (at_once ? 2 : round + 1); ++which) {
+                    const Pending it = pend[which];
+                    const int first = which == 0 ? first0 : first1, n = which == 0 ? n0 : n1, tile_rows = p.tokens * p.unit_heads;
+                    if (it.parts == 0 || !wait(join_go + 8 * which, 0)) continue;
+                    // A row for each warp, of every part, or a part.
+                    const uint32_t mem = sm_q + (at_once && which == 1 ? size0 : 0) + lane * 16;
+                    const bool few = n < 8;
+#pragma unroll 1
+                    for (int part = few ? warp : 0; part < it.parts; part += few ? 8 : 1) {
+                        // slot 1 for the CTA in which the item begins, 0 for the others
+                        const int64_t slot = static_cast<int64_t>(part == 0 ? G : 0) + it.a + part;
+                        const float *rows = p.ws + slot * 256 * PartRow<D>::FLOATS + lane * 4;
+                        const uint32_t to = mem + part * n * PartRow<D>::BYTES;
+#pragma unroll 2
+                        for (int r = few ? 0 : warp; r < n; r += few ? 1 : 8) {
+                            const int of = first + r, part_row = of < tile_rows ? of : 128 + of - tile_rows;
+                            const float *from = rows + part_row * PartRow<D>::FLOATS;
+                            if (lane < PartRow<D>::BYTES / 16) copy16(to + r * PartRow<D>::BYTES, from);
+                            if (lane + 32 < PartRow<D>::BYTES / 16) copy16(to + r * PartRow<D>::BYTES + 512, from + 128);
                         }
                     }
-                    float top = MM;
-                    for (int o = width >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    const float g = ex2((MM - (top == -INFINITY ? 0.f : top)) * sl);
-                    LL *= g;
-                    acc.x *= g;
-                    acc.y *= g;
-                    acc.z *= g;
-                    acc.w *= g;
-                    for (int o = width >> 1; o > 0; o >>= 1) {
-                        LL += __shfl_xor_sync(0xffffffffu, LL, o);
-                        acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o);
-                        acc.y += __shfl_xor_sync(0xffffffffu, acc.y, o);
-                        acc.z += __shfl_xor_sync(0xffffffffu, acc.z, o);
-                        acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
-                    }
-                    const int tok = r / p.unit_heads, in_group = h0 + r - tok * p.unit_heads;
-                    if ((lane & (width - 1)) != 0 || u >= end || in_group >= p.group) continue;
-                    const int64_t out_token = static_cast<int64_t>(it.row0) + tok;
-                    const int head = kvh * p.group + in_group;
-                    const float inv = LL == 0.f ? 0.f : 1.f / LL;
-                    __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + out_token * p.o_row + head * p.o_head + 4 * c4;
-                    *reinterpret_cast<uint2 *>(dst) =
-                        make_uint2(pack_bf16x2(__float_as_uint(acc.x * inv), __float_as_uint(acc.y * inv)),
-                                   pack_bf16x2(__float_as_uint(acc.z * inv), __float_as_uint(acc.w * inv)));
-                    if (c4 == 0) store_lse(out_token, head, top, LL);
                 }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                arrive(joined);
+                if (!alive || !wait(joined, n_joined++ & 1)) break;
+#pragma unroll 1
+                for (int which = at_once ? 0 : round; which < (at_once ? 2 : round + 1); ++which) {
+                    const Pending it = pend[which];
+                    const int first = which == 0 ? first0 : first1, n = which == 0 ? n0 : n1;
+                    if (it.parts == 0) continue;
+                    const int kvh = it.unit / p.blocks, h0 = (it.unit - kvh * p.blocks) * p.unit_heads;
+                    float *mem = reinterpret_cast<float *>(base + (at_once && which == 1 ? size0 : 0));
+                    const int step = n * PartRow<D>::FLOATS;    // from part to part
+                    // A row's weights of its parts, in place of their maxima: by a lane for each part,
+                    // or, where there are many rows, by a lane for each row.
+                    const bool many = n > 32;
+                    const int by = many ? 1 : 32, q0 = many ? 0 : lane;
+#pragma unroll 1
+                    for (int r = many ? threadIdx.x : warp; r < n; r += many ? 256 : 8) {
+                        float *at = mem + r * PartRow<D>::FLOATS + D;
+                        float M = -INFINITY, L = 0.f;
+#pragma unroll 4
+                        for (int q = q0; q < it.parts; q += by) M = fmaxf(M, at[q * step]);
+                        if (!many)
+                            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+                        const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll 4
+                        for (int q = q0; q < it.parts; q += by) L += at[q * step + 1] * ex2((at[q * step] - ref) * sl);
+                        if (!many)
+                            for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+                        const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll 4
+                        for (int q = q0; q < it.parts; q += by) at[q * step] = ex2((at[q * step] - ref) * sl) * inv;
+                        const int tok = (first + r) / p.unit_heads, in_group = h0 + first + r - tok * p.unit_heads;
+                        if (q0 == 0 && in_group < p.group)
+                            store_lse(p, static_cast<int64_t>(it.row0) + tok, kvh * p.group + in_group, M, L);
+                    }
+                    __syncwarp();
+                    arrive(joined);
+                    if (!wait(joined, n_joined++ & 1)) break;
+                    // Then four columns of a row by a lane.
+                    const int side = lane / (D / 4), col = (lane & (D / 4 - 1)) * 4;
+#pragma unroll 4
+                    for (int r = warp * (128 / D) + side; r < n; r += 8 * (128 / D)) {
+                        const float *at = mem + r * PartRow<D>::FLOATS;
+                        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                        for (int q = 0; q < it.parts; ++q) {
+                            const float4 v = *reinterpret_cast<const float4 *>(at + q * step + col);
+                            const float f = at[q * step + D];
+                            acc.x += v.x * f;
+                            acc.y += v.y * f;
+                            acc.z += v.z * f;
+                            acc.w += v.w * f;
+                        }
+                        const int tok = (first + r) / p.unit_heads, in_group = h0 + first + r - tok * p.unit_heads;
+                        if (in_group >= p.group) continue;
+                        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + (static_cast<int64_t>(it.row0) + tok) * p.o_row +
+                                             (kvh * p.group + in_group) * p.o_head + col;
+                        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(__float_as_uint(acc.x), __float_as_uint(acc.y)),
+                                                                     pack_bf16x2(__float_as_uint(acc.z), __float_as_uint(acc.w)));
+                    }
+                    __syncwarp();
+                }
+                if (at_once) break;
+                arrive(joined);                                // the memory is free again
+                if (!wait(joined, n_joined++ & 1)) break;
             }
         }
     } else {
@@ -659,10 +741,10 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
             // -------------------------------------------------------- loads
             uint32_t c = 0;                            // ring position
             const int box = KEYS < (1 << p.b.page_shift) ? KEYS : (1 << p.b.page_shift), boxes = KEYS / box;
-            for (uint32_t k = 0; w.more() && alive; ++k, w.next()) {
-                const Seq &q = w.q;
-                const bool two = w.tokens() > p.tokens;
-                const int unit = w.unit(), kvh = unit / p.blocks;
+            for (uint32_t k = 0; there(k); ++k) {
+                const Item &it = items[k % ITEMS];
+                const bool two = it.ntok > p.tokens;
+                const int unit = it.unit, kvh = unit / p.blocks, len = it.len, todo = it.todo;
                 if (k > 0 && !wait(q_empty, (k - 1) & 1)) break;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(q_full, (two ? 2 : 1) * HALVES * p.tokens * p.unit_heads * 128);
@@ -670,14 +752,14 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
                         for (int hf = 0; hf < HALVES; ++hf)
                             tma_load_3d(sm_q + t * Sh::TILE_BYTES + hf * Sh::HALF_BYTES, &p.tmQ, q_full, hf * 64,
                                         kvh * p.group + (unit - kvh * p.blocks) * p.unit_heads,
-                                        q.start + w.first_token() + t * p.tokens);
+                                        it.row0 + t * p.tokens);
                 }
                 __syncwarp();
-                const int32_t *table = p.b.page_table + w.s * p.b.table_row;
-                const int pages = (q.len + (1 << p.b.page_shift) - 1) >> p.b.page_shift;
+                const int32_t *table = p.b.page_table + it.seq * p.b.table_row;
+                const int pages = (len + (1 << p.b.page_shift) - 1) >> p.b.page_shift;
                 int cached0 = 0, cached_n = 0, ids = -1;  // page ids, one per lane
-                for (int j = 0; j < w.todo() && alive; ++j) {
-                    const int kt = q.tile(w.t0 + j), key0 = kt * KEYS, ext = extent(q.len, kt);
+                for (int j = 0; j < todo && alive; ++j) {
+                    const int kt = it.tile(j), key0 = kt * KEYS, ext = extent(len, kt);
                     const int n_box = (ext + box - 1) / box, page0 = key0 >> p.b.page_shift;
                     if (page0 + boxes > cached0 + cached_n) {
                         cached0 = page0;
@@ -685,7 +767,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
                         // a page that no row sees may be another sequence's by now, or nobody's
                         const int64_t first = static_cast<int64_t>(cached0 + lane) << p.b.page_shift;
                         const bool seen = cached0 + lane < pages &&
-                                          (p.window == 0 || first + (int64_t(1) << p.b.page_shift) > q.lo || first < p.sinks);
+                                          (p.window == 0 || first + (int64_t(1) << p.b.page_shift) > it.lo || first < p.sinks);
                         ids = seen ? table[cached0 + lane] : -1;
                         if (seen && (ids < 0 || ids >= p.b.num_pages)) {
                             atomicCAS(p.b.status, 0, UB_ERR_ARG);
@@ -696,7 +778,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
                         const uint32_t st = c % NST;
                         if (c >= NST && !wait(kv_empty + 8 * st, (c / NST - 1) & 1)) break;
                         // The last tile of V goes through the zeroing warp when it ends inside 16 keys.
-                        const bool fix = kind == 1 && ext > q.len - key0;
+                        const bool fix = kind == 1 && ext > len - key0;
                         const uint32_t bar = (fix ? v_raw : kv_full) + 8 * st;
                         if (lane == 0) mbar_arrive_expect_tx(bar, n_box * HALVES * box * 128);
                         __syncwarp();
@@ -710,71 +792,134 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
                         if (lane == 0) *issued = c + 1;
                     }
                 }
+                if (!alive) break;
+                arrive(it_empty + 8 * (k % ITEMS));
             }
         } else if (warp < 11) {
             // -------------------------------------------------------- MMA issue
+            // Step by step: O += P V of a tile, then S of the pipeline's next one. The pipelines take
+            // turns, so that one's MMAs run during the other's softmax: without turns the two fall
+            // into step and leave the tensor core and the arithmetic idle by turns (32 sequences of 64
+            // drafts over 8192 keys, 4 query heads to a key head: 272 against 231 us, heads of 64: 224
+            // against 173). But a turn does not wait for keys that have not landed.
             const int i = warp - 9;
-            uint32_t c = 0, n_p = 0;
-            const uint32_t tp = tmem + TM_S + i * 128, to = tmem + TM_O + i * 128;
+            uint32_t c = 0, n_p = 0, step = 0;
+            const uint32_t ts = tmem + TM_S + i * 128, to = tmem + TM_O + i * 128;
             const uint64_t k_desc = smem_desc_sw128(sm_kv), v_desc = smem_desc_v(sm_kv, Sh::HALF_BYTES);
             constexpr uint32_t o_idesc = attn_idesc(D, true);
             // A pipeline skips the other's key tiles, and the ring may turn meanwhile: a barrier's
             // parity tells two turns apart only once the loads of this one have been issued.
-            auto wait_kv = [&](uint32_t at) {
-                bool there = __all_sync(0xffffffffu, static_cast<int32_t>(*issued - at) > 0) != 0;
-                if (!there) {
-                    WaitClock clk;
-                    for (uint32_t n = 1; !there; ++n) {
-                        there = __all_sync(0xffffffffu, static_cast<int32_t>(*issued - at) > 0) != 0;
-                        if ((n & 15u) == 0 && !there && !__all_sync(0xffffffffu, clk.ok(wc))) return alive = false;
-                    }
+            auto poll = [&](const volatile uint32_t *word, uint32_t least) {  // until *word >= least
+                bool come = __all_sync(0xffffffffu, static_cast<int32_t>(*word - least) >= 0) != 0;
+                if (come) return true;
+                WaitClock clk;
+                for (uint32_t n = 1; !come; ++n) {
+                    come = __all_sync(0xffffffffu, static_cast<int32_t>(*word - least) >= 0) != 0;
+                    if ((n & 15u) == 0 && !come && !__all_sync(0xffffffffu, clk.ok(wc))) return alive = false;
                 }
-                return wait(kv_full + 8 * (at % NST), (at / NST) & 1);
+                return true;
             };
-            for (uint32_t k = 0; w.more() && alive; ++k, w.next()) {
-                const bool two = w.tokens() > p.tokens;
-                const int todo = w.todo(), len = w.q.len;
-                const int last = two ? todo - 1 : todo - 1 - ((todo - 1 - i) & 1);  // this pipeline's; below zero: none
+            auto wait_kv = [&](uint32_t at) {
+                return poll(issued, at + 1) && wait(kv_full + 8 * (at % NST), (at / NST) & 1);
+            };
+            auto landed = [&](uint32_t at) {
+                return __all_sync(0xffffffffu, static_cast<int32_t>(*issued - at) > 0 &&
+                                                   mbar_try_wait(kv_full + 8 * (at % NST), (at / NST) & 1)) != 0;
+            };
+            auto pass = [&](uint32_t step) {
+                if (lane == 0) turn[i] = step;
+                __syncwarp();
+            };
+            for (uint32_t k = 0; there(k); ++k) {
+                // Broadcast from lane 0, so that the compiler knows them to be the same in every lane:
+                // descriptors then stay in uniform registers, and an issue costs less than the MMA.
+                auto same = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+                const Item &it = items[k % ITEMS];
+                const bool two = same(it.ntok) > p.tokens;
+                const int todo = same(it.todo), len = same(it.len), t0 = same(it.t0), far = same(it.far), gap = same(it.near) - far;
+                const int stride = two ? 1 : 2, j0 = two ? 0 : i;
                 const uint64_t q_desc = smem_desc_sw128(sm_q + (two ? i * Sh::TILE_BYTES : 0));
-                if (!wait(q_full, k & 1)) break;
-                if (last < 0) arrive(q_empty);
-                // O of the last item has been read
-                if (last < 0 && k > 0 && !wait(o_empty + 8 * i, (k - 1) & 1)) break;
-                for (int j = 0; j < todo; ++j, c += 2) {
-                    if (!two && (j & 1) != i) continue;
-                    const uint32_t ks = c % NST, vs = (c + 1) % NST;
-                    const int ext = extent(len, w.q.tile(w.t0 + j));
-                    if (!wait_kv(c)) break;
+                auto ext_of = [&](int j) { return extent(len, t0 + j < far ? t0 + j : t0 + j + gap); };
+                auto scores = [&](int j) {             // S of key tile j, which has landed
+                    const uint32_t st = (c + 2 * j) % NST;
+                    const uint32_t s_idesc = attn_idesc(ext_of(j), false), freed = kv_empty + 8 * st;
+                    const uint64_t kk = k_desc + st * (Sh::TILE_BYTES / 16);
+                    const bool last = j + stride >= todo;
                     tc_fence_after();
                     if (elect_one()) {
-                        const uint32_t s_idesc = attn_idesc(ext, false);
-                        const uint64_t kk = k_desc + ks * (Sh::TILE_BYTES / 16);
 #pragma unroll
                         for (int s = 0; s < D / 16; ++s) {
                             const int o = (s / 4) * (Sh::HALF_BYTES / 16) + (s % 4) * 2;
-                            umma_ss(tp, q_desc + o, kk + o, s_idesc, s > 0);
+                            umma_ss(ts, q_desc + o, kk + o, s_idesc, s > 0);
                         }
                         umma_commit(s_full + 8 * i);
-                        umma_commit(kv_empty + 8 * ks);
-                        if (!two) umma_commit(kv_empty + 8 * ks);
-                        if (j == last) umma_commit(q_empty);
+                        umma_commit(freed);
+                        if (!two) umma_commit(freed);
+                        if (last) umma_commit(q_empty);
                     }
                     __syncwarp();
-                    if (!wait(p_full + 8 * i, n_p & 1)) break;
-                    ++n_p;
-                    if (k > 0 && j == (two ? 0 : i) && !wait(o_empty + 8 * i, (k - 1) & 1)) break;
-                    if (!wait_kv(c + 1)) break;
-                    tc_fence_after();
-                    if (elect_one()) {
-                        const uint64_t v = v_desc + vs * (Sh::TILE_BYTES / 16);
-                        for (int s = 0; s < ext / 16; ++s)
-                            umma_ts(to, tp + s * 8, v + s * 128, o_idesc, j > (two ? 0 : i) || s > 0);
-                        umma_commit(kv_empty + 8 * vs);
-                        if (!two) umma_commit(kv_empty + 8 * vs);
-                        if (j == last) umma_commit(o_full + 8 * i);
-                    }
-                    __syncwarp();
+                };
+                if (!wait(q_full, k & 1)) break;
+                if (j0 >= todo) {
+                    arrive(q_empty);
+                    if (k > 0 && !wait(o_empty + 8 * i, (k - 1) & 1)) break;
+                } else {
+                    if (!wait_kv(c + 2 * j0)) break;
+                    scores(j0);
                 }
+                const int steps = two ? todo : (todo + 1) / 2;  // of either pipeline
+                for (int n = 0; n < steps; ++n) {
+                    const int j = j0 + n * stride, next = j + stride;
+                    ++step;
+                    if (j >= todo) {                   // the other's last tile
+                        pass(step);
+                        break;
+                    }
+                    const uint32_t at = c + 2 * j + 1, st = at % NST, freed = kv_empty + 8 * st;
+                    const uint64_t v = v_desc + st * (Sh::TILE_BYTES / 16);
+                    const int ext = ext_of(j);
+                    // O of the last item has been read
+                    if (k > 0 && n == 0 && !wait(o_empty + 8 * i, (k - 1) & 1)) break;
+                    auto product = [&](int from) {     // O += P V, from step `from` on
+                        tc_fence_after();
+                        if (elect_one()) {
+                            if (ext == KEYS) {
+#pragma unroll
+                                for (int s = 0; s < KEYS / 16; ++s)
+                                    if (s >= from) umma_ts(to, ts + s * 8, v + s * 128, o_idesc, n > 0 || s > 0);
+                            } else {  // the sequence's last keys
+                                for (int s = 0; s < ext / 16; ++s) umma_ts(to, ts + s * 8, v + s * 128, o_idesc, n > 0 || s > 0);
+                            }
+                            umma_commit(freed);
+                            if (!two) umma_commit(freed);
+                            if (next >= todo) umma_commit(o_full + 8 * i);
+                        }
+                        __syncwarp();
+                    };
+                    if (!wait_kv(at) || !poll(turn + (1 - i), step - 1 + i)) break;
+                    if (EARLY) {
+                        if (!wait(p_part + 8 * i, n_p & 1)) break;
+                        tc_fence_after();
+                        if (ext == KEYS && elect_one()) {
+#pragma unroll
+                            for (int s = 0; s < PART; ++s) umma_ts(to, ts + s * 8, v + s * 128, o_idesc, n > 0 || s > 0);
+                        }
+                        __syncwarp();
+                    }
+                    if (!wait(p_full + 8 * i, n_p & 1)) break;
+                    product(EARLY ? PART : 0);
+                    const bool now = next < todo && landed(c + 2 * next);
+                    if (now) scores(next);
+                    pass(step);
+                    if (next < todo && !now) {
+                        if (!wait_kv(c + 2 * next)) break;
+                        scores(next);
+                    }
+                    ++n_p;
+                }
+                if (!alive) break;
+                c += 2 * todo;
+                arrive(it_empty + 8 * (k % ITEMS));
             }
             // everything issued has completed before TMEM goes back
             if (elect_one()) {
@@ -783,13 +928,40 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
             }
             __syncwarp();
         } else {
-            // -------------------------------------------------------- the last keys of V
+            // -------------------------------------------------------- schedule, the last keys of V
+            Walk w(p);
+            if (p.many_units)
+                begin<int64_t>(w, lane, blockIdx.x, gridDim.x);
+            else
+                begin<int>(w, lane, blockIdx.x, gridDim.x);
+            auto publish = [&](uint32_t k) {
+                if (k >= ITEMS && !wait(it_empty + 8 * (k % ITEMS), (k / ITEMS - 1) & 1)) return;
+                if (lane == 0) {
+                    Item it;
+                    it.seq = -1;
+                    if (w.more()) {
+                        const int first = w.first_token();
+                        it = Item{w.s, w.q.start + first, w.tokens(), first, w.unit(), w.q.len, w.q.text, w.q.lo, w.q.near, w.q.far,
+                                  w.t0, w.todo(), w.whole() ? 1 : 0};
+                        if (!it.whole) {
+                            const int64_t item0 = w.x - w.off;
+                            const int a = w.split.owner(item0);
+                            pend[w.t0 == 0 ? 1 : 0] =
+                                Pending{it.row0, it.ntok, it.unit, a, w.split.owner(item0 + w.q.span() - w.q.per) - a + 1};
+                        }
+                    }
+                    items[k % ITEMS] = it;
+                }
+                arrive(it_full + 8 * (k % ITEMS));
+            };
             uint32_t c = 0, used = 0;                  // ring position; phase bit per stage of v_raw
-            for (; w.more() && alive; w.next()) {
-                const int todo = w.todo(), len = w.q.len;
-                const int kt = w.q.tile(w.t0 + todo - 1), valid = len - kt * KEYS;
-                const int ext = todo > 0 ? extent(len, kt) : 0;
-                if (ext > valid) {
+            publish(0);
+            for (uint32_t k = 0; w.more() && alive; ++k) {
+                const int todo = w.todo(), kt = w.q.tile(w.t0 + todo - 1), valid = w.q.len - kt * KEYS;
+                const int ext = todo > 0 ? extent(w.q.len, kt) : 0;
+                w.next();
+                publish(k + 1);                        // before this one's last keys are waited for
+                if (alive && todo > 0 && ext > valid) {
                     const uint32_t st = (c + 2 * todo - 1) % NST;
                     if (!wait(v_raw + 8 * st, (used >> st) & 1)) break;
                     used ^= 1u << st;
