@@ -304,6 +304,7 @@ struct Plan {
     uint32_t split_end;  // ranks [0, split_end): pieces of the split items, item by item
     uint32_t total;      // ... then the whole items
     int n_split;         // token tiles (of each unit) that are split
+    uint32_t whole;      // not 0: ranks [0, whole) are whole items, the pieces of the rest follow
 };
 constexpr int MIN_SPLIT = PROMPT_WHOLE_KEYS / PROMPT_KEYS;
 // Key tiles of a piece, at least, where the CTAs would allow shorter ones. It matters to a few
@@ -316,9 +317,25 @@ constexpr int MIN_PIECE = 5;
 template <bool WINDOW>
 __device__ Plan plan_of(const Schedule &sc, int units, int ctas, int slots, int cap)
 {
-    Plan pl{1, 0u, static_cast<uint32_t>(sc.tiles) * units, 0};
+    Plan pl{1, 0u, static_cast<uint32_t>(sc.tiles) * units, 0, 0u};
     const int cmax = WINDOW && sc.cmax > cap ? cap : sc.cmax;
-    if (pl.total >= static_cast<uint32_t>(ctas) || cmax <= MIN_SPLIT) return pl;
+    if (cmax <= MIN_SPLIT) return pl;
+    if (pl.total >= static_cast<uint32_t>(ctas)) {
+        // Windows make items of one length, of which one more than fill the CTAs takes as long as
+        // twice as many: the items of an incomplete last round are split where two CTAs or more can
+        // share each of them and they have more than MIN_SPLIT key tiles (of one or two rounds: of
+        // more rounds the last is a small part).
+        const uint32_t rounds = pl.total / ctas, left = pl.total - rounds * ctas;
+        if (!WINDOW || rounds > 2u || left == 0u) return pl;
+        uint32_t pieces = static_cast<uint32_t>(ctas) / left;
+        if (pieces * MIN_PIECE > static_cast<uint32_t>(cmax)) pieces = cmax / MIN_PIECE;
+        if (pieces * left > static_cast<uint32_t>(slots)) pieces = slots / left;
+        if (pieces < 2u || static_cast<uint32_t>(sc.counts(MIN_SPLIT + 1)) * units <= pl.total - left) return pl;
+        pl.pieces = static_cast<int>(pieces);
+        pl.whole = pl.total - left;
+        pl.total = pl.whole + left * pieces;
+        return pl;
+    }
     // 32 limits at once, from an even share up to the longest item, closer together near the
     // first; of those that give no more pieces than there are CTAs and slots, the one of the
     // shortest longest piece.
@@ -344,11 +361,20 @@ template <bool WINDOW>
 __device__ Item item_of(const Schedule &sc, const Plan &pl, int units, uint32_t g)
 {
     uint32_t rank = g;   // among the items; fewer than 2^32: T * heads rows
-    int piece = 0, pieces = 1;
-    if (g < pl.split_end) {
+    int piece = 0, pieces = 1, slot = -1;
+    if (WINDOW && pl.whole > 0u) {
+        if (g >= pl.whole) {
+            pieces = pl.pieces;
+            rank = (g - pl.whole) / static_cast<uint32_t>(pieces);
+            piece = static_cast<int>(g - pl.whole - rank * pieces);
+            slot = static_cast<int>(rank) * pieces;
+            rank += pl.whole;
+        }
+    } else if (g < pl.split_end) {
         pieces = pl.pieces;
         rank = g / static_cast<uint32_t>(pieces);
         piece = static_cast<int>(g - rank * pieces);
+        slot = static_cast<int>(rank) * pieces;
     } else if (pl.pieces > 1) {
         rank = g - static_cast<uint32_t>(pl.n_split * units * (pl.pieces - 1));
     }
@@ -362,7 +388,7 @@ __device__ Item item_of(const Schedule &sc, const Plan &pl, int units, uint32_t 
     if (pieces > 1) {
         it.j0 = piece_begin(level, piece, pieces);
         it.j1 = piece_begin(level, piece + 1, pieces);
-        it.slot = static_cast<int>(rank) * pieces;
+        it.slot = slot;
         it.piece = piece;
         it.pieces = pieces;
     }
@@ -471,7 +497,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
         const float sl = p.scale * 1.4426950408889634f;
         uint32_t n_s = 0, n_l = 0;                     // phases used
         Item it;
-        for (uint32_t k = 0; next_item(k, it); ++k) {
+        uint32_t k = 0;
+        for (; next_item(k, it); ++k) {
             const Sight<WINDOW> in = sight<WINDOW>(p, it.off);
             const Range2 r = ranges(it, tpt, in.gap());
             if (r.n[i] == 0) continue;
@@ -558,9 +585,10 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
             sm_max[i * 128 + row] = m;
             arrive(l_full + 8 * i);
         }
-        // A split item is the only one of its CTA and of the CTAs of its other pieces. When all
-        // pieces' parts are there, each CTA joins a share: 16 columns of 128 rows at a time.
-        it = items[0];
+        // A split item is the last one of its CTA (without windows the only one) and of the CTAs of
+        // its other pieces. When all pieces' parts are there, each CTA joins a share: 16 columns of
+        // 128 rows at a time.
+        it = items[k > 0 ? (k - 1) % ITEMS : 0];
         if (it.slot >= 0 && alive) {
             if (warp == 0) {
                 // a count of the item's pieces, and one, never reset, of how often all have come
@@ -963,7 +991,10 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
         };
         auto draw = [&](uint32_t k) {
             uint32_t g = 2 * gridDim.x - 1 - blockIdx.x;
-            if (k >= 2) {
+            if (WINDOW && plan.whole > 0u) {
+                // a piece of the last round is its CTA's last item: all is dealt, nothing drawn
+                if (k >= 2) g = k * gridDim.x + blockIdx.x;
+            } else if (k >= 2) {
                 uint32_t ticket = 0;
                 if (lane == 0) ticket = atomicAdd(p.tickets, 1u);
                 g = 2 * gridDim.x + __shfl_sync(0xffffffffu, ticket, 0);

@@ -145,6 +145,26 @@ def test_few_tokens_over_long_windows_are_split(buf, window, sinks, heads, kv_he
     check(b, q, lambda s: (b.rows(b.k_cache, s), b.rows(b.v_cache, s)), out, lse, window, sinks, new)
 
 
+@pytest.mark.parametrize("n,heads,kv_heads,dim,window", [(10, 8, 8, 128, 2500), (11, 8, 8, 64, 1700), (20, 8, 8, 64, 2500), (40, 8, 2, 128, 3300),
+                                                         (13, 6, 6, 128, 2000), (39, 4, 4, 64, 1500)])
+def test_incomplete_last_rounds_are_split(buf, n, heads, kv_heads, dim, window):
+    """A few items more than one or two for each SM: those are cut along their keys, after the whole ones."""
+    new = [300 - 7 * (i % 3) for i in range(n)]
+    kv = [m + 4000 + 13 * i for i, m in enumerate(new)]
+    b = ref.Batch(new, kv, page=32, kv_heads=kv_heads, dim=dim, pad=1, seed=n, fill=float("nan"))
+    buf.set_active_shape([b.T, 256])
+    q = b.randn(b.T, heads, dim, std=1.5)
+    table = drop_unseen(b, window, 4, new)
+    out = sentinel((b.T, heads, dim))
+    args = (q, b.k_cache, b.v_cache, b.starts, b.lens, table)
+    _, lse = buf.attn_prompt_paged(*args, out=out, lse=True, window=window, sinks=4)
+    ok(buf)
+    check(b, q, lambda s: (b.rows(b.k_cache, s), b.rows(b.v_cache, s)), out, lse, window, 4, new)
+    for _ in range(2):
+        assert torch.equal(buf.attn_prompt_paged(*args, window=window, sinks=4)[:sum(new)], out[:sum(new)])
+    ok(buf)
+
+
 def test_rows_without_a_key(buf):
     """kv_lens below the new tokens: the first rows have no position in the cache."""
     b = ref.Batch([40, 200], [30, 140], page=16, kv_heads=2, dim=128, seed=3, fill=float("nan"))
