@@ -46,14 +46,13 @@ constexpr int SOFTMAX_REGS = 216, SINGLE_REGS = 72;
 static_assert(2 * SOFTMAX_REGS + SINGLE_REGS == 3 * 168, "register split");
 constexpr int ITEMS = 4;                 // items published ahead
 constexpr int TM_S = 0, TM_O = 256;      // TMEM columns: S_i at 128 i (and P_i in its place), O_i at 256 + 128 i
-constexpr int PART = 4;                  // steps of 16 keys whose weights are handed over early (heads of 128)
 constexpr float RESCALE_LOG2 = 8.f;      // growth of the maximum (log2) that is put off
 // Units of the split, about 0.08 us: what a key tile takes in an item of one q tile and of two, heads
 // of 64 and of 128; the end of an item (the pipelines run empty, O joined and written, the next
 // queries loaded); a join. From the times of CTAs of calls of mixed items: key tiles 0.5-0.6 and
 // 1.1 us with heads of 64, 0.6-1.0 and 1.2 with heads of 128, ends 2-4 us, a join 6.
 __host__ __device__ constexpr int tile_units(int head_dim, bool two) { return two ? 15 : (head_dim == 64 ? 7 : 9); }
-constexpr int ITEM_COST = 42, JOIN_COST = 80;
+constexpr int ITEM_COST = 50, JOIN_COST = 80;
 constexpr int MIN_UNITS = 24;            // of a CTA, at least: no less than any tile
 static_assert(ITEM_COST <= TREE_MOST_UNITS && tile_units(128, true) <= MIN_UNITS, "units");
 
@@ -153,8 +152,9 @@ struct Split {
 struct Walk {
     const TreeParams &p;
     Split split;
-    int64_t x, left;  // first unit of the item here (not counted for whole items), units to go
+    int64_t x, left;  // first unit of the item here, units to go; whole items: items to go
     int off;          // units of the item that are others' (before x)
+    bool by_items;    // whole items only
     int s, item;      // sequence, item of it
     int t0, t1;
     Seq q;
@@ -163,6 +163,11 @@ struct Walk {
     __device__ __forceinline__ bool more() const { return left > 0 && s < p.b.n_seqs; }
     __device__ __forceinline__ void cut()
     {
+        if (by_items) {
+            t0 = 0;
+            t1 = q.tiles;
+            return;
+        }
         const uint32_t per = q.per, end = off + left < q.span() ? static_cast<int>(off + left) : q.span();
         t0 = static_cast<int>((off + per - 1) / per);
         t1 = static_cast<int>((end + per - 1) / per);
@@ -179,7 +184,7 @@ struct Walk {
     }
     __device__ __forceinline__ void next()
     {
-        const int units = q.cost() - off < left ? q.cost() - off : static_cast<int>(left);
+        const int units = by_items ? 1 : (q.cost() - off < left ? q.cost() - off : static_cast<int>(left));
         x += units;
         left -= units;
         off = 0;
@@ -191,8 +196,8 @@ struct Walk {
             settle_on();
         }
     }
-    __device__ __forceinline__ int unit() const { return item / q.blocks; }
-    __device__ __forceinline__ int first_token() const { return (item % q.blocks) * 2 * p.tokens; }
+    __device__ __forceinline__ int unit() const { return q.blocks == 1 ? item : item / q.blocks; }
+    __device__ __forceinline__ int first_token() const { return (item - unit() * q.blocks) * 2 * p.tokens; }
     __device__ __forceinline__ int tokens() const  // of this item
     {
         const int n = q.n - first_token();
@@ -211,6 +216,7 @@ __device__ __forceinline__ void begin(Walk &w, int lane, int cta, int grid)
     const TreeParams &p = w.p;
     w.left = w.x = 0;
     w.off = w.s = w.item = w.t0 = w.t1 = 0;
+    w.by_items = false;
     w.split = Split{0, 0};
     const int n_seqs = p.b.n_seqs;
     Seq own = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
@@ -229,24 +235,25 @@ __device__ __forceinline__ void begin(Walk &w, int lane, int cta, int grid)
     total = warp_sum(total) * p.units;
     most = __reduce_max_sync(0xffffffffu, most);
     if (items == 0) return;
-    // A CTA per item where no item is much longer than an equal share would be: a share saves the
-    // difference and costs a join. Else equal shares, of at least MIN_UNITS units, or a CTA per
-    // item where those are shorter.
-    const bool whole = items <= grid && static_cast<int64_t>(most - JOIN_COST) * grid <= total - items * ITEM_COST;
-    I ctas = whole ? items : total / MIN_UNITS;
-    if (!whole && ctas < items) ctas = items;
-    ctas = ctas > grid ? grid : ctas;
+    // Whole items, as many for each CTA, where the longest ones in every round would not take much
+    // longer than equal shares: a share saves the difference and costs a join. Else equal shares,
+    // of at least MIN_UNITS units.
+    const I rounds = quotient(items + grid - 1, static_cast<I>(grid));
+    w.by_items = static_cast<int64_t>(rounds) * most <= quotient(total - items * ITEM_COST, static_cast<I>(grid)) + JOIN_COST;
+    const I work = w.by_items ? items : total;
+    I ctas = w.by_items ? items : total / MIN_UNITS;
+    ctas = ctas < 1 ? 1 : (ctas > grid ? grid : ctas);
     if (cta >= ctas) return;
-    const I base = quotient(total, ctas);
-    w.split = Split{base, total - base * ctas};
-    const I at = whole ? cta : static_cast<I>(w.split.first(cta));
+    const I base = quotient(work, ctas);
+    w.split = Split{base, work - base * ctas};
+    const I at = static_cast<I>(w.split.first(cta));
     // The sequence that holds item or unit `at`, and those before it.
     I seen = 0;
 #pragma unroll 1
     for (int i0 = 0; i0 < n_seqs; i0 += 32) {
         Seq q = own;
         if (i0 > 0) q = seq_of(p, i0 + lane < n_seqs ? i0 + lane : n_seqs - 1);
-        I mine = i0 + lane < n_seqs ? static_cast<I>(q.blocks) * p.units * (whole ? 1 : q.cost()) : 0, upto = mine;
+        I mine = i0 + lane < n_seqs ? static_cast<I>(q.blocks) * p.units * (w.by_items ? 1 : q.cost()) : 0, upto = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const I y = __shfl_up_sync(0xffffffffu, upto, o);
@@ -262,12 +269,11 @@ __device__ __forceinline__ void begin(Walk &w, int lane, int cta, int grid)
         }
         seen += __shfl_sync(0xffffffffu, upto, 31);
     }
-    if (whole) {
+    w.x = at;
+    w.left = w.split.first(cta + 1) - at;
+    if (w.by_items) {
         w.item = static_cast<int>(at - seen);
-        w.left = w.q.span();
     } else {
-        w.x = at;
-        w.left = w.split.first(cta + 1) - at;
         w.item = static_cast<int>(quotient(at - seen, static_cast<I>(w.q.cost())));
         w.off = static_cast<int>(at - seen - static_cast<I>(w.item) * w.q.cost());
     }
@@ -281,7 +287,7 @@ struct Item {
     int seq;         // sequence; -1: no more items
     int row0, ntok;  // first token of the call, tokens
     int first;       // first draft
-    int unit;        // heads
+    int kvh, h0;     // key/value head; first query head, of those that share it
     int len, text;   // as in Seq
     int lo, near, far;
     int t0, todo;    // key tiles in sight: the first one, how many (0: the item has no keys)
@@ -290,7 +296,7 @@ struct Item {
 };
 // An item that other CTAs have parts of, for the join.
 struct Pending {
-    int row0, n, unit;  // first token and tokens, heads
+    int row0, n, kvh, h0;
     int a, parts;       // the CTA in which it begins, and how many have parts; 0: no such item
 };
 
@@ -316,15 +322,18 @@ __device__ __forceinline__ void keys_seen(const TreeParams &p, int start, int te
         bits[w] = low_bits(text - first);
         if (p.window > 0) bits[w] &= ~low_bits(pos - p.window + 1 - first) | low_bits(p.sinks - first);
     }
-    const int gone = key0 - text;  // drafts before this tile, or before the cache
-    const int least = gone > -text ? gone : -text;
-    for (int d = 0; i >= 0 && i >= least; ++d) {
-        const int c = i - gone;
-        const bool seen = c < KEYS && (p.window == 0 || d < p.window || pos - d < p.sinks);
+    // The ancestors come in falling order: word by word, from the last.
+    const int gone = key0 - text;  // drafts before this tile
+    if (gone + KEYS <= 0) return;  // no drafts in it (the same for all lanes)
+    int d = 0;                     // steps from the row's own draft
+    for (; i >= gone + KEYS; ++d) i = parent_of(p, start, i);
 #pragma unroll
-        for (int w = 0; w < 4; ++w)
-            if (seen && (c >> 5) == w) bits[w] |= 1u << (c & 31);
-        i = parent_of(p, start, i);
+    for (int w = 3; w >= 0; --w) {
+        const int from = gone + 32 * w, least = from > -text ? from : -text;  // (below -text: before the cache)
+        for (; i >= 0 && i >= least; ++d) {
+            if (p.window == 0 || d < p.window || pos - d < p.sinks) bits[w] |= 1u << ((i - from) & 31);
+            i = parent_of(p, start, i);
+        }
     }
     __syncwarp();
 }
@@ -352,7 +361,6 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
 {
     using Sh = TreeShape<D>;
     constexpr int NST = Sh::STAGES, HALVES = D / 64;
-    constexpr bool EARLY = D == 128;
     extern __shared__ __align__(1024) uint8_t base[];
     const uint32_t sm_q = smem_u32(base), sm_kv = sm_q + 2 * Sh::TILE_BYTES;
     float *sm_max = reinterpret_cast<float *>(base + (2 + NST) * Sh::TILE_BYTES);  // [2][128]
@@ -362,14 +370,14 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
                    misc = kv_full + 24 * NST;
     const uint32_t q_full = misc, q_empty = misc + 8, s_full = misc + 16, p_full = misc + 32, o_full = misc + 48,
                    o_empty = misc + 64, both = misc + 80, parts_done = misc + 88, join_go = misc + 96, drain = misc + 112,
-                   p_part = misc + 128, joined = misc + 144;
-    const uint32_t it_full = misc + 152, it_empty = it_full + 8 * ITEMS;
-    Item *items = reinterpret_cast<Item *>(reinterpret_cast<uint8_t *>(bars) + 24 * NST + 152 + 16 * ITEMS);
+                   joined = misc + 128;
+    const uint32_t it_full = misc + 136, it_empty = it_full + 8 * ITEMS;
+    Item *items = reinterpret_cast<Item *>(reinterpret_cast<uint8_t *>(bars) + 24 * NST + 136 + 16 * ITEMS);
     Pending *pend = reinterpret_cast<Pending *>(items + ITEMS);  // begun before this CTA; going on after it
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(pend + 2);
     volatile uint32_t *issued = tmem_slot + 1;   // ring positions whose loads have been issued
     volatile uint32_t *turn = issued + 1;        // steps that the issuer of each pipeline has done
-    static_assert(24 * NST + 152 + 16 * ITEMS + sizeof(Item) * ITEMS + sizeof(Pending) * 2 + 16 <= 768, "barrier area");
+    static_assert(24 * NST + 136 + 16 * ITEMS + sizeof(Item) * ITEMS + sizeof(Pending) * 2 + 16 <= 768, "barrier area");
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     if ((sm_q & 1023u) != 0u) {  // the swizzled tiles need what the declaration asks for
@@ -386,8 +394,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
         mbar_init(q_empty, 2);               // both issuing warps
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full + 8 * i, 1);
-            mbar_init(p_part + 8 * i, 4);    // heads of 128: the first PART steps of P written, O rescaled
-            mbar_init(p_full + 8 * i, 4);
+            mbar_init(p_full + 8 * i, 4);    // P written, O rescaled
             mbar_init(o_full + 8 * i, 1);
             mbar_init(o_empty + 8 * i, 8);   // all softmax warps
             mbar_init(join_go + 8 * i, 1);
@@ -459,6 +466,12 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
             __syncwarp();
             float m = -INFINITY, l = 0.f;
             for (int j = two ? 0 : i; j < todo; j += two ? 1 : 2) {
+                // Some row does not see all of the tile: drafts, or keys left of a window. The walks run
+                // while S is computed.
+                const int key0 = it.tile(j) * KEYS;
+                const bool edge = key0 + KEYS > it.text || (p.window > 0 && key0 <= it.len - p.window && key0 + KEYS > p.sinks);
+                uint32_t bits[4];
+                if (edge) keys_seen(p, it.row0 - it.first, it.text, draft, pos, key0, bits);
                 if (!wait(s_full + 8 * i, n_s & 1)) break;
                 ++n_s;
                 tc_fence_after();
@@ -466,11 +479,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, reinterpret_cast<uint32_t *>(s) + c * 32);
                 tmem_wait_ld();
-                // Some row does not see all of the tile: drafts, or keys left of a window.
-                const int key0 = it.tile(j) * KEYS;
-                if (key0 + KEYS > it.text || (p.window > 0 && key0 <= it.len - p.window && key0 + KEYS > p.sinks)) {
-                    uint32_t bits[4];
-                    keys_seen(p, it.row0 - it.first, it.text, draft, pos, key0, bits);
+                if (edge) {
 #pragma unroll
                     for (int c = 0; c < 128; ++c)
                         if (((bits[c >> 5] >> (c & 31)) & 1u) == 0u) s[c] = -INFINITY;
@@ -515,12 +524,10 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
                         pk[c / 2] = pack_bf16x2(__float_as_uint(e0), __float_as_uint(e1));
                     }
                     tmem_st16(ts + c0 / 2, pk);
-                    if ((EARLY && c0 + 32 == PART * 16) || c0 == 96) {
-                        tmem_wait_st();
-                        tc_fence_before();
-                        arrive((c0 == 96 ? p_full : p_part) + 8 * i);
-                    }
                 }
+                tmem_wait_st();
+                tc_fence_before();
+                arrive(p_full + 8 * i);
                 const uint64_t all = add2(sum[0], sum[1]);
                 l = l * f + (low(all) + high(all));
             }
@@ -537,9 +544,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
             tc_fence_after();
             const bool whole = it.whole != 0;
             const int64_t out_token = static_cast<int64_t>(it.row0) + token;
-            const int kvh = it.unit / p.blocks;
-            const int in_group = (it.unit - kvh * p.blocks) * p.unit_heads + row_head;
-            const int head = kvh * p.group + in_group;
+            const int in_group = it.h0 + row_head, head = it.kvh * p.group + in_group;
             const bool mine = real && in_group < p.group;
             // One q tile: the two pipelines' O of a row, joined; half of the columns each.
             float f0 = 1.f, f1 = 1.f, M = m, L = l;
@@ -558,7 +563,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
             const float inv = 1.f / L;
             // a pipeline without a key tile has nothing there
             const bool has0 = two ? i == 0 : todo > 0, has1 = two ? i == 1 : todo > 1;
-#pragma unroll 1
+#pragma unroll 2
             for (int c = c0; c < c1; c += 16) {
                 float v[16], u[16];
                 if (has0) tmem_ld16(tmem + TM_O + lanes + c, reinterpret_cast<uint32_t *>(v));
@@ -675,7 +680,6 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
                     const Pending it = pend[which];
                     const int first = which == 0 ? first0 : first1, n = which == 0 ? n0 : n1;
                     if (it.parts == 0) continue;
-                    const int kvh = it.unit / p.blocks, h0 = (it.unit - kvh * p.blocks) * p.unit_heads;
                     float *mem = reinterpret_cast<float *>(base + (at_once && which == 1 ? size0 : 0));
                     const int step = n * PartRow<D>::FLOATS;    // from part to part
                     // A row's weights of its parts, in place of their maxima: by a lane for each part,
@@ -698,9 +702,9 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
                         const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll 4
                         for (int q = q0; q < it.parts; q += by) at[q * step] = ex2((at[q * step] - ref) * sl) * inv;
-                        const int tok = (first + r) / p.unit_heads, in_group = h0 + first + r - tok * p.unit_heads;
+                        const int tok = (first + r) / p.unit_heads, in_group = it.h0 + first + r - tok * p.unit_heads;
                         if (q0 == 0 && in_group < p.group)
-                            store_lse(p, static_cast<int64_t>(it.row0) + tok, kvh * p.group + in_group, M, L);
+                            store_lse(p, static_cast<int64_t>(it.row0) + tok, it.kvh * p.group + in_group, M, L);
                     }
                     __syncwarp();
                     arrive(joined);
@@ -720,10 +724,10 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
                             acc.z += v.z * f;
                             acc.w += v.w * f;
                         }
-                        const int tok = (first + r) / p.unit_heads, in_group = h0 + first + r - tok * p.unit_heads;
+                        const int tok = (first + r) / p.unit_heads, in_group = it.h0 + first + r - tok * p.unit_heads;
                         if (in_group >= p.group) continue;
                         __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + (static_cast<int64_t>(it.row0) + tok) * p.o_row +
-                                             (kvh * p.group + in_group) * p.o_head + col;
+                                             (it.kvh * p.group + in_group) * p.o_head + col;
                         *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(__float_as_uint(acc.x), __float_as_uint(acc.y)),
                                                                      pack_bf16x2(__float_as_uint(acc.z), __float_as_uint(acc.w)));
                     }
@@ -744,14 +748,14 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
             for (uint32_t k = 0; there(k); ++k) {
                 const Item &it = items[k % ITEMS];
                 const bool two = it.ntok > p.tokens;
-                const int unit = it.unit, kvh = unit / p.blocks, len = it.len, todo = it.todo;
+                const int kvh = it.kvh, len = it.len, todo = it.todo;
                 if (k > 0 && !wait(q_empty, (k - 1) & 1)) break;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(q_full, (two ? 2 : 1) * HALVES * p.tokens * p.unit_heads * 128);
                     for (int t = 0; t < (two ? 2 : 1); ++t)
                         for (int hf = 0; hf < HALVES; ++hf)
                             tma_load_3d(sm_q + t * Sh::TILE_BYTES + hf * Sh::HALF_BYTES, &p.tmQ, q_full, hf * 64,
-                                        kvh * p.group + (unit - kvh * p.blocks) * p.unit_heads,
+                                        kvh * p.group + it.h0,
                                         it.row0 + t * p.tokens);
                 }
                 __syncwarp();
@@ -840,53 +844,31 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
                 const int stride = two ? 1 : 2, j0 = two ? 0 : i;
                 const uint64_t q_desc = smem_desc_sw128(sm_q + (two ? i * Sh::TILE_BYTES : 0));
                 auto ext_of = [&](int j) { return extent(len, t0 + j < far ? t0 + j : t0 + j + gap); };
-                auto scores = [&](int j) {             // S of key tile j, which has landed
-                    const uint32_t st = (c + 2 * j) % NST;
-                    const uint32_t s_idesc = attn_idesc(ext_of(j), false), freed = kv_empty + 8 * st;
-                    const uint64_t kk = k_desc + st * (Sh::TILE_BYTES / 16);
-                    const bool last = j + stride >= todo;
-                    tc_fence_after();
-                    if (elect_one()) {
-#pragma unroll
-                        for (int s = 0; s < D / 16; ++s) {
-                            const int o = (s / 4) * (Sh::HALF_BYTES / 16) + (s % 4) * 2;
-                            umma_ss(ts, q_desc + o, kk + o, s_idesc, s > 0);
-                        }
-                        umma_commit(s_full + 8 * i);
-                        umma_commit(freed);
-                        if (!two) umma_commit(freed);
-                        if (last) umma_commit(q_empty);
-                    }
-                    __syncwarp();
-                };
                 if (!wait(q_full, k & 1)) break;
+                // O of the last item has been read before this one's first product.
                 if (j0 >= todo) {
                     arrive(q_empty);
                     if (k > 0 && !wait(o_empty + 8 * i, (k - 1) & 1)) break;
-                } else {
-                    if (!wait_kv(c + 2 * j0)) break;
-                    scores(j0);
                 }
                 const int steps = two ? todo : (todo + 1) / 2;  // of either pipeline
-                for (int n = 0; n < steps; ++n) {
+#pragma unroll 1
+                for (int n = -1; n < steps; ++n) {
                     const int j = j0 + n * stride, next = j + stride;
-                    ++step;
-                    if (j >= todo) {                   // the other's last tile
-                        pass(step);
-                        break;
-                    }
-                    const uint32_t at = c + 2 * j + 1, st = at % NST, freed = kv_empty + 8 * st;
-                    const uint64_t v = v_desc + st * (Sh::TILE_BYTES / 16);
-                    const int ext = ext_of(j);
-                    // O of the last item has been read
-                    if (k > 0 && n == 0 && !wait(o_empty + 8 * i, (k - 1) & 1)) break;
-                    auto product = [&](int from) {     // O += P V, from step `from` on
+                    bool passed = n < 0;               // the other pipeline may have its turn
+                    if (n >= 0) ++step;
+                    if (n >= 0 && j < todo) {
+                        const uint32_t at = c + 2 * j + 1, st = at % NST, freed = kv_empty + 8 * st;
+                        const uint64_t v = v_desc + st * (Sh::TILE_BYTES / 16);
+                        const int ext = ext_of(j);
+                        if (k > 0 && n == 0 && !wait(o_empty + 8 * i, (k - 1) & 1)) break;
+                        if (!wait_kv(at) || !poll(turn + (1 - i), step - 1 + i)) break;
+                        if (!wait(p_full + 8 * i, n_p & 1)) break;
+                        ++n_p;
                         tc_fence_after();
                         if (elect_one()) {
                             if (ext == KEYS) {
 #pragma unroll
-                                for (int s = 0; s < KEYS / 16; ++s)
-                                    if (s >= from) umma_ts(to, ts + s * 8, v + s * 128, o_idesc, n > 0 || s > 0);
+                                for (int s = 0; s < KEYS / 16; ++s) umma_ts(to, ts + s * 8, v + s * 128, o_idesc, n > 0 || s > 0);
                             } else {  // the sequence's last keys
                                 for (int s = 0; s < ext / 16; ++s) umma_ts(to, ts + s * 8, v + s * 128, o_idesc, n > 0 || s > 0);
                             }
@@ -895,27 +877,31 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
                             if (next >= todo) umma_commit(o_full + 8 * i);
                         }
                         __syncwarp();
-                    };
-                    if (!wait_kv(at) || !poll(turn + (1 - i), step - 1 + i)) break;
-                    if (EARLY) {
-                        if (!wait(p_part + 8 * i, n_p & 1)) break;
+                    }
+                    if (next >= todo || !landed(c + 2 * next)) {
+                        if (!passed) pass(step);
+                        passed = true;
+                        if (next >= todo) continue;
+                        if (!wait_kv(c + 2 * next)) break;
+                    }
+                    {   // S of key tile `next`, which has landed
+                        const uint32_t st = (c + 2 * next) % NST, s_idesc = attn_idesc(ext_of(next), false), freed = kv_empty + 8 * st;
+                        const uint64_t kk = k_desc + st * (Sh::TILE_BYTES / 16);
                         tc_fence_after();
-                        if (ext == KEYS && elect_one()) {
+                        if (elect_one()) {
 #pragma unroll
-                            for (int s = 0; s < PART; ++s) umma_ts(to, ts + s * 8, v + s * 128, o_idesc, n > 0 || s > 0);
+                            for (int s = 0; s < D / 16; ++s) {
+                                const int o = (s / 4) * (Sh::HALF_BYTES / 16) + (s % 4) * 2;
+                                umma_ss(ts, q_desc + o, kk + o, s_idesc, s > 0);
+                            }
+                            umma_commit(s_full + 8 * i);
+                            umma_commit(freed);
+                            if (!two) umma_commit(freed);
+                            if (next + stride >= todo) umma_commit(q_empty);
                         }
                         __syncwarp();
                     }
-                    if (!wait(p_full + 8 * i, n_p & 1)) break;
-                    product(EARLY ? PART : 0);
-                    const bool now = next < todo && landed(c + 2 * next);
-                    if (now) scores(next);
-                    pass(step);
-                    if (next < todo && !now) {
-                        if (!wait_kv(c + 2 * next)) break;
-                        scores(next);
-                    }
-                    ++n_p;
+                    if (!passed) pass(step);
                 }
                 if (!alive) break;
                 c += 2 * todo;
@@ -940,14 +926,14 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
                     Item it;
                     it.seq = -1;
                     if (w.more()) {
-                        const int first = w.first_token();
-                        it = Item{w.s, w.q.start + first, w.tokens(), first, w.unit(), w.q.len, w.q.text, w.q.lo, w.q.near, w.q.far,
+                        const int first = w.first_token(), unit = w.unit(), kvh = p.blocks == 1 ? unit : unit / p.blocks;
+                        it = Item{w.s, w.q.start + first, w.tokens(), first, kvh, (unit - kvh * p.blocks) * p.unit_heads, w.q.len, w.q.text, w.q.lo, w.q.near, w.q.far,
                                   w.t0, w.todo(), w.whole() ? 1 : 0};
                         if (!it.whole) {
                             const int64_t item0 = w.x - w.off;
                             const int a = w.split.owner(item0);
                             pend[w.t0 == 0 ? 1 : 0] =
-                                Pending{it.row0, it.ntok, it.unit, a, w.split.owner(item0 + w.q.span() - w.q.per) - a + 1};
+                                Pending{it.row0, it.ntok, it.kvh, it.h0, a, w.split.owner(item0 + w.q.span() - w.q.per) - a + 1};
                         }
                     }
                     items[k % ITEMS] = it;
