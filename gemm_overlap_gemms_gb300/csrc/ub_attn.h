@@ -200,7 +200,7 @@ struct PageCopyParams {
     int32_t *status;
     int pdl;
 };
-cudaError_t launch_kv_copy(const PageCopyParams &p, int sms, cudaStream_t s);
+cudaError_t launch_kv_copy(const PageCopyParams &p, cudaStream_t s);
 
 struct AcceptParams {
     SeqBatch b;

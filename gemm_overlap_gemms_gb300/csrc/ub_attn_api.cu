@@ -520,7 +520,7 @@ int ub_kv_copy(ub_handle_t h, const ub_attn_t *in, const int32_t *pairs, int64_t
     p.pdl = c.pdl;
     bool timed = false;
     if (int rc = handle_prof_start(h, UB_OP_KV_COPY, s, &timed)) return rc;
-    const cudaError_t e = launch_kv_copy(p, c.sms, s);
+    const cudaError_t e = launch_kv_copy(p, s);
     if (e != cudaSuccess) return cuda_failed(e, "page copy kernel launch");
     return handle_prof_stop(h, UB_OP_KV_COPY, s, timed);
 }
