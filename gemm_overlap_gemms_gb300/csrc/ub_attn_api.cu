@@ -532,7 +532,8 @@ int ub_kv_accept(ub_handle_t h, const ub_attn_t *in, const int32_t *parents, int
     ub_attn_t a;
     if (int rc = check_cache_call(fn, h, in, &a)) return rc;
     if (a.n_seqs <= 0) return fail_call(UB_ERR_ZERO, "%s: %d sequences", fn, a.n_seqs);
-    if (!a.seq_starts || !parents || !leaves || !new_lens) return fail_call(UB_ERR_ARG, "%s: a null array", fn);
+    if (!a.seq_starts || (!parents && n_tokens > 0) || !leaves || !new_lens)
+        return fail_call(UB_ERR_ARG, "%s: a null array", fn);
     if (n_tokens < 0 || n_tokens > INT32_MAX) return fail_call(UB_ERR_ARG, "%s: %lld tokens", fn, (long long)n_tokens);
     if (int rc = check_cache_sizes(fn, &a)) return rc;
     if (int rc = check_table(fn, a)) return rc;

@@ -828,7 +828,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
             };
             auto landed = [&](uint32_t at) {
                 return __all_sync(0xffffffffu, static_cast<int32_t>(*issued - at) > 0 &&
-                                                   mbar_try_wait(kv_full + 8 * (at % NST), (at / NST) & 1)) != 0;
+                                                   mbar_test(kv_full + 8 * (at % NST), (at / NST) & 1)) != 0;
             };
             auto pass = [&](uint32_t step) {
                 if (lane == 0) turn[i] = step;
