@@ -356,6 +356,55 @@ struct PartRow {
     static constexpr int BYTES = 4 * FLOATS;
 };
 
+// The join of a CTA's rows [first, first + n) of an item: its parts' rows one after the other at
+// `mem`, with their weights in the place of the maxima. A lane has columns [col, col + 4) of rows r0,
+// r0 + 8 * 128 / D and so on.
+template <int D>
+struct JoinRows {
+    const TreeParams &p;
+    const Pending &it;
+    const float *mem;
+    int first, n, r0, col;
+    template <int ROWS_AT_ONCE>
+    __device__ __forceinline__ void run() const
+    {
+        constexpr int STEP = 8 * (128 / D);
+        const int step = n * PartRow<D>::FLOATS;  // from part to part
+#pragma unroll 1
+        for (int r1 = r0; r1 < n; r1 += STEP * ROWS_AT_ONCE) {
+            float4 acc[ROWS_AT_ONCE];
+            const float *at[ROWS_AT_ONCE];
+#pragma unroll
+            for (int e = 0; e < ROWS_AT_ONCE; ++e) {
+                acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                at[e] = mem + (r1 + e * STEP < n ? r1 + e * STEP : r1) * PartRow<D>::FLOATS;
+            }
+#pragma unroll(8 / ROWS_AT_ONCE)
+            for (int q = 0; q < it.parts; ++q) {
+#pragma unroll
+                for (int e = 0; e < ROWS_AT_ONCE; ++e) {
+                    const float4 v = *reinterpret_cast<const float4 *>(at[e] + q * step + col);
+                    const float f = at[e][q * step + D];
+                    acc[e].x += v.x * f;
+                    acc[e].y += v.y * f;
+                    acc[e].z += v.z * f;
+                    acc[e].w += v.w * f;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < ROWS_AT_ONCE; ++e) {
+                const int r = r1 + e * STEP, tok = (first + r) / p.unit_heads;
+                const int in_group = it.h0 + first + r - tok * p.unit_heads;
+                if (r >= n || in_group >= p.group) continue;
+                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + (static_cast<int64_t>(it.row0) + tok) * p.o_row +
+                                     (it.kvh * p.group + in_group) * p.o_head + col;
+                *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(__float_as_uint(acc[e].x), __float_as_uint(acc[e].y)),
+                                                             pack_bf16x2(__float_as_uint(acc[e].z), __float_as_uint(acc[e].w)));
+            }
+        }
+    }
+};
+
 template <int D>
 __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __grid_constant__ TreeParams p)
 {
@@ -709,28 +758,13 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
                     __syncwarp();
                     arrive(joined);
                     if (!wait(joined, n_joined++ & 1)) break;
-                    // Then four columns of a row by a lane.
-                    const int side = lane / (D / 4), col = (lane & (D / 4 - 1)) * 4;
-#pragma unroll 4
-                    for (int r = warp * (128 / D) + side; r < n; r += 8 * (128 / D)) {
-                        const float *at = mem + r * PartRow<D>::FLOATS;
-                        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                        for (int q = 0; q < it.parts; ++q) {
-                            const float4 v = *reinterpret_cast<const float4 *>(at + q * step + col);
-                            const float f = at[q * step + D];
-                            acc.x += v.x * f;
-                            acc.y += v.y * f;
-                            acc.z += v.z * f;
-                            acc.w += v.w * f;
-                        }
-                        const int tok = (first + r) / p.unit_heads, in_group = it.h0 + first + r - tok * p.unit_heads;
-                        if (in_group >= p.group) continue;
-                        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + (static_cast<int64_t>(it.row0) + tok) * p.o_row +
-                                             (it.kvh * p.group + in_group) * p.o_head + col;
-                        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(__float_as_uint(acc.x), __float_as_uint(acc.y)),
-                                                                     pack_bf16x2(__float_as_uint(acc.z), __float_as_uint(acc.w)));
-                    }
+                    // Then four columns of a row by a lane, several rows at once where there are many.
+                    constexpr int SIDE = 128 / D;
+                    const JoinRows<D> rows{p, it, mem, first, n, warp * SIDE + lane / (D / 4), (lane & (D / 4 - 1)) * 4};
+                    if (n > 8 * SIDE)
+                        rows.template run<4>();
+                    else
+                        rows.template run<1>();
                     __syncwarp();
                 }
                 if (at_once) break;
