@@ -25,10 +25,9 @@
 //
 // Roles (12 warps, one CTA per SM):
 //   warps 0-3, 4-7   softmax of pipeline 0 and 1, one thread per row; the item's end; joins
-//   warp 8           loads (TMA): Q, then K and V tiles in a ring
+//   warp 8           loads (TMA) of Q and K tiles; of V tiles of heads of 64
 //   warps 9, 10      MMA issue for pipeline 0 and 1
-//   warp 11          schedule: this CTA's items; and zeroes the rows of V past a sequence's end in
-//                    its last tile (their weights are zero, their values may be anything)
+//   warp 11          schedule: this CTA's items; loads of V tiles of heads of 128
 #include <cuda_bf16.h>
 
 #include "ub_attn.h"
@@ -60,7 +59,12 @@ template <int D>
 struct TreeShape {
     static constexpr int TILE_BYTES = KEYS * D * 2;
     static constexpr int HALF_BYTES = KEYS * 128;         // 64 columns of a tile
-    static constexpr int STAGES = D == 128 ? 5 : 10;
+    static constexpr int K_STAGES = D == 128 ? 3 : 5, V_STAGES = D == 128 ? 2 : 5, STAGES = K_STAGES + V_STAGES;
+    // A box takes the warp that loads it 80 cycles, and a tile of heads of 128 in pages of 16 rows
+    // has 16 of them: as long as HBM takes for half of it. K and V have a warp each there (4 sequences
+    // of few drafts: 13.2 to 11.6 us); with heads of 64 the second warp's waits take more issue slots
+    // from the softmax than its loads save (64 sequences, 32 heads of 64: 172 us for 150).
+    static constexpr bool TWO_LOADERS = D == 128;
     static constexpr int CONTROL = 2048 + 768;            // (m, l) of two tiles; barriers
     static constexpr int SMEM = (2 + STAGES) * TILE_BYTES + CONTROL;
     // The rows that a CTA joins: those of an item and one more of each part at most.
@@ -77,7 +81,6 @@ struct Seq {
     int tiles;      // key tiles in sight, at least one
     int blocks;     // items of a key/value head
     int per;        // units of a key tile
-    __device__ __forceinline__ int tile(int t) const { return t < far ? t : t - far + near; }
     // Units of an item (2^24 tiles at most).
     __device__ __forceinline__ int span() const { return tiles * per; }
     __device__ __forceinline__ int cost() const { return span() + ITEM_COST; }
@@ -409,24 +412,23 @@ template <int D>
 __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __grid_constant__ TreeParams p)
 {
     using Sh = TreeShape<D>;
-    constexpr int NST = Sh::STAGES, HALVES = D / 64;
+    constexpr int NST = Sh::STAGES, KST = Sh::K_STAGES, VST = Sh::V_STAGES, HALVES = D / 64;
     extern __shared__ __align__(1024) uint8_t base[];
     const uint32_t sm_q = smem_u32(base), sm_kv = sm_q + 2 * Sh::TILE_BYTES;
     float *sm_max = reinterpret_cast<float *>(base + (2 + NST) * Sh::TILE_BYTES);  // [2][128]
     float *sm_sum = sm_max + 256;                                                  // [2][128]
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm_sum + 256);
-    const uint32_t kv_full = smem_u32(bars), v_raw = kv_full + 8 * NST, kv_empty = kv_full + 16 * NST,
-                   misc = kv_full + 24 * NST;
+    const uint32_t kv_full = smem_u32(bars), kv_empty = kv_full + 8 * NST, misc = kv_full + 16 * NST;
     const uint32_t q_full = misc, q_empty = misc + 8, s_full = misc + 16, p_full = misc + 32, o_full = misc + 48,
                    o_empty = misc + 64, both = misc + 80, parts_done = misc + 88, join_go = misc + 96, drain = misc + 112,
                    joined = misc + 128;
     const uint32_t it_full = misc + 136, it_empty = it_full + 8 * ITEMS;
-    Item *items = reinterpret_cast<Item *>(reinterpret_cast<uint8_t *>(bars) + 24 * NST + 136 + 16 * ITEMS);
+    Item *items = reinterpret_cast<Item *>(reinterpret_cast<uint8_t *>(bars) + 16 * NST + 136 + 16 * ITEMS);
     Pending *pend = reinterpret_cast<Pending *>(items + ITEMS);  // begun before this CTA; going on after it
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(pend + 2);
-    volatile uint32_t *issued = tmem_slot + 1;   // ring positions whose loads have been issued
-    volatile uint32_t *turn = issued + 1;        // steps that the issuer of each pipeline has done
-    static_assert(24 * NST + 136 + 16 * ITEMS + sizeof(Item) * ITEMS + sizeof(Pending) * 2 + 16 <= 768, "barrier area");
+    volatile uint32_t *issued = tmem_slot + 1;   // key tiles whose loads have been issued, of K and of V
+    volatile uint32_t *turn = issued + 2;        // steps that the issuer of each pipeline has done
+    static_assert(16 * NST + 136 + 16 * ITEMS + sizeof(Item) * ITEMS + sizeof(Pending) * 2 + 20 <= 768, "barrier area");
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     if ((sm_q & 1023u) != 0u) {  // the swizzled tiles need what the declaration asks for
@@ -436,7 +438,6 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
     if (threadIdx.x == 0) {
         for (int i = 0; i < NST; ++i) {
             mbar_init(kv_full + 8 * i, 1);
-            mbar_init(v_raw + 8 * i, 1);
             mbar_init(kv_empty + 8 * i, 2);  // both pipelines, or one of them twice
         }
         mbar_init(q_full, 1);
@@ -454,7 +455,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
             mbar_init(it_empty + 8 * i, 11);  // every warp but the schedule's
         }
         pend[0].parts = pend[1].parts = 0;
-        *issued = turn[0] = turn[1] = 0u;
+        issued[0] = issued[1] = turn[0] = turn[1] = 0u;
         mbar_init(both, 8);
         mbar_init(parts_done, 8);
         mbar_init(joined, 8);
@@ -775,61 +776,62 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
     } else {
         // the four single warps
         fewer_registers<SINGLE_REGS>();
+        // The key tiles of an item, of K (kind 0), V (1) or both, into their rings: `c` are before them.
+        auto load_tiles = [&](const Item &it, int from, int to, uint32_t &c) {
+            const int box = KEYS < (1 << p.b.page_shift) ? KEYS : (1 << p.b.page_shift), boxes = KEYS / box;
+            const int len = it.len, todo = it.todo;
+            const int32_t *table = p.b.page_table + it.seq * p.b.table_row;
+            const int pages = (len + (1 << p.b.page_shift) - 1) >> p.b.page_shift;
+            int cached0 = 0, cached_n = 0, ids = -1;   // page ids, one per lane
+            for (int j = 0; j < todo; ++j, ++c) {
+                const int kt = it.tile(j), key0 = kt * KEYS, ext = extent(len, kt);
+                const int n_box = (ext + box - 1) / box, page0 = key0 >> p.b.page_shift;
+                if (page0 + boxes > cached0 + cached_n) {
+                    cached0 = page0;
+                    cached_n = 32;
+                    // a page that no row sees may be another sequence's by now, or nobody's
+                    const int64_t first = static_cast<int64_t>(cached0 + lane) << p.b.page_shift;
+                    const bool seen = cached0 + lane < pages &&
+                                      (p.window == 0 || first + (int64_t(1) << p.b.page_shift) > it.lo || first < p.sinks);
+                    ids = seen ? table[cached0 + lane] : -1;
+                    if (seen && (ids < 0 || ids >= p.b.num_pages)) {
+                        atomicCAS(p.b.status, 0, UB_ERR_ARG);
+                        ids = -1;                      // outside the tensor: filled with zeros
+                    }
+                }
+                for (int kind = from; kind < to; ++kind) {
+                    const uint32_t stages = kind == 0 ? KST : VST, lap = c / stages;
+                    const uint32_t st = c - lap * stages + (kind == 0 ? 0 : KST), bar = kv_full + 8 * st;
+                    if (lap > 0 && !wait(kv_empty + 8 * st, (lap - 1) & 1)) return;
+                    if (lane == 0) mbar_arrive_expect_tx(bar, n_box * HALVES * box * 128);
+                    __syncwarp();
+                    const int bx = lane / HALVES, hf = lane - bx * HALVES;
+                    const int page = __shfl_sync(0xffffffffu, ids, (page0 - cached0 + bx) & 31);
+                    if (bx < n_box)
+                        tma_load_4d(sm_kv + st * Sh::TILE_BYTES + hf * Sh::HALF_BYTES + bx * box * 128,
+                                    kind == 0 ? &p.tmK : &p.tmV, bar, hf * 64,
+                                    boxes > 1 ? 0 : key0 & ((1 << p.b.page_shift) - 1), it.kvh, page);
+                    __syncwarp();
+                    if (lane == 0) issued[kind] = c + 1;
+                }
+            }
+        };
         if (warp == 8) {
             // -------------------------------------------------------- loads
-            uint32_t c = 0;                            // ring position
-            const int box = KEYS < (1 << p.b.page_shift) ? KEYS : (1 << p.b.page_shift), boxes = KEYS / box;
+            uint32_t c = 0;
             for (uint32_t k = 0; there(k); ++k) {
                 const Item &it = items[k % ITEMS];
                 const bool two = it.ntok > p.tokens;
-                const int kvh = it.kvh, len = it.len, todo = it.todo;
                 if (k > 0 && !wait(q_empty, (k - 1) & 1)) break;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(q_full, (two ? 2 : 1) * HALVES * p.tokens * p.unit_heads * 128);
                     for (int t = 0; t < (two ? 2 : 1); ++t)
                         for (int hf = 0; hf < HALVES; ++hf)
                             tma_load_3d(sm_q + t * Sh::TILE_BYTES + hf * Sh::HALF_BYTES, &p.tmQ, q_full, hf * 64,
-                                        kvh * p.group + it.h0,
-                                        it.row0 + t * p.tokens);
+                                        it.kvh * p.group + it.h0, it.row0 + t * p.tokens);
                 }
                 __syncwarp();
-                const int32_t *table = p.b.page_table + it.seq * p.b.table_row;
-                const int pages = (len + (1 << p.b.page_shift) - 1) >> p.b.page_shift;
-                int cached0 = 0, cached_n = 0, ids = -1;  // page ids, one per lane
-                for (int j = 0; j < todo && alive; ++j) {
-                    const int kt = it.tile(j), key0 = kt * KEYS, ext = extent(len, kt);
-                    const int n_box = (ext + box - 1) / box, page0 = key0 >> p.b.page_shift;
-                    if (page0 + boxes > cached0 + cached_n) {
-                        cached0 = page0;
-                        cached_n = 32;
-                        // a page that no row sees may be another sequence's by now, or nobody's
-                        const int64_t first = static_cast<int64_t>(cached0 + lane) << p.b.page_shift;
-                        const bool seen = cached0 + lane < pages &&
-                                          (p.window == 0 || first + (int64_t(1) << p.b.page_shift) > it.lo || first < p.sinks);
-                        ids = seen ? table[cached0 + lane] : -1;
-                        if (seen && (ids < 0 || ids >= p.b.num_pages)) {
-                            atomicCAS(p.b.status, 0, UB_ERR_ARG);
-                            ids = -1;                  // outside the tensor: filled with zeros
-                        }
-                    }
-                    for (int kind = 0; kind < 2 && alive; ++kind, ++c) {
-                        const uint32_t st = c % NST;
-                        if (c >= NST && !wait(kv_empty + 8 * st, (c / NST - 1) & 1)) break;
-                        // The last tile of V goes through the zeroing warp when it ends inside 16 keys.
-                        const bool fix = kind == 1 && ext > len - key0;
-                        const uint32_t bar = (fix ? v_raw : kv_full) + 8 * st;
-                        if (lane == 0) mbar_arrive_expect_tx(bar, n_box * HALVES * box * 128);
-                        __syncwarp();
-                        const int bx = lane / HALVES, hf = lane - bx * HALVES;
-                        const int page = __shfl_sync(0xffffffffu, ids, (page0 - cached0 + bx) & 31);
-                        if (bx < n_box)
-                            tma_load_4d(sm_kv + st * Sh::TILE_BYTES + hf * Sh::HALF_BYTES + bx * box * 128,
-                                        kind == 0 ? &p.tmK : &p.tmV, bar, hf * 64,
-                                        boxes > 1 ? 0 : key0 & ((1 << p.b.page_shift) - 1), kvh, page);
-                        __syncwarp();
-                        if (lane == 0) *issued = c + 1;
-                    }
-                }
+                load_tiles(it, 0, Sh::TWO_LOADERS ? 1 : 2, c);
                 if (!alive) break;
                 arrive(it_empty + 8 * (k % ITEMS));
             }
@@ -857,12 +859,13 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
                 }
                 return true;
             };
-            auto wait_kv = [&](uint32_t at) {
-                return poll(issued, at + 1) && wait(kv_full + 8 * (at % NST), (at / NST) & 1);
+            auto wait_k = [&](uint32_t at) { return poll(issued, at + 1) && wait(kv_full + 8 * (at % KST), (at / KST) & 1); };
+            auto wait_v = [&](uint32_t at) {
+                return poll(issued + 1, at + 1) && wait(kv_full + 8 * (KST + at % VST), (at / VST) & 1);
             };
-            auto landed = [&](uint32_t at) {
+            auto landed = [&](uint32_t at) {           // K
                 return __all_sync(0xffffffffu, static_cast<int32_t>(*issued - at) > 0 &&
-                                                   mbar_test(kv_full + 8 * (at % NST), (at / NST) & 1)) != 0;
+                                                   mbar_test(kv_full + 8 * (at % KST), (at / KST) & 1)) != 0;
             };
             auto pass = [&](uint32_t step) {
                 if (lane == 0) turn[i] = step;
@@ -877,7 +880,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
                 const int todo = same(it.todo), len = same(it.len), t0 = same(it.t0), far = same(it.far), gap = same(it.near) - far;
                 const int stride = two ? 1 : 2, j0 = two ? 0 : i;
                 const uint64_t q_desc = smem_desc_sw128(sm_q + (two ? i * Sh::TILE_BYTES : 0));
-                auto ext_of = [&](int j) { return extent(len, t0 + j < far ? t0 + j : t0 + j + gap); };
+                auto tile_of = [&](int j) { return t0 + j < far ? t0 + j : t0 + j + gap; };
                 if (!wait(q_full, k & 1)) break;
                 // O of the last item has been read before this one's first product.
                 if (j0 >= todo) {
@@ -891,11 +894,23 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
                     bool passed = n < 0;               // the other pipeline may have its turn
                     if (n >= 0) ++step;
                     if (n >= 0 && j < todo) {
-                        const uint32_t at = c + 2 * j + 1, st = at % NST, freed = kv_empty + 8 * st;
+                        const uint32_t st = KST + (c + j) % VST, freed = kv_empty + 8 * st;
                         const uint64_t v = v_desc + st * (Sh::TILE_BYTES / 16);
-                        const int ext = ext_of(j);
+                        const int kt = tile_of(j), ext = extent(len, kt), valid = len - kt * KEYS;
                         if (k > 0 && n == 0 && !wait(o_empty + 8 * i, (k - 1) & 1)) break;
-                        if (!wait_kv(at) || !poll(turn + (1 - i), step - 1 + i)) break;
+                        if (!wait_v(c + j)) break;
+                        if (ext > valid) {
+                            // What is past the sequence's end has the weight zero, and may hold anything:
+                            // zeros take its place (two q tiles: by both issuers, whoever comes first).
+                            const uint32_t mem = sm_kv + st * Sh::TILE_BYTES;
+                            for (int u = lane; u < (ext - valid) * (D / 8); u += 32) {
+                                const int r = valid + u / (D / 8), ch = u % (D / 8);
+                                st_shared_v4(mem + (ch / 8) * Sh::HALF_BYTES + r * 128 + (ch % 8) * 16, 0u, 0u, 0u, 0u);
+                            }
+                            fence_proxy_async_shared();
+                            __syncwarp();
+                        }
+                        if (!poll(turn + (1 - i), step - 1 + i)) break;
                         if (!wait(p_full + 8 * i, n_p & 1)) break;
                         ++n_p;
                         tc_fence_after();
@@ -912,14 +927,15 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
                         }
                         __syncwarp();
                     }
-                    if (next >= todo || !landed(c + 2 * next)) {
+                    if (next >= todo || !landed(c + next)) {
                         if (!passed) pass(step);
                         passed = true;
                         if (next >= todo) continue;
-                        if (!wait_kv(c + 2 * next)) break;
+                        if (!wait_k(c + next)) break;
                     }
                     {   // S of key tile `next`, which has landed
-                        const uint32_t st = (c + 2 * next) % NST, s_idesc = attn_idesc(ext_of(next), false), freed = kv_empty + 8 * st;
+                        const uint32_t st = (c + next) % KST, freed = kv_empty + 8 * st;
+                        const uint32_t s_idesc = attn_idesc(extent(len, tile_of(next)), false);
                         const uint64_t kk = k_desc + st * (Sh::TILE_BYTES / 16);
                         tc_fence_after();
                         if (elect_one()) {
@@ -938,7 +954,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
                     if (!passed) pass(step);
                 }
                 if (!alive) break;
-                c += 2 * todo;
+                c += todo;
                 arrive(it_empty + 8 * (k % ITEMS));
             }
             // everything issued has completed before TMEM goes back
@@ -948,7 +964,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
             }
             __syncwarp();
         } else {
-            // -------------------------------------------------------- schedule, the last keys of V
+            // -------------------------------------------------------- schedule
             Walk w(p);
             if (p.many_units)
                 begin<int64_t>(w, lane, blockIdx.x, gridDim.x);
@@ -961,7 +977,8 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
                     it.seq = -1;
                     if (w.more()) {
                         const int first = w.first_token(), unit = w.unit(), kvh = p.blocks == 1 ? unit : unit / p.blocks;
-                        it = Item{w.s, w.q.start + first, w.tokens(), first, kvh, (unit - kvh * p.blocks) * p.unit_heads, w.q.len, w.q.text, w.q.lo, w.q.near, w.q.far,
+                        it = Item{w.s, w.q.start + first, w.tokens(), first, kvh,
+                                  (unit - kvh * p.blocks) * p.unit_heads, w.q.len, w.q.text, w.q.lo, w.q.near, w.q.far,
                                   w.t0, w.todo(), w.whole() ? 1 : 0};
                         if (!it.whole) {
                             const int64_t item0 = w.x - w.off;
@@ -974,26 +991,15 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
                 }
                 arrive(it_full + 8 * (k % ITEMS));
             };
-            uint32_t c = 0, used = 0;                  // ring position; phase bit per stage of v_raw
+            uint32_t c = 0;
             publish(0);
             for (uint32_t k = 0; w.more() && alive; ++k) {
-                const int todo = w.todo(), kt = w.q.tile(w.t0 + todo - 1), valid = w.q.len - kt * KEYS;
-                const int ext = todo > 0 ? extent(w.q.len, kt) : 0;
+                // read again: it takes no registers beside the loads
+                if (Sh::TWO_LOADERS && k > 0) w.q = seq_of(p, w.s);
                 w.next();
-                publish(k + 1);                        // before this one's last keys are waited for
-                if (alive && todo > 0 && ext > valid) {
-                    const uint32_t st = (c + 2 * todo - 1) % NST;
-                    if (!wait(v_raw + 8 * st, (used >> st) & 1)) break;
-                    used ^= 1u << st;
-                    const uint32_t v = sm_kv + st * Sh::TILE_BYTES;
-                    for (int u = lane; u < (ext - valid) * (D / 8); u += 32) {
-                        const int rr = valid + u / (D / 8), ch = u % (D / 8);
-                        st_shared_v4(v + (ch / 8) * Sh::HALF_BYTES + rr * 128 + (ch % 8) * 16, 0u, 0u, 0u, 0u);
-                    }
-                    fence_proxy_async_shared();
-                    arrive(kv_full + 8 * st);
-                }
-                c += 2 * todo;
+                publish(k + 1);                        // before this one's loads may have to wait
+                if constexpr (Sh::TWO_LOADERS)
+                    if (alive) load_tiles(items[k % ITEMS], 1, 2, c);
             }
         }
     }

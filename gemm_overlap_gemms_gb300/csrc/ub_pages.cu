@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(POOL_THREADS) ub_pool_take_kernel(const __grid
         report(p.status, UB_ERR_CAPACITY);
         return -1;
     };
-    if (FORK) {
+    if constexpr (FORK) {
         for (int64_t i0 = rows.lo; i0 < rows.hi; i0 += POOL_WARPS) {
             const int64_t i = i0 + warp;
             const Child c = i < rows.hi ? child_of(p, static_cast<int>(i)) : Child{-1, 0, 0};
@@ -247,23 +247,23 @@ __global__ void __launch_bounds__(POOL_THREADS) ub_pool_take_kernel(const __grid
                 to[j] = c.part != 0 && j == c.whole ? copy : (page < 0 ? -1 : page);
             }
         }
-        return;
-    }
-    for (int64_t s0 = rows.lo; s0 < rows.hi; s0 += POOL_WARPS) {
-        const int64_t s = s0 + warp;
-        const Entries e = s < rows.hi ? take_range(p, static_cast<int>(s)) : Entries{0, 0};
-        int32_t *row = p.table + s * p.table_row;
-        int mine = 0;
-        for (int64_t j = e.first + lane; j < e.last; j += 32) mine += row[j] < 0 ? 1 : 0;
-        mine = __reduce_add_sync(0xffffffffu, mine);
-        int total;
-        int64_t k = next + warps_before(mine, scratch, &total);
-        next += total;
-        for (int64_t j0 = e.first; j0 < e.last; j0 += 32) {
-            const bool miss = j0 + lane < e.last && row[j0 + lane] < 0;
-            const uint32_t hit = __ballot_sync(0xffffffffu, miss);
-            if (miss) row[j0 + lane] = page_of(k + __popc(hit & ((1u << lane) - 1u)));
-            k += __popc(hit);
+    } else {
+        for (int64_t s0 = rows.lo; s0 < rows.hi; s0 += POOL_WARPS) {
+            const int64_t s = s0 + warp;
+            const Entries e = s < rows.hi ? take_range(p, static_cast<int>(s)) : Entries{0, 0};
+            int32_t *row = p.table + s * p.table_row;
+            int mine = 0;
+            for (int64_t j = e.first + lane; j < e.last; j += 32) mine += row[j] < 0 ? 1 : 0;
+            mine = __reduce_add_sync(0xffffffffu, mine);
+            int total;
+            int64_t k = next + warps_before(mine, scratch, &total);
+            next += total;
+            for (int64_t j0 = e.first; j0 < e.last; j0 += 32) {
+                const bool miss = j0 + lane < e.last && row[j0 + lane] < 0;
+                const uint32_t hit = __ballot_sync(0xffffffffu, miss);
+                if (miss) row[j0 + lane] = page_of(k + __popc(hit & ((1u << lane) - 1u)));
+                k += __popc(hit);
+            }
         }
     }
 }
