@@ -11,9 +11,14 @@
 // where query heads share a key/value head, a power of two of those heads per token (row =
 // token * pack + head). Where items of 128 rows, one q tile, are no more than the CTAs, they
 // are the items (882 tokens, 12 heads: 18 against 20 us; in calls of more items the second
-// tile runs in the first one's pauses and saves reading keys and values twice). Per 128 keys and q tile the tensor core computes S = Q K^T (128 x
-// 128, both operands from shared memory) and O += P V (P from TMEM, V read MN-major); the
-// softmax in between is per TMEM lane, one thread per row, without shuffles.
+// tile runs in the first one's pauses and saves reading keys and values twice). Per 128 keys and
+// q tile the tensor core computes S = Q K^T (128 x 128, both operands from shared memory) and
+// O += P V (P from TMEM, V read MN-major); the softmax in between is per TMEM lane, one thread
+// per row, without shuffles.
+//
+// WINDOW: a row sees the keys j > pos - window and j < sinks. An item then has the key tiles of
+// its rows' windows and of the sinks only, whatever its position: items are of one length, and
+// the schedule orders them by the keys that they reach all the same.
 //
 // Roles (16 warps, one CTA per SM, persistent over items):
 //   warps 0-3, 4-7   softmax of q tile 0 and 1: S from TMEM, P back into the columns of S
@@ -38,6 +43,10 @@
 // item is known 1.6 us after the grid ahead has finished, and the call ends with its longest
 // item (8037 tokens in four sequences, 8 heads each way: 42 us, of which the 24 key tiles of
 // the longest item take 36). Heads of 64: half the MMAs, the same softmax: 2440 cycles a step.
+// Windows: one sequence of 8160 tokens, 8 heads of 128, window 1024 and 4 sinks (11 key tiles an
+// item): 44 us. A CTA takes 8 us to its first scores, 15 us for an item's steps (1.36 each, the
+// masked ones 2) and 5 from one item's last weights to the next one's first scores: Q has one
+// place in shared memory, and the code of an item's ends has left the instruction cache by then.
 #include <cuda_bf16.h>
 #include <limits.h>
 
@@ -116,6 +125,12 @@ __device__ __forceinline__ Sight<WINDOW> sight(const PromptParams &p, int off)
         s.far = sunk < s.near ? sunk : s.near;
     }
     return s;
+}
+
+// The lowest n bits.
+__device__ __forceinline__ uint32_t bits_below(int n)
+{
+    return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
 }
 
 struct Range2 {
@@ -515,17 +530,20 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                 for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, reinterpret_cast<uint32_t *>(s) + c * 32);
                 tmem_wait_ld();
                 const int key0 = in.tile(it.j0 + j) * PROMPT_KEYS, cols = reach - key0;
-                if (cols < PROMPT_KEYS) {
+                // Columns past the row, and those between the sinks and its window: 32 at a time, where
+                // a row of the warp has any (16 sequences of 8158 tokens, window 1024: 37.5 us; every
+                // column compared: 41).
+                const int from = WINDOW ? p.sinks - key0 : 0, to = WINDOW ? it.off + token - p.window + 1 - key0 : 0;
+                if (__any_sync(0xffffffffu, cols < PROMPT_KEYS || (WINDOW && to > 0 && from < PROMPT_KEYS))) {
 #pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (c >= cols) s[c] = -INFINITY;
-                }
-                if (WINDOW) {  // columns between the sinks and the row's window
-                    const int from = p.sinks - key0, to = it.off + token - p.window + 1 - key0;
-                    if (to > 0 && from < PROMPT_KEYS) {
+                    for (int c0 = 0; c0 < 128; c0 += 32) {
+                        uint32_t seen = bits_below(cols - c0);
+                        if (WINDOW) seen &= bits_below(from - c0) | ~bits_below(to - c0);
+                        if (__any_sync(0xffffffffu, seen != 0xffffffffu)) {
 #pragma unroll
-                        for (int c = 0; c < 128; ++c)
-                            if (c >= from && c < to) s[c] = -INFINITY;
+                            for (int c = 0; c < 32; ++c)
+                                if (!(seen & (1u << c))) s[c0 + c] = -INFINITY;
+                        }
                     }
                 }
                 float mx[4] = {m, m, m, m};
@@ -725,6 +743,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                 if (r.n[i] == 0) {
                     if (it.slot >= 0) continue;        // no key in this piece: not a part of this q tile
                     const float zero[32] = {};
+#pragma unroll 1
                     for (int c = 0; c < D; c += 32) store(i, c, zero, 0.f, true);
                     store_lse(i, -INFINITY, 0.f);
                     continue;
@@ -736,7 +755,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                 ++n_o[i];
                 tc_fence_after();
                 const float inv = 1.f / l;
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     float v[32];
                     tmem_ld32(tmem + TM_O + i * 128 + lanes + c, reinterpret_cast<uint32_t *>(v));
