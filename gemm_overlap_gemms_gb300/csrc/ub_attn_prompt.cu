@@ -44,9 +44,9 @@
 // item (8037 tokens in four sequences, 8 heads each way: 42 us, of which the 24 key tiles of
 // the longest item take 36). Heads of 64: half the MMAs, the same softmax: 2440 cycles a step.
 // Windows: one sequence of 8160 tokens, 8 heads of 128, window 1024 and 4 sinks (11 key tiles an
-// item): 44 us. A CTA takes 8 us to its first scores, 15 us for an item's steps (1.36 each, the
-// masked ones 2) and 5 from one item's last weights to the next one's first scores: Q has one
-// place in shared memory, and the code of an item's ends has left the instruction cache by then.
+// item): 42 us. A CTA takes 7 us to its first scores, 15 us for an item's steps (1.2-1.4 each, the
+// masked ones up to 2) and 4-5 from one item's last weights to the next one's first scores: Q has
+// one place in shared memory, and the code of an item's ends runs cold.
 #include <cuda_bf16.h>
 #include <limits.h>
 
@@ -76,12 +76,12 @@ struct PromptShape {
     static constexpr int TILE_BYTES = PROMPT_KEYS * D * 2;
     static constexpr int HALF_BYTES = PROMPT_KEYS * 128;  // 64 columns of a tile
     static constexpr int STAGES = D == 128 ? 5 : 10;
-    static constexpr int SMEM = (2 + STAGES) * TILE_BYTES + 2048 + 768;
+    static constexpr int SMEM = (2 + STAGES) * TILE_BYTES + 2048 + 1024;
     static_assert(SMEM <= 232448, "shared memory");
     static_assert(STAGES < DONE, "an unseen release per ring position at most");
 };
 
-// One work item as the schedule warp publishes it.
+// One work item.
 struct Item {
     int row0;    // first token (row of q); -1: no more items
     int ntok;    // tokens
@@ -159,6 +159,14 @@ __device__ __forceinline__ Range2 ranges(const Item &it, int tpt, int gap)
     r.limmax = r.lim[0] > r.lim[1] ? r.lim[0] : r.lim[1];
     return r;
 }
+// What the schedule warp publishes: ready for use, as code that runs once per item is cold, and all
+// roles would run it at the same time (four sequences in windows, as below: 37.5 to 35.3 us; one
+// sequence of 16384 tokens 302 to 298).
+template <bool WINDOW>
+struct Work : Item {
+    Sight<WINDOW> in;
+    Range2 r;
+};
 // The same values, known to be the same in every lane.
 __device__ __forceinline__ Range2 uniform(Range2 r)
 {
@@ -430,10 +438,10 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                    l_full = misc + 80, l_empty = misc + 96, o_full = misc + 112, drain = misc + 128, want = misc + 144,
                    parts_done = misc + 168, join_go = misc + 176,
                    it_full = misc + 184, it_empty = it_full + 8 * ITEMS;
-    Item *items = reinterpret_cast<Item *>(reinterpret_cast<uint8_t *>(bars) + 16 * NST + 8 * DONE + 184 + 16 * ITEMS);
+    auto *items = reinterpret_cast<Work<WINDOW> *>(reinterpret_cast<uint8_t *>(bars) + 16 * NST + 8 * DONE + 184 + 16 * ITEMS);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(items + ITEMS);
     volatile uint32_t *turn = tmem_slot + 1;     // steps that the issuer of each q tile has done
-    static_assert(16 * NST + 8 * DONE + 184 + 16 * ITEMS + sizeof(Item) * ITEMS + 12 <= 768, "barrier area");
+    static_assert(16 * NST + 8 * DONE + 184 + 16 * ITEMS + sizeof(Work<WINDOW>) * ITEMS + 12 <= 1024, "barrier area");
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     if ((sm_q & 1023u) != 0u) {  // the swizzled tiles need what the declaration asks for
@@ -495,7 +503,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
         if (lane == 0) mbar_arrive(bar);
     };
     // The k-th item of this CTA; false at the end (or when a wait ran out).
-    auto next_item = [&](uint32_t k, Item &it) {
+    auto next_item = [&](uint32_t k, Work<WINDOW> &it) {
         const uint32_t slot = k % ITEMS;
         if (!wait(it_full + 8 * slot, (k / ITEMS) & 1)) return false;
         it = items[slot];
@@ -511,17 +519,17 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
         const uint32_t ts = tmem + TM_S + i * 128 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const float sl = p.scale * 1.4426950408889634f;
         uint32_t n_s = 0, n_l = 0;                     // phases used
-        Item it;
+        Work<WINDOW> it;
         uint32_t k = 0;
         for (; next_item(k, it); ++k) {
-            const Sight<WINDOW> in = sight<WINDOW>(p, it.off);
-            const Range2 r = ranges(it, tpt, in.gap());
-            if (r.n[i] == 0) continue;
+            const Sight<WINDOW> in = it.in;
+            const int n = i == 0 ? it.r.n[0] : it.r.n[1];
+            if (n == 0) continue;
             const int token = i * tpt + (row >> p.pack_shift);
             int reach = it.off + token + 1;            // keys this row sees
             reach = reach > it.len ? it.len : reach;
             float m = -INFINITY, l = 0.f;
-            for (int j = 0; j < r.n[i]; ++j) {
+            for (int j = 0; j < n; ++j) {
                 if (!wait(s_full + 8 * i, n_s & 1)) break;
                 ++n_s;
                 tc_fence_after();
@@ -531,8 +539,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                 tmem_wait_ld();
                 const int key0 = in.tile(it.j0 + j) * PROMPT_KEYS, cols = reach - key0;
                 // Columns past the row, and those between the sinks and its window: 32 at a time, where
-                // a row of the warp has any (16 sequences of 8158 tokens, window 1024: 37.5 us; every
-                // column compared: 41).
+                // a row of the warp has any (four sequences of 8037 tokens together, 8 heads, window
+                // 1024: 37.5 us; every column compared: 41.4).
                 const int from = WINDOW ? p.sinks - key0 : 0, to = WINDOW ? it.off + token - p.window + 1 - key0 : 0;
                 if (__any_sync(0xffffffffu, cols < PROMPT_KEYS || (WINDOW && to > 0 && from < PROMPT_KEYS))) {
 #pragma unroll
@@ -632,8 +640,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                 arrive(join_go);
             }
             if (alive && wait(join_go, 0)) {
-                const int gap = sight<WINDOW>(p, it.off).gap();
-                const Range2 r = ranges(it, tpt, gap);
+                const int gap = it.in.gap();
+                const Range2 r = it.r;
                 const int per = D / 16;                // units of a q tile
                 for (int u = it.piece + it.pieces * i; u < 2 * per; u += 2 * it.pieces) {
                     const int t = u / per, c = (u - t * per) * 16;
@@ -709,9 +717,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
         const int row = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         uint32_t n_o[2] = {0, 0};
-        Item it;
+        Work<WINDOW> it;
         for (uint32_t k = 0; next_item(k, it); ++k) {
-            const Range2 r = ranges(it, tpt, sight<WINDOW>(p, it.off).gap());
+            const Range2 r = it.r;
             // A split item's part: [columns / 4][256 rows][4] fp32 and the rows' maxima and sums.
             float4 *part_o = reinterpret_cast<float4 *>(p.ws) + static_cast<int64_t>(it.slot + it.piece) * (64 * D) + row;
             float *part_m = p.ws_rows + static_cast<int64_t>(it.slot + it.piece) * 512 + row;
@@ -789,22 +797,22 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
         uint32_t c = 0, n_q[2] = {0, 0};               // ring position, Q loads so far
         uint32_t n_done = 0, freed = 0;                // releases seen; ring positions that they freed
         uint32_t two = 0, n_ends = 0;                  // bit of each release to come: frees two positions
-        Item it;
+        Work<WINDOW> it;
         const int box = PROMPT_KEYS < (1 << p.b.page_shift) ? PROMPT_KEYS : (1 << p.b.page_shift);
         constexpr int HALVES = D / 64;
         for (uint32_t k = 0;; ++k) {
             if (k >= 2) arrive(want);                  // every load of item k - 1 has been issued
             if (!next_item(k, it)) break;
-            const Sight<WINDOW> in = sight<WINDOW>(p, it.off);
-            const Range2 r = ranges(it, tpt, in.gap());
+            const Sight<WINDOW> in = it.in;
+            const Range2 r = it.r;
             const int kvh = (it.unit << p.pack_shift) / p.group;
             const int32_t *table = p.paged ? p.b.page_table + it.src * p.b.table_row : nullptr;
             const int pages = p.paged ? (it.len + (1 << p.b.page_shift) - 1) >> p.b.page_shift : 0;
             int cached0 = 0, cached_n = 0, ids = -1;   // page ids, one per lane
             auto load_q = [&](int i) {
-                if (r.n[i] == 0) return;
-                if (n_q[i] > 0 && !wait(q_empty + 8 * i, (n_q[i] - 1) & 1)) return;
-                ++n_q[i];
+                if ((i == 0 ? r.n[0] : r.n[1]) == 0) return;
+                const int n = i == 0 ? n_q[0]++ : n_q[1]++;
+                if (n > 0 && !wait(q_empty + 8 * i, (n - 1) & 1)) return;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(q_full + 8 * i, Sh::TILE_BYTES);
                     for (int hf = 0; hf < HALVES; ++hf)
@@ -813,8 +821,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                 }
                 __syncwarp();
             };
-            load_q(0);
-            for (int j = 0; j < r.nmax && alive; ++j) {
+            for (int j = 0; j < 2 || j < r.nmax; ++j) {
+                if (j < 2) load_q(j);
+                if (!alive || j >= r.nmax) continue;
                 const int kt = in.tile(it.j0 + j), key0 = kt * PROMPT_KEYS;
                 // every key that is multiplied is loaded (pages past the length as zeros)
                 const int n_box = p.paged ? (extent(r.limmax, kt) + box - 1) / box : 1;
@@ -865,7 +874,6 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                     }
                     __syncwarp();
                 }
-                if (j == 0 && alive) load_q(1);
             }
             if (!alive) break;
         }
@@ -894,11 +902,11 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
             }
             return true;
         };
-        Item it;
+        Work<WINDOW> it;
         for (uint32_t k = 0; next_item(k, it); ++k) {
-            Sight<WINDOW> in = sight<WINDOW>(p, it.off);
+            Sight<WINDOW> in = it.in;
             if (WINDOW) in.near = __shfl_sync(0xffffffffu, in.near, 0), in.far = __shfl_sync(0xffffffffu, in.far, 0);
-            const Range2 r = uniform(ranges(it, tpt, in.gap()));
+            const Range2 r = uniform(it.r);
             const int n = i == 0 ? r.n[0] : r.n[1], lim = i == 0 ? r.lim[0] : r.lim[1];
             const int j0 = __shfl_sync(0xffffffffu, it.j0, 0);
             if (n > 0) {
@@ -1005,7 +1013,12 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
         // the rest by tickets, drawn when the loads of the item before have been issued.
         auto publish = [&](uint32_t k, Item it) {
             if (k >= ITEMS && !wait(it_empty + 8 * (k % ITEMS), (k / ITEMS - 1) & 1)) return;
-            if (lane == 0) items[k % ITEMS] = it;
+            if (lane == 0) {
+                Work<WINDOW> &w = items[k % ITEMS];
+                static_cast<Item &>(w) = it;
+                w.in = sight<WINDOW>(p, it.off);
+                w.r = ranges(it, tpt, w.in.gap());
+            }
             arrive(it_full + 8 * (k % ITEMS));
         };
         auto draw = [&](uint32_t k) {
@@ -1034,8 +1047,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) ub_attn_prompt_kernel(const __g
                 it1 = draw(k + 1);
                 if (!alive) break;
             }
-            const Sight<WINDOW> in = sight<WINDOW>(p, it.off);
-            const Range2 r = ranges(it, tpt, in.gap());
+            const Sight<WINDOW> in = items[k % ITEMS].in;
+            const Range2 r = items[k % ITEMS].r;
             const int j = r.nmax - 1, kt = in.tile(it.j0 + j), valid = it.len - kt * PROMPT_KEYS;
             const int ext = r.nmax > 0 ? extent(r.limmax, kt) : 0;
             if (ext > valid) {
