@@ -53,6 +53,10 @@ constexpr float RESCALE_LOG2 = 8.f;      // growth of the maximum (log2) that is
 __host__ __device__ constexpr int tile_units(int head_dim, bool two) { return two ? 15 : (head_dim == 64 ? 7 : 9); }
 constexpr int ITEM_COST = 50, JOIN_COST = 80;
 constexpr int MIN_UNITS = 24;            // of a CTA, at least: no less than any tile
+// Units of a CTA up to which items of one q tile are preferred. 16 sequences of 64 drafts, 8 query
+// and 2 key/value heads of 128, against items of two: 1024 keys 16.9 and 26.9 us, 2048 keys 29.9 and
+// 28.4, 4096 keys (150 units) 37.4 and 43.3, 6000 keys (200) 46.6 and 50.8, 8192 keys (250) 60.5 and 56.8.
+constexpr int SHORT_SHARE = 200;
 static_assert(ITEM_COST <= TREE_MOST_UNITS && tile_units(128, true) <= MIN_UNITS, "units");
 
 template <int D>
@@ -85,7 +89,8 @@ struct Seq {
     __device__ __forceinline__ int span() const { return tiles * per; }
     __device__ __forceinline__ int cost() const { return span() + ITEM_COST; }
 };
-__device__ __forceinline__ Seq seq_from(const TreeParams &p, int a, int z, int len)
+// height: tokens of an item
+__device__ __forceinline__ Seq seq_from(const TreeParams &p, int a, int z, int len, int height)
 {
     Seq q;
     a = a < 0 ? 0 : (a > p.T ? p.T : a);
@@ -100,13 +105,13 @@ __device__ __forceinline__ Seq seq_from(const TreeParams &p, int a, int z, int l
     const int sunk = (p.sinks + KEYS - 1) / KEYS;
     q.far = sunk < q.near ? sunk : q.near;
     q.tiles = q.len > 0 ? (q.len + KEYS - 1) / KEYS - q.near + q.far : 1;
-    q.blocks = static_cast<int>(static_cast<uint32_t>(q.n + 2 * p.tokens - 1) / static_cast<uint32_t>(2 * p.tokens));
-    q.per = tile_units(p.head_dim, q.n > p.tokens);
+    q.blocks = static_cast<int>(static_cast<uint32_t>(q.n + height - 1) / static_cast<uint32_t>(height));
+    q.per = tile_units(p.head_dim, height > p.tokens && q.n > p.tokens);
     return q;
 }
-__device__ __forceinline__ Seq seq_of(const TreeParams &p, int s)
+__device__ __forceinline__ Seq seq_of(const TreeParams &p, int s, int height)
 {
-    return seq_from(p, p.b.seq_starts[s], p.b.seq_starts[s + 1], p.b.kv_lens[s]);
+    return seq_from(p, p.b.seq_starts[s], p.b.seq_starts[s + 1], p.b.kv_lens[s], height);
 }
 // Lane l's sequence.
 __device__ __forceinline__ Seq from_lane(const Seq &q, int l)
@@ -158,6 +163,7 @@ struct Walk {
     int64_t x, left;  // first unit of the item here, units to go; whole items: items to go
     int off;          // units of the item that are others' (before x)
     bool by_items;    // whole items only
+    int height;       // tokens of an item: one or two q tiles of them
     int s, item;      // sequence, item of it
     int t0, t1;
     Seq q;
@@ -178,7 +184,7 @@ struct Walk {
     __device__ __forceinline__ void settle_on()  // an item of sequence s, or of the next that has one
     {
         while (s < p.b.n_seqs) {
-            q = seq_of(p, s);
+            q = seq_of(p, s, height);
             if (item < q.blocks * p.units) break;
             item = 0;
             ++s;
@@ -200,11 +206,11 @@ struct Walk {
         }
     }
     __device__ __forceinline__ int unit() const { return q.blocks == 1 ? item : item / q.blocks; }
-    __device__ __forceinline__ int first_token() const { return (item - unit() * q.blocks) * 2 * p.tokens; }
+    __device__ __forceinline__ int first_token() const { return (item - unit() * q.blocks) * height; }
     __device__ __forceinline__ int tokens() const  // of this item
     {
         const int n = q.n - first_token();
-        return n < 2 * p.tokens ? n : 2 * p.tokens;
+        return n < height ? n : height;
     }
     // Whole in this CTA; and how many key tiles of it there are to do (an item without keys: none).
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == q.tiles; }
@@ -222,22 +228,36 @@ __device__ __forceinline__ void begin(Walk &w, int lane, int cta, int grid)
     w.by_items = false;
     w.split = Split{0, 0};
     const int n_seqs = p.b.n_seqs;
-    Seq own = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-    if (lane < n_seqs) own = seq_of(p, lane);
-    // Sums over the sequences: items, and units of the split.
-    I items = own.blocks, total = static_cast<I>(own.blocks) * own.cost();
-    int most = own.blocks > 0 ? own.span() : 0;
+    Seq own;
+    I items, total;
+    int most;
+    w.height = 2 * p.tokens;
 #pragma unroll 1
-    for (int i = lane + 32; i < n_seqs; i += 32) {
-        const Seq q = seq_of(p, i);
-        items += q.blocks;
-        total += static_cast<I>(q.blocks) * q.cost();
-        most = q.blocks > 0 && q.span() > most ? q.span() : most;
+    for (;;) {
+        // Sums over the sequences: items, and units of the split; q tiles.
+        I tiles = 0;
+        items = total = 0;
+        most = 0;
+        own = Seq{0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 1
+        for (int i = lane; i < n_seqs; i += 32) {
+            const Seq q = seq_of(p, i, w.height);
+            if (i == lane) own = q;
+            items += q.blocks;
+            tiles += static_cast<uint32_t>(q.n + p.tokens - 1) / static_cast<uint32_t>(p.tokens);
+            total += static_cast<I>(q.blocks) * q.cost();
+            most = q.blocks > 0 && q.span() > most ? q.span() : most;
+        }
+        items = warp_sum(items) * p.units;
+        tiles = warp_sum(tiles) * p.units;
+        total = warp_sum(total) * p.units;
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (items == 0) return;
+        // Items of one q tile where those are no more than the CTAs and the shares are short: the
+        // keys are then read twice, but a part that has to be joined is half as large.
+        if (tiles > grid || tiles == items || total > static_cast<I>(grid) * SHORT_SHARE) break;
+        w.height = p.tokens;
     }
-    items = warp_sum(items) * p.units;
-    total = warp_sum(total) * p.units;
-    most = __reduce_max_sync(0xffffffffu, most);
-    if (items == 0) return;
     // Whole items, as many for each CTA, where the longest ones in every round would not take much
     // longer than equal shares: a share saves the difference and costs a join. Else equal shares,
     // of at least MIN_UNITS units.
@@ -255,7 +275,7 @@ __device__ __forceinline__ void begin(Walk &w, int lane, int cta, int grid)
 #pragma unroll 1
     for (int i0 = 0; i0 < n_seqs; i0 += 32) {
         Seq q = own;
-        if (i0 > 0) q = seq_of(p, i0 + lane < n_seqs ? i0 + lane : n_seqs - 1);
+        if (i0 > 0) q = seq_of(p, i0 + lane < n_seqs ? i0 + lane : n_seqs - 1, w.height);
         I mine = i0 + lane < n_seqs ? static_cast<I>(q.blocks) * p.units * (w.by_items ? 1 : q.cost()) : 0, upto = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -995,7 +1015,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
             publish(0);
             for (uint32_t k = 0; w.more() && alive; ++k) {
                 // read again: it takes no registers beside the loads
-                if (Sh::TWO_LOADERS && k > 0) w.q = seq_of(p, w.s);
+                if (Sh::TWO_LOADERS && k > 0) w.q = seq_of(p, w.s, w.height);
                 w.next();
                 publish(k + 1);                        // before this one's loads may have to wait
                 if constexpr (Sh::TWO_LOADERS)
