@@ -412,7 +412,8 @@ int tree_call(const char *fn, ub_handle_t h, const ub_attn_t *in, const int32_t 
     int64_t grid = c.sms < TREE_MOST_CTAS ? c.sms : TREE_MOST_CTAS;
     const int64_t items = (T / (2 * p.tokens) + (a.n_seqs < T ? a.n_seqs : T)) * p.units;
     const int64_t tiles = (keys + TREE_KEYS - 1) / TREE_KEYS;
-    if (items <= grid && items * tiles < grid) grid = items * tiles;
+    const int64_t q_tiles = (T / p.tokens + (a.n_seqs < T ? a.n_seqs : T)) * p.units;
+    if (q_tiles <= grid && q_tiles * tiles < grid) grid = q_tiles * tiles;
     p.many_units = items > INT32_MAX / TREE_MOST_UNITS / (tiles + 1) ? 1 : 0;
     const int64_t room = static_cast<int64_t>(c.ws_floats) + 512 * PROMPT_SLOTS;
     if (DECODE_COUNTERS * grid > c.join_words || TREE_SLOTS * grid * tree_slot_floats(a.head_dim) > room)

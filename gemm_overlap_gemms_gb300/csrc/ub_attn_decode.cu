@@ -42,6 +42,9 @@
 // counted, joined). 64 sequences, 127938 keys, 2 key/value heads (131 MB): 29 us, 18 of them
 // streaming. 15 sequences of 2900 keys, one key/value head, 8 query heads (22 MB, 10 parts
 // each): 10.4 us. Four sequences of 300 keys, 8 heads: 7.4-9.4 us a call, bound by the host's side.
+//
+// WINDOW: the keys j > kv_len - 1 - window and j < sinks, in the tiles that hold one. The 128
+// sequences of above, window 2048 and 64 sinks (1.06 GB): 161 us, 6.6 TB/s.
 #include <cuda_bf16.h>
 
 #include "ub_attn.h"

@@ -488,7 +488,9 @@ int ub_attn_decode_window(ub_handle_t h, const ub_attn_t *a, int32_t window, int
  * the text, its ancestors and itself; with window > 0 of those only the keys whose position lies
  * within `window` positions of its own, itself included, or below `sinks`. Types, outputs, lse and
  * arguments as ub_attn_prompt over a cache. The drafts of a sequence may be many or one. A place
- * below zero (kv_lens[s] < n_s) is no key; a row without any key gives 0 and lse -inf.
+ * below zero (kv_lens[s] < n_s) is no key; a row without any key gives 0 and lse -inf. The rows of
+ * the cache up to kv_lens have to be finite, unseen drafts' too (an infinite value times its weight
+ * of zero is no number); what lies behind them may be anything.
  * The (sequence, heads, 128 keys) tiles are split evenly over the GPU and joined in a fixed
  * order; the CTAs of an item that is split wait for one another (bounded, UB_ERR_TIMEOUT).
  *
