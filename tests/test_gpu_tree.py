@@ -103,6 +103,21 @@ def test_splits(buf, new, past, heads, kv_heads, dim):
     ok(buf)
 
 
+@pytest.mark.parametrize("window,sinks", [(0, 0), (500, 3)])
+@pytest.mark.parametrize("new,past,heads,kv_heads,dim", [
+    ([40 + i % 25 for i in range(44)], [100 + 37 * i for i in range(44)], 8, 2, 128),
+    ([33 + i % 32 for i in range(40)], [3000 + 50 * i for i in range(40)], 16, 4, 64),
+    ([64, 50], [70000, 70100], 8, 2, 128), ([130, 64, 1], [66000, 67000, 68000], 16, 4, 64)])
+def test_items_of_two_query_tiles(buf, new, past, heads, kv_heads, dim, window, sinks):
+    """More query tiles than CTAs, and few over so many keys that each takes them for two."""
+    b = ref.Batch(new, [n + k for n, k in zip(new, past)], page=64, kv_heads=kv_heads, dim=dim, seed=dim, fill=float("nan"))
+    q, parents, out = run(buf, b, heads, dim, window=window, sinks=sinks)
+    for _ in range(3):
+        again = buf.attn_tree(q, b.k_cache, b.v_cache, b.starts, b.lens, b.table, parents, window=window, sinks=sinks)
+        assert torch.equal(out, again)
+    ok(buf)
+
+
 @pytest.mark.parametrize("window,sinks", [(1, 0), (2, 3), (5, 0), (40, 4), (128, 200), (300, 1), (2000, 0), (1 << 30, 0)])
 @pytest.mark.parametrize("dim,page", [(128, 16), (64, 128)])
 def test_windows(buf, window, sinks, dim, page):
