@@ -135,6 +135,37 @@ def test_windows(buf, window, sinks, dim, page):
     run(buf, b, 8, dim, "chain", window=window, sinks=sinks, table=table)
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (70, 5)])
+def test_strided_views(buf, dim, window, sinks):
+    """Queries inside a fused projection, outputs by heads, caches and table as views."""
+    new, heads, kv_heads = [5, 64, 1, 40, 9], 8, 2
+    kv = [n + past for n, past in zip(new, [200, 0, 33, 900, 4000])]
+    b = ref.Batch(new, kv, page=16, kv_heads=kv_heads, dim=dim, pad=2, seed=dim, fill=float("nan"))
+    whole = torch.stack((b.k_cache, b.v_cache)).transpose(1, 2).contiguous()  # pages inside the heads
+    b.k_cache, b.v_cache = whole[0].transpose(0, 1), whole[1].transpose(0, 1)
+    wide = torch.full((len(new), b.table.shape[1] + 7), 1 << 30, dtype=torch.int32, device="cuda")
+    wide[:, :-7] = b.table
+    buf.set_active_shape([b.T, 256])
+    per, parents = trees(b)
+    q = b.randn(b.T, heads + 2 * kv_heads, dim, std=1.5)[:, :heads]
+    out = sentinel((heads, b.T, dim)).transpose(0, 1)
+    _, lse = buf.attn_tree(q, b.k_cache, b.v_cache, b.starts, b.lens, wide[:, :-7], parents, out=out, lse=True,
+                           window=window, sinks=sinks)
+    ok(buf)
+    check(b, q, per, out.contiguous(), lse, window, sinks)
+
+
+@pytest.mark.parametrize("most,window", [(1, 0), (3, 0), (3, 64), (40, 0)])
+def test_many_sequences(buf, most, window):
+    """More sequences than a warp looks at at once, and than there are CTAs; some without drafts."""
+    rng = random.Random(most)
+    new = [rng.randint(0, most) for _ in range(700)]
+    kv = [n + rng.randint(0, 300) for n in new]
+    b = ref.Batch(new, kv, page=32, kv_heads=2, dim=64, pad=1, seed=most, fill=float("nan"))
+    run(buf, b, 4, 64, window=window, sinks=2)
+
+
 def test_a_chain_is_a_prompt(buf):
     """A chain of drafts is what attn_prompt_paged computes, an only draft what attn_decode does."""
     b = ref.Batch([40, 9], [900, 9], page=16, kv_heads=2, dim=128, seed=2, fill=float("nan"))

@@ -165,6 +165,31 @@ def test_incomplete_last_rounds_are_split(buf, n, heads, kv_heads, dim, window):
     ok(buf)
 
 
+@pytest.mark.parametrize("window,sinks", [(70, 5), (600, 0)])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_strided_views(buf, window, sinks, dim):
+    """Queries inside a fused projection, outputs by heads, caches and table as views."""
+    new, heads, kv_heads = [5, 300, 1, 40], 8, 2
+    kv = [n + past for n, past in zip(new, [200, 0, 33, 900])]
+    b = ref.Batch(new, kv, page=16, kv_heads=kv_heads, dim=dim, pad=2, seed=dim, fill=float("nan"))
+    whole = torch.stack((b.k_cache, b.v_cache)).transpose(1, 2).contiguous()  # pages inside the heads
+    b.k_cache, b.v_cache = whole[0].transpose(0, 1), whole[1].transpose(0, 1)
+    wide = torch.full((len(new), b.table.shape[1] + 7), 1 << 30, dtype=torch.int32, device="cuda")
+    wide[:, :-7] = b.table
+    buf.set_active_shape([b.T, 256])
+    q = b.randn(b.T, heads + 2 * kv_heads, dim, std=1.5)[:, :heads]
+    out = sentinel((heads, b.T, dim)).transpose(0, 1)
+    _, lse = buf.attn_prompt_paged(q, b.k_cache, b.v_cache, b.starts, b.lens, wide[:, :-7], out=out, lse=True,
+                                   window=window, sinks=sinks)
+    ok(buf)
+    check(b, q, lambda s: (b.rows(b.k_cache, s), b.rows(b.v_cache, s)), out.contiguous(), lse, window, sinks, new)
+    out = sentinel((heads, b.T, dim)).transpose(0, 1)
+    _, lse = buf.attn_decode(q, b.k_cache, b.v_cache, b.lens, wide[:, :-7], out=out, lse=True, window=window, sinks=sinks)
+    ok(buf)
+    check_rows(b, q, out.contiguous(), lse, window, sinks, range(len(kv)))
+    assert is_sentinel(out[len(kv):].contiguous())
+
+
 def test_rows_without_a_key(buf):
     """kv_lens below the new tokens: the first rows have no position in the cache."""
     b = ref.Batch([40, 200], [30, 140], page=16, kv_heads=2, dim=128, seed=3, fill=float("nan"))
