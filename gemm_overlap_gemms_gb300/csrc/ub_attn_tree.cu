@@ -323,7 +323,12 @@ struct Item {
     int lo, near, far;
     int t0, todo;    // key tiles in sight: the first one, how many (0: the item has no keys)
     int whole;       // all of the item's
-    __device__ __forceinline__ int tile(int j) const { return t0 + j < far ? t0 + j : t0 + j - far + near; }
+    // The last keys first: a row's path, which is walked from its own draft up, is then walked once.
+    __device__ __forceinline__ int tile(int j) const
+    {
+        const int t = t0 + todo - 1 - j;
+        return t < far ? t : t - far + near;
+    }
 };
 // An item that other CTAs have parts of, for the join.
 struct Pending {
@@ -343,9 +348,10 @@ __device__ __forceinline__ int parent_of(const TreeParams &p, int start, int i)
     return -1;
 }
 
-// Which of the 128 keys from key0 on draft `i` at position `pos` sees (i < 0: a row of no draft);
-// start: the token of the sequence's first draft, text: keys before the drafts.
-__device__ __forceinline__ void keys_seen(const TreeParams &p, int start, int text, int i, int pos, int key0, uint32_t *bits)
+// Which of the 128 keys from key0 on a row at position `pos` sees; start: the token of the
+// sequence's first draft, text: keys before the drafts. `i` is the first draft of the row's path that
+// no tile behind this one holds (below zero: none), `d` how far it is from the row's own; both go on.
+__device__ __forceinline__ void keys_seen(const TreeParams &p, int start, int text, int &i, int &d, int pos, int key0, uint32_t *bits)
 {
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
@@ -356,7 +362,6 @@ __device__ __forceinline__ void keys_seen(const TreeParams &p, int start, int te
     // The ancestors come in falling order: word by word, from the last.
     const int gone = key0 - text;  // drafts before this tile
     if (gone + KEYS <= 0) return;  // no drafts in it (the same for all lanes)
-    int d = 0;                     // steps from the row's own draft
     for (; i >= gone + KEYS; ++d) i = parent_of(p, start, i);
 #pragma unroll
     for (int w = 3; w >= 0; --w) {
@@ -543,13 +548,14 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
                 for (int up = parent_of(p, it.row0 - it.first, draft); up >= 0; up = parent_of(p, it.row0 - it.first, up)) ++pos;
             __syncwarp();
             float m = -INFINITY, l = 0.f;
+            int up = draft, steps = 0;                 // on the row's path
             for (int j = two ? 0 : i; j < todo; j += two ? 1 : 2) {
                 // Some row does not see all of the tile: drafts, or keys left of a window. The walks run
                 // while S is computed.
                 const int key0 = it.tile(j) * KEYS;
                 const bool edge = key0 + KEYS > it.text || (p.window > 0 && key0 <= it.len - p.window && key0 + KEYS > p.sinks);
                 uint32_t bits[4];
-                if (edge) keys_seen(p, it.row0 - it.first, it.text, draft, pos, key0, bits);
+                if (edge) keys_seen(p, it.row0 - it.first, it.text, up, steps, pos, key0, bits);
                 if (!wait(s_full + 8 * i, n_s & 1)) break;
                 ++n_s;
                 tc_fence_after();
@@ -810,13 +816,12 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
             const int len = it.len, todo = it.todo;
             const int32_t *table = p.b.page_table + it.seq * p.b.table_row;
             const int pages = (len + (1 << p.b.page_shift) - 1) >> p.b.page_shift;
-            int cached0 = 0, cached_n = 0, ids = -1;   // page ids, one per lane
+            int cached0 = INT32_MAX, ids = -1;         // page ids, one per lane
             for (int j = 0; j < todo; ++j, ++c) {
                 const int kt = it.tile(j), key0 = kt * KEYS, ext = extent(len, kt);
                 const int n_box = (ext + box - 1) / box, page0 = key0 >> p.b.page_shift;
-                if (page0 + boxes > cached0 + cached_n) {
-                    cached0 = page0;
-                    cached_n = 32;
+                if (page0 < cached0) {                 // this tile's pages, and those before it
+                    cached0 = page0 + boxes > 32 ? page0 + boxes - 32 : 0;
                     // a page that no row sees may be another sequence's by now, or nobody's
                     const int64_t first = static_cast<int64_t>(cached0 + lane) << p.b.page_shift;
                     const bool seen = cached0 + lane < pages &&
@@ -908,7 +913,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
                 const int todo = same(it.todo), len = same(it.len), t0 = same(it.t0), far = same(it.far), gap = same(it.near) - far;
                 const int stride = two ? 1 : 2, j0 = two ? 0 : i;
                 const uint64_t q_desc = smem_desc_sw128(sm_q + (two ? i * Sh::TILE_BYTES : 0));
-                auto tile_of = [&](int j) { return t0 + j < far ? t0 + j : t0 + j + gap; };
+                auto tile_of = [&](int j) { const int t = t0 + todo - 1 - j; return t < far ? t : t + gap; };
                 if (!wait(q_full, k & 1)) break;
                 // O of the last item has been read before this one's first product.
                 if (j0 >= todo) {
