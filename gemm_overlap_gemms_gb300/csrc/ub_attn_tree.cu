@@ -56,10 +56,15 @@ constexpr int TM_S = 0, TM_O = 256;      // TMEM columns: S_i at 128 i (and P_i 
 constexpr float RESCALE_LOG2 = 8.f;      // growth of the maximum (log2) that is put off
 // Units of the split, about 0.08 us: what a key tile takes in an item of one q tile and of two, heads
 // of 64 and of 128; the end of an item (the pipelines run empty, O joined and written, the next
-// queries loaded); a join. From the times of CTAs of calls of mixed items: key tiles 0.5-0.6 and
-// 1.1 us with heads of 64, 0.6-1.0 and 1.2 with heads of 128, ends 2-4 us, a join 6.
+// queries loaded). From the times of CTAs of calls of mixed items: key tiles 0.5-0.6 and 1.1 us with
+// heads of 64, 0.6-1.0 and 1.2 with heads of 128, ends 2-4 us.
 __host__ __device__ constexpr int tile_units(int head_dim, bool two) { return two ? 15 : (head_dim == 64 ? 7 : 9); }
-constexpr int ITEM_COST = 50, JOIN_COST = 80;
+constexpr int ITEM_COST = 50;
+// A join, more of them at once taking longer (their parts, and the latest of their CTAs). 8 query and
+// 8 key/value heads of 128, 16 drafts over 2048 keys, joined and whole: 2 sequences (16 items) 16.3
+// and 20.4 us, 4 18.4 and 20.8, 8 24.6 and 21.4; 16 of 64 drafts, 8 heads on 2 (64 items), 2048 keys
+// 29.8 and 22.3, 3000 keys 37.5 and 28.8, 6000 keys 45.6 and 48.5.
+__device__ __forceinline__ int join_units(int items) { return 80 + items; }
 constexpr int MIN_UNITS = 24;            // of a CTA, at least: no less than any tile
 // Units of a CTA up to which items of one q tile are preferred. 16 sequences of 64 drafts, 8 query
 // and 2 key/value heads of 128, against items of two: 1024 keys 16.9 and 26.9 us, 2048 keys 29.9 and
@@ -270,7 +275,8 @@ __device__ __forceinline__ void begin(Walk &w, int lane, int cta, int grid)
     // longer than equal shares: a share saves the difference and costs a join. Else equal shares,
     // of at least MIN_UNITS units.
     const I rounds = quotient(items + grid - 1, static_cast<I>(grid));
-    w.by_items = static_cast<int64_t>(rounds) * most <= quotient(total - items * ITEM_COST, static_cast<I>(grid)) + JOIN_COST;
+    w.by_items = static_cast<int64_t>(rounds) * most <= quotient(total - items * ITEM_COST, static_cast<I>(grid)) +
+                 join_units(static_cast<int>(items < 96 ? items : 96));
     const I work = w.by_items ? items : total;
     I ctas = w.by_items ? items : total / MIN_UNITS;
     ctas = ctas < 1 ? 1 : (ctas > grid ? grid : ctas);
@@ -565,8 +571,12 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
                 tmem_wait_ld();
                 if (edge) {
 #pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (((bits[c >> 5] >> (c & 31)) & 1u) == 0u) s[c] = -INFINITY;
+                    for (int w = 0; w < 4; ++w)
+                        if (__any_sync(0xffffffffu, bits[w] != 0xffffffffu)) {
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if ((bits[w] & (1u << c)) == 0u) s[32 * w + c] = -INFINITY;
+                        }
                 }
                 float mx[4] = {m, m, m, m};
 #pragma unroll
