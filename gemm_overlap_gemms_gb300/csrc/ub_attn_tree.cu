@@ -8,26 +8,28 @@
 //
 // Few rows over many keys: bound by HBM as long as the keys and values are read once. A q tile is
 // 128 rows, token by token and in a token the query heads of one key/value head (any number of
-// them up to 128: 128 / heads tokens). A work item is up to two q tiles of one sequence and
-// key/value head. The tensor core takes S = Q K^T (128 rows x 128 keys, from shared memory) and
+// them up to 128: 128 / heads tokens). A work item is up to two q tiles (in short calls one) of
+// one sequence and key/value head. The tensor core takes S = Q K^T (128 rows x 128 keys, from shared memory) and
 // O += P V (P from TMEM), and has two pipelines of S, softmax, P and O:
 //  - an item of one q tile gives them alternate key tiles, so that the chain S -> softmax -> P V
 //    of a tile (2200 cycles) hides behind the other's, and joins the two O in TMEM at its end;
 //  - an item of two q tiles gives each its q tile, and both take every key tile.
-// What a draft sees of the other drafts is found where it is needed, in the one or two key tiles
-// that hold drafts: a thread walks from its row's draft up its parents and sets a bit per key.
+// What a draft sees of the other drafts is found where it is needed, in the key tiles that hold
+// drafts: a thread walks from its row's draft up its parents and sets a bit per key. The last tile
+// comes first, so that the walk goes on from tile to tile and runs while the first keys are loaded.
 // So a tree may have any number of drafts, and nothing is prepared or kept between calls.
 //
 // Work split: the (item, key tile) pairs of the whole call are laid end to end and every CTA
 // takes an equal, contiguous range, found on the device from the starts and lengths, as in
-// ub_attn_decode.cu. The parts of an item that spans CTAs go to the workspace and are joined, in
-// CTA order, by all its CTAs, a share of the outputs each, once a counter says that all are there.
+// ub_attn_decode.cu; or every CTA takes whole items, where that costs less than the joins. The parts
+// of an item that spans CTAs go to the workspace and are joined, in CTA order, by all its CTAs, a
+// share of the outputs each, once a counter says that all are there.
 //
-// Measured (GB300): 32 sequences of 16 drafts over 8192 keys, 8 heads of 128 each way (1.07 GB): 171
-// us, 6.3 TB/s, HBM-bound; heads of 64 98 us, 5.5 TB/s (an item's end, 3-4 us, weighs more). With 64
-// drafts and 4 query heads to a key head, 256 rows on a key tile, 225 us (heads of 64: 164): a step
+// Measured (GB300): 32 sequences of 16 drafts over 8192 keys, 8 heads of 128 each way (1.07 GB): 169
+// us, 6.4 TB/s, HBM-bound; heads of 64 98 us, 5.5 TB/s (an item's end, 3-4 us, weighs more). With 64
+// drafts and 4 query heads to a key head, 256 rows on a key tile, 223 us (heads of 64: 164): a step
 // of both pipelines, 2300 cycles, as in ub_attn_prompt.cu. 16 sequences of 16-64 drafts, 72945 keys
-// (77 MB), 8 query heads on two: 38 us, of which 4 are schedule, 4 the first loads, 16 tiles, 4 the
+// (77 MB), 8 query heads on two: 37.4 us, of which 4 are schedule, 4 the first loads, 16 tiles, 4 the
 // wait for all parts, 5-9 the join. Four sequences of 3-12 drafts, 1534 keys: 11.4 us,
 // five dependent trips to memory, three key tiles and the output.
 //
