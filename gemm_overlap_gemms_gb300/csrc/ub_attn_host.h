@@ -32,6 +32,28 @@ struct Range {
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// A device array of 32-bit words: what a call writes may not overlap what it reads, or what else it
+// writes, as its CTAs do both at once.
+struct Words {
+    const char *name;
+    const void *data;
+    int64_t n;
+};
+inline bool overlap(const Words &a, const Words &b)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.data), y = reinterpret_cast<uintptr_t>(b.data);
+    return a.n > 0 && b.n > 0 && x < y + 4 * static_cast<uintptr_t>(b.n) && y < x + 4 * static_cast<uintptr_t>(a.n);
+}
+// Words from a table's first entry to its last.
+inline int64_t extent_of(int64_t rows, int64_t row, int64_t width) { return rows > 0 ? (rows - 1) * row + width : 0; }
+// `out` against each of `n` others.
+inline int check_apart(const char *fn, const Words &out, const Words *others, int n)
+{
+    for (int i = 0; i < n; ++i)
+        if (overlap(out, others[i])) return fail_call(UB_ERR_ARG, "%s: %s overlaps %s", fn, out.name, others[i].name);
+    return UB_OK;
+}
+
 inline int cuda_failed(cudaError_t e, const char *what)
 {
     return fail_call(UB_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));

@@ -10,15 +10,6 @@ using namespace ubk;
 
 namespace {
 
-bool overlap(const void *a, int64_t a_words, const void *b, int64_t b_words)
-{
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + 4 * static_cast<uintptr_t>(b_words) && y < x + 4 * static_cast<uintptr_t>(a_words);
-}
-
-// Words from a table's first entry to its last.
-int64_t extent_of(int64_t rows, int64_t row, int64_t width) { return rows > 0 ? (rows - 1) * row + width : 0; }
-
 int check_rows(const char *fn, const char *what, int64_t rows, int64_t row, int64_t width)
 {
     if (rows > 1 && (row < width || row > INT32_MAX))
@@ -26,6 +17,12 @@ int check_rows(const char *fn, const char *what, int64_t rows, int64_t row, int6
     if (rows > INT32_MAX || rows * width > INT32_MAX)
         return fail_call(UB_ERR_ARG, "%s: %s of %lld rows of %lld entries is too large", fn, what, (long long)rows, (long long)width);
     return UB_OK;
+}
+
+Words refs_of(const ub_pool_t &in) { return {"refs", in.refs, in.num_pages}; }
+Words table_of(const ub_pool_t &in)
+{
+    return {"page_table", in.page_table, extent_of(in.n_seqs, in.table_row, in.table_width)};
 }
 
 int check_pool(const char *fn, ub_handle_t h, const ub_pool_t *in)
@@ -43,7 +40,9 @@ int check_pool(const char *fn, ub_handle_t h, const ub_pool_t *in)
     if (in->num_pages > INT32_MAX || in->table_width > INT32_MAX || in->table_width * in->page_size > INT32_MAX - 256)
         return fail_call(UB_ERR_ARG, "%s: pool of %lld pages, table of %lld entries: too large", fn, (long long)in->num_pages,
                          (long long)in->table_width);
-    return check_rows(fn, "page_table", in->n_seqs, in->table_row, in->table_width);
+    if (int rc = check_rows(fn, "page_table", in->n_seqs, in->table_row, in->table_width)) return rc;
+    const Words table = table_of(*in);
+    return check_apart(fn, refs_of(*in), &table, 1);
 }
 
 // The device and the handle's state, the launch, and its timing.
@@ -78,6 +77,9 @@ int rows_call(const char *fn, ub_handle_t h, PoolOp op, const ub_pool_t *in, con
 {
     if (int rc = check_pool(fn, h, in)) return rc;
     if (!begin || !end) return fail_call(UB_ERR_ARG, "%s: begin or end is null", fn);
+    const Words inputs[] = {{"begin", begin, in->n_seqs}, {"end", end, in->n_seqs}};
+    if (int rc = check_apart(fn, refs_of(*in), inputs, 2)) return rc;
+    if (int rc = check_apart(fn, table_of(*in), inputs, 2)) return rc;
     PoolParams p;
     memset(&p, 0, sizeof p);
     p.n = in->n_seqs;
@@ -109,9 +111,13 @@ int ub_kv_fork(ub_handle_t h, const ub_pool_t *pool, const int32_t *kv_lens, con
     if (n_children == 0) return UB_OK;
     if (!kv_lens || !source || !new_table || !copies) return fail_call(UB_ERR_ARG, "%s: a null array", fn);
     if (int rc = check_rows(fn, "new_table", n_children, new_row, pool->table_width)) return rc;
-    const int64_t words = extent_of(n_children, new_row, pool->table_width);
-    if (overlap(new_table, words, pool->page_table, extent_of(pool->n_seqs, pool->table_row, pool->table_width)))
-        return fail_call(UB_ERR_ARG, "%s: new_table overlaps page_table", fn);
+    const Words arrays[] = {table_of(*pool),
+                            refs_of(*pool),
+                            {"kv_lens", kv_lens, pool->n_seqs},
+                            {"source", source, n_children},
+                            {"new_table", new_table, extent_of(n_children, new_row, pool->table_width)}};
+    if (int rc = check_apart(fn, arrays[4], arrays, 4)) return rc;
+    if (int rc = check_apart(fn, {"copies", copies, 2 * n_children}, arrays, 5)) return rc;
     PoolParams p;
     memset(&p, 0, sizeof p);
     p.n = n_children;
@@ -133,12 +139,20 @@ int ub_kv_compact(ub_handle_t h, const ub_pool_t *pool, int32_t *refs_out, int32
         return fail_call(UB_ERR_ARG, "%s: room for %lld moves of %lld pages: half as many are needed", fn, (long long)n_moves,
                          (long long)pool->num_pages);
     if (int rc = check_rows(fn, "table_out", pool->n_seqs, out_row, pool->table_width)) return rc;
-    const int64_t words = extent_of(pool->n_seqs, pool->table_row, pool->table_width);
+    // refs_out and table_out may be refs and page_table, whole.
     const bool same_table = table_out == pool->page_table && (pool->n_seqs == 1 || out_row == pool->table_row);
-    if (!same_table && overlap(table_out, extent_of(pool->n_seqs, out_row, pool->table_width), pool->page_table, words))
-        return fail_call(UB_ERR_ARG, "%s: table_out overlaps page_table and is not the same", fn);
-    if (refs_out != pool->refs && overlap(refs_out, pool->num_pages, pool->refs, pool->num_pages))
-        return fail_call(UB_ERR_ARG, "%s: refs_out overlaps refs and is not the same", fn);
+    const Words refs = refs_of(*pool), to_refs = {"refs_out", refs_out, pool->num_pages}, table = table_of(*pool);
+    const Words to_table = {"table_out", table_out, extent_of(pool->n_seqs, out_row, pool->table_width)};
+    const Words arrays[] = {refs, table, to_refs, to_table, {"moves", moves, 2 * n_moves}};
+    if (refs_out != pool->refs)
+        if (int rc = check_apart(fn, to_refs, &refs, 1)) return rc;
+    if (!same_table)
+        if (int rc = check_apart(fn, to_table, &table, 1)) return rc;
+    if (int rc = check_apart(fn, to_refs, &table, 1)) return rc;
+    if (int rc = check_apart(fn, to_table, &refs, 1)) return rc;
+    if (int rc = check_apart(fn, to_table, &to_refs, 1)) return rc;
+    if (int rc = check_apart(fn, arrays[4], arrays, 4)) return rc;
+    if (int rc = check_apart(fn, {"used", used, 1}, arrays, 5)) return rc;
     PoolParams p;
     memset(&p, 0, sizeof p);
     p.n = n_moves;

@@ -500,8 +500,8 @@ int ub_attn_decode_window(ub_handle_t h, const ub_attn_t *a, int32_t window, int
  * path a_0 < a_1 < .. < a_m = leaves[s] move from their places L_s + a_d to L_s + d, keys and
  * values, and new_lens[s] = L_s + m + 1 (L_s for no draft); other rows of the cache stay as they
  * are. It reads seq_starts, kv_lens, page_table and the cache's fields of ub_attn_t; `parents` has
- * n_tokens entries, whatever the active shape is now. new_lens must not overlap kv_lens: with a
- * cache for each layer, every layer's call takes the same lengths.
+ * n_tokens entries, whatever the active shape is now. new_lens must not overlap kv_lens (with a
+ * cache for each layer, every layer's call takes the same lengths) nor any other array it reads.
  *
  * Recorded in the sticky status (UB_ERR_ARG), besides what ub_kv_append lists: a parent outside
  * [-1, own place) (taken as -1), and in ub_kv_accept a leaf outside [-1, n_s), starts out of order
@@ -550,9 +550,10 @@ int ub_kv_accept(ub_handle_t h, const ub_attn_t *a, const int32_t *parents, int6
  * leaves it), freeing or sharing a page whose count is not above zero, rows to take outside the
  * table (cut), a source or a length out of range, a pair with one page outside the cache (skipped).
  *
- * One kernel each, on `stream`; take, fork and compact use the handle's workspace, so the
- * calls of a handle are ordered as the attention's are. Host errors: UB_ERR_ARG, UB_ERR_ZERO,
- * UB_ERR_ALIGN, UB_ERR_CUDA.
+ * An array that a call writes overlaps no other of its arrays (UB_ERR_ARG), but for the two pairs
+ * named at ub_kv_compact. One kernel each, on `stream`; take, fork and compact use the handle's
+ * workspace, so the calls of a handle are ordered as the attention's are. Host errors: UB_ERR_ARG,
+ * UB_ERR_ZERO, UB_ERR_ALIGN, UB_ERR_CUDA.
  */
 typedef struct {
     uint32_t size;       /* sizeof(ub_pool_t) */

@@ -253,6 +253,34 @@ def test_refused_calls(buf):
     assert refs.tolist() == pool.refs and table.tolist() == pool.table
 
 
+def test_overlapping_arrays_are_refused(buf):
+    """What a call writes among what it reads, or among what else it writes."""
+    pool = Pool(4, 10, 50)
+    refs, table = pool.device()
+    lens, source = ints(pool.lens), ints([0, 1])
+    new = torch.zeros(2, 10, dtype=torch.int32, device="cuda")
+    scratch = torch.zeros(200, dtype=torch.int32, device="cuda")
+    moves = scratch[:50].view(25, 2)
+    pairs = lambda t: t.reshape(-1)[:4].view(2, 2)
+    for bad in (lambda: buf.kv_take(refs, table, refs[:4], lens, 16), lambda: buf.kv_free(refs, table, lens, table[1, :4], 16),
+                lambda: buf.kv_free(refs, refs[:40].view(4, 10), lens, lens, 16),
+                lambda: buf.kv_fork(refs, table, lens, source, new, 16, copies=pairs(new)),
+                lambda: buf.kv_fork(refs, table, lens, source, new, 16, copies=pairs(refs)),
+                lambda: buf.kv_fork(refs, table, lens, source, new, 16, copies=pairs(table)),
+                lambda: buf.kv_fork(refs, table, lens, source, new, 16, copies=pairs(lens)),
+                lambda: buf.kv_fork(refs, table, lens, source, refs[:20].view(2, 10), 16),
+                lambda: buf.kv_fork(refs, table, lens, pairs(new)[0], new, 16),
+                lambda: buf.kv_compact(refs, table, moves=moves, used=scratch[49:50]),
+                lambda: buf.kv_compact(refs, table, refs_out=scratch[:50], moves=moves),
+                lambda: buf.kv_compact(refs, table, table_out=scratch[10:50].view(4, 10), refs_out=scratch[:50]),
+                lambda: buf.kv_compact(refs, table, moves=moves, used=refs[:1]),
+                lambda: buf.kv_compact(refs, table, moves=moves, used=table[0, :1])):
+        with pytest.raises(ub.UbError):
+            bad()
+    status(buf)
+    assert refs.tolist() == pool.refs and table.tolist() == pool.table and not scratch.any() and not new.any()
+
+
 def test_forked_drafted_decoding(buf):
     """The operators together, as a server uses them: a prompt forked into candidates, each with its
     own drafts, verified, the accepted ones kept, pages taken, given up and moved together; against

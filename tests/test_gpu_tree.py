@@ -406,3 +406,14 @@ def test_accept_refuses_lengths_in_place(buf):
         buf.kv_accept(b.k_cache, b.v_cache, b.starts, b.lens, b.table, parents, leaves, new_lens=b.lens)
     with pytest.raises((TypeError, ValueError)):
         buf.kv_accept(b.k_cache, b.v_cache, b.starts, b.lens, b.table, parents.long(), leaves)
+
+
+def test_accept_refuses_what_it_reads_as_new_lengths(buf):
+    b = ref.Batch([6, 2], [50, 9], page=16, kv_heads=1, dim=64)
+    _, parents = trees(b)
+    leaves = torch.zeros(2, dtype=torch.int32, device="cuda")
+    for new_lens in (leaves, b.starts[:2], b.starts[1:], parents[:2], parents[-2:], b.table.view(-1)[:2], b.lens):
+        with pytest.raises(ub.UbError):
+            buf.kv_accept(b.k_cache, b.v_cache, b.starts, b.lens, b.table, parents, leaves, new_lens=new_lens)
+    ok(buf)
+    assert leaves.tolist() == [0, 0] and b.lens.tolist() == [50, 9]
