@@ -15,9 +15,9 @@
 //    of a tile (2200 cycles) hides behind the other's, and joins the two O in TMEM at its end;
 //  - an item of two q tiles gives each its q tile, and both take every key tile.
 // What a draft sees of the other drafts is found where it is needed, in the key tiles that hold
-// drafts: a thread walks from its row's draft up its parents and sets a bit per key. The last tile
-// comes first, so that the walk goes on from tile to tile and runs while the first keys are loaded.
-// So a tree may have any number of drafts, and nothing is prepared or kept between calls.
+// drafts: a bit per key, from the parents of 32 drafts at a time. The last tile comes first, so that a
+// row's path goes on from tile to tile, and is looked up while the first keys are loaded. So a tree may
+// have any number of drafts, and nothing is prepared or kept between calls.
 //
 // Work split: the (item, key tile) pairs of the whole call are laid end to end and every CTA
 // takes an equal, contiguous range, found on the device from the starts and lengths, as in
@@ -331,7 +331,7 @@ struct Item {
     int lo, near, far;
     int t0, todo;    // key tiles in sight: the first one, how many (0: the item has no keys)
     int whole;       // all of the item's
-    // The last keys first: a row's path, which is walked from its own draft up, is then walked once.
+    // The last keys first: a row's path, which goes from its own draft up, is then taken once.
     __device__ __forceinline__ int tile(int j) const
     {
         const int t = t0 + todo - 1 - j;
@@ -347,39 +347,77 @@ struct Pending {
 // The low `n` bits (n may be below zero or past 32).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
 
-// The draft that draft i of a sequence follows, -1: the text.
-__device__ __forceinline__ int parent_of(const TreeParams &p, int start, int i)
+// A row's way along its path: the next draft of it that no tile so far has held (below zero: none
+// left), and how many came before that one, the row's own among them.
+struct Path {
+    int draft, steps;
+};
+// Which of the 128 keys from key0 on each row of a warp sees; start: the token of the sequence's first
+// draft, text: keys before its n drafts. The drafts are taken a word of 32 keys at a time, from the last:
+// a lane has one of them, its ancestors within the word come from doubling steps along the parents,
+// and the rows on it read them there and go on with the first ancestor before the word. So a path
+// costs a few steps per word, however long it is (48 sequences, chains of 7-51 drafts in a window, 8
+// heads: 27.7 us; each row walking by itself, a trip to memory for each ancestor: 40.4. One chain of
+// 16384 drafts: 1.8 and 7.0 ms).
+__device__ __forceinline__ void keys_seen(const TreeParams &p, int start, int n, int text, Path &path, int key0, int lane, uint32_t *bits)
 {
-    const int up = p.parents[start + i];
-    if (up >= -1 && up < i) return up;
-    atomicCAS(p.b.status, 0, UB_ERR_ARG);
-    return -1;
-}
-
-// Which of the 128 keys from key0 on a row at position `pos` sees; start: the token of the
-// sequence's first draft, text: keys before the drafts. `i` is the first draft of the row's path that
-// no tile behind this one holds (below zero: none), `d` how far it is from the row's own; both go on.
-__device__ __forceinline__ void keys_seen(const TreeParams &p, int start, int text, int &i, int &d, int pos, int key0, uint32_t *bits)
-{
+    const int gone = key0 - text;  // drafts before this tile
+    // A row's position is needed where its window ends; drafts further from it than that lie in
+    // such tiles, too.
+    const bool ends = p.window > 0 && key0 <= text + n - p.window;
+    int pos = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) bits[w] = 0u;
+#pragma unroll 1
+    for (int pass = ends ? 0 : 1; pass < 2; ++pass) {  // to the end of the path, for the position; this tile's
+        int i = path.draft, d = path.steps;
+        const int low = pass == 0 || gone < 0 ? 0 : gone;
+#pragma unroll 1
+        for (;;) {
+            const int top = __reduce_max_sync(0xffffffffu, i);
+            if (top < low) break;
+            const int from = gone + ((top - gone) & ~31), word = (from - gone) >> 5;
+            const int least = from > 0 ? from : 0, mine = from + lane;  // the word's first draft, the lane's
+            int up = mine >= 0 && mine < n ? p.parents[start + mine] : -1;
+            if (up < -1 || (up >= mine && up >= 0)) {  // it does not come before its child: the text
+                atomicCAS(p.b.status, 0, UB_ERR_ARG);
+                up = -1;
+            }
+            uint32_t held = 1u << lane;
+#pragma unroll
+            for (int twice = 0; twice < 5 && __any_sync(0xffffffffu, up >= least); ++twice) {
+                const uint32_t h = __shfl_sync(0xffffffffu, held, (up - from) & 31);
+                const int u = __shfl_sync(0xffffffffu, up, (up - from) & 31);
+                if (up >= least) held |= h, up = u;
+            }
+            const int at = i - from;
+            held = __shfl_sync(0xffffffffu, held, at & 31);
+            up = __shfl_sync(0xffffffffu, up, at & 31);
+            if (i < least) continue;
+            uint32_t see = pass == 1 ? held : 0u;
+            if (p.window > 0 && word < 4 && d + __popc(held) > p.window)  // a path that leaves the window
+                for (uint32_t rest = see, k = d; rest != 0u; ++k) {
+                    const uint32_t last = 0x80000000u >> __clz(rest);
+                    rest ^= last;
+                    if (static_cast<int>(k) >= p.window && pos - static_cast<int>(k) >= p.sinks) see ^= last;
+                }
+#pragma unroll
+            for (int w = 0; w < 4; ++w) bits[w] |= w == word ? see : 0u;
+            d += __popc(held);
+            i = up < least ? up : -1;                  // (always below: 32 drafts are five steps)
+        }
+        if (pass == 0)
+            pos = text + d - 1;
+        else
+            path = Path{i, d};
+    }
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
         const int first = key0 + 32 * w;
-        bits[w] = low_bits(text - first);
-        if (p.window > 0) bits[w] &= ~low_bits(pos - p.window + 1 - first) | low_bits(p.sinks - first);
+        uint32_t old = low_bits(text - first);
+        if (ends) old &= ~low_bits(pos - p.window + 1 - first) | low_bits(p.sinks - first);
+        bits[w] |= old;
     }
-    // The ancestors come in falling order: word by word, from the last.
-    const int gone = key0 - text;  // drafts before this tile
-    if (gone + KEYS <= 0) return;  // no drafts in it (the same for all lanes)
-    for (; i >= gone + KEYS; ++d) i = parent_of(p, start, i);
-#pragma unroll
-    for (int w = 3; w >= 0; --w) {
-        const int from = gone + 32 * w, least = from > -text ? from : -text;  // (below -text: before the cache)
-        for (; i >= 0 && i >= least; ++d) {
-            if (p.window == 0 || d < p.window || pos - d < p.sinks) bits[w] |= 1u << ((i - from) & 31);
-            i = parent_of(p, start, i);
-        }
-    }
-    __syncwarp();
 }
 
 __device__ __forceinline__ void store_lse(const TreeParams &p, int64_t token, int head, float m, float l)
@@ -550,20 +588,15 @@ __global__ void __launch_bounds__(TR_THREADS, 1) ub_attn_tree_kernel(const __gri
             const bool two = it.ntok > p.tokens;
             const int token = (two ? i * p.tokens : 0) + row_token;  // of the item
             const bool real = row_token < p.tokens && token < it.ntok;
-            const int draft = real ? it.first + token : -1;
-            int pos = it.text;
-            if (p.window > 0 && draft >= 0)
-                for (int up = parent_of(p, it.row0 - it.first, draft); up >= 0; up = parent_of(p, it.row0 - it.first, up)) ++pos;
-            __syncwarp();
+            Path path{real ? it.first + token : -1, 0};
             float m = -INFINITY, l = 0.f;
-            int up = draft, steps = 0;                 // on the row's path
             for (int j = two ? 0 : i; j < todo; j += two ? 1 : 2) {
                 // Some row does not see all of the tile: drafts, or keys left of a window. The walks run
                 // while S is computed.
                 const int key0 = it.tile(j) * KEYS;
                 const bool edge = key0 + KEYS > it.text || (p.window > 0 && key0 <= it.len - p.window && key0 + KEYS > p.sinks);
                 uint32_t bits[4];
-                if (edge) keys_seen(p, it.row0 - it.first, it.text, up, steps, pos, key0, bits);
+                if (edge) keys_seen(p, it.row0 - it.first, it.len - it.text, it.text, path, key0, lane, bits);
                 if (!wait(s_full + 8 * i, n_s & 1)) break;
                 ++n_s;
                 tc_fence_after();
