@@ -25,12 +25,12 @@
 // of an item that spans CTAs go to the workspace and are joined, in CTA order, by all its CTAs, a
 // share of the outputs each, once a counter says that all are there.
 //
-// Measured (GB300): 32 sequences of 16 drafts over 8192 keys, 8 heads of 128 each way (1.07 GB): 169
-// us, 6.4 TB/s, HBM-bound; heads of 64 98 us, 5.5 TB/s (an item's end, 3-4 us, weighs more). With 64
-// drafts and 4 query heads to a key head, 256 rows on a key tile, 223 us (heads of 64: 164): a step
+// Measured (GB300): 32 sequences of 16 drafts over 8192 keys, 8 heads of 128 each way (1.07 GB): 170
+// us, 6.3 TB/s, HBM-bound; heads of 64 98 us, 5.5 TB/s (an item's end, 3-4 us, weighs more). With 64
+// drafts and 4 query heads to a key head, 256 rows on a key tile, 230 us (heads of 64: 161): a step
 // of both pipelines, 2300 cycles, as in ub_attn_prompt.cu. 16 sequences of 16-64 drafts, 72945 keys
-// (77 MB), 8 query heads on two: 37.4 us, of which 4 are schedule, 4 the first loads, 16 tiles, 4 the
-// wait for all parts, 5-9 the join. Four sequences of 3-12 drafts, 1534 keys: 11.4 us,
+// (77 MB), 8 query heads on two: 38 us, of which 4 are schedule, 4 the first loads, 16 tiles, 4 the
+// wait for all parts, 5-9 the join. Four sequences of 3-12 drafts, 1534 keys: 11 us,
 // five dependent trips to memory, three key tiles and the output.
 //
 // Roles (12 warps, one CTA per SM):
