@@ -317,6 +317,25 @@ def test_append_of_a_chain_is_the_plain_one(buf):
     assert torch.equal(one, two) and all(torch.equal(x, y) for x, y in zip(*caches))
 
 
+@pytest.mark.parametrize("new,past", [([300, 33, 64, 1, 32], [5, 0, 90, 3, 31]), ([1500], [100]), ([31, 32, 33, 65] * 9, [7] * 36)])
+def test_append_and_attention_of_deep_chains(buf, new, past):
+    """Chains past a word of 32 drafts: what the plain calls compute."""
+    kv = [n + k for n, k in zip(new, past)]
+    b = ref.Batch(new, kv, page=16, kv_heads=2, dim=128, pad=3, seed=2)
+    buf.set_active_shape([b.T, 256])
+    _, parents = trees(b, "chain")
+    q, k, v = b.randn(b.T, 8, 128), b.randn(b.T, 2, 128), b.randn(b.T, 2, 128)
+    angle = torch.rand(2000, 64, generator=b.gen, device="cuda") * 6
+    args = (q, k, v, angle.cos(), angle.sin(), b.starts, b.lens, b.table)
+    caches = [(b.k_cache.clone(), b.v_cache.clone()) for _ in range(2)]
+    n = sum(new)
+    one, two = buf.kv_append(*args, *caches[0])[:n], buf.kv_append(*args, *caches[1], parents=parents)[:n]
+    ok(buf)
+    assert torch.equal(one, two) and all(torch.equal(x, y) for x, y in zip(*caches))
+    for window, sinks in ((0, 0), (50, 2), (200, 0)):
+        run(buf, b, 8, 128, "chain", window=window, sinks=sinks)
+
+
 # ---------------------------------------------------------------- accept
 
 def check_accept(b, per, leaves, before, new_lens):
