@@ -116,6 +116,7 @@ int ub_kv_fork(ub_handle_t h, const ub_pool_t *pool, const int32_t *kv_lens, con
                             {"kv_lens", kv_lens, pool->n_seqs},
                             {"source", source, n_children},
                             {"new_table", new_table, extent_of(n_children, new_row, pool->table_width)}};
+    if (int rc = check_apart(fn, arrays[1], arrays + 2, 2)) return rc;  // (lengths and sources are read twice)
     if (int rc = check_apart(fn, arrays[4], arrays, 4)) return rc;
     if (int rc = check_apart(fn, {"copies", copies, 2 * n_children}, arrays, 5)) return rc;
     PoolParams p;
