@@ -539,12 +539,10 @@ int ub_kv_accept(ub_handle_t h, const ub_attn_t *in, const int32_t *parents, int
     if (int rc = check_cache_sizes(fn, &a)) return rc;
     if (int rc = check_table(fn, a)) return rc;
     if (int rc = check_caches(fn, &a)) return rc;
-    const Words inputs[] = {{"kv_lens", a.kv_lens, a.n_seqs},
-                            {"leaves", leaves, a.n_seqs},
-                            {"seq_starts", a.seq_starts, static_cast<int64_t>(a.n_seqs) + 1},
-                            {"parents", parents, n_tokens},
-                            {"page_table", a.page_table, extent_of(a.n_seqs, a.table_row, a.table_width)}};
-    if (int rc = check_apart(fn, {"new_lens", new_lens, a.n_seqs}, inputs, 5)) return rc;
+    const Words inputs[] = {words("kv_lens", a.kv_lens, a.n_seqs), words("leaves", leaves, a.n_seqs),
+                            words("seq_starts", a.seq_starts, static_cast<int64_t>(a.n_seqs) + 1), words("parents", parents, n_tokens),
+                            rows_of("page_table", a.page_table, a.n_seqs, a.table_row, a.table_width)};
+    if (int rc = check_apart(fn, words("new_lens", new_lens, a.n_seqs), inputs, 5)) return rc;
     if (static_cast<int64_t>(a.n_seqs) * ((2 * static_cast<int64_t>(a.kv_heads) * a.head_dim / 8 + 127) / 128) > INT32_MAX)
         return fail_call(UB_ERR_ARG, "%s: %d sequences of %d heads are too many", fn, a.n_seqs, a.kv_heads);
     DeviceScope g(handle_device(h));

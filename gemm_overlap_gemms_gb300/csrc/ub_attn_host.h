@@ -32,20 +32,35 @@ struct Range {
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// A device array of 32-bit words: what a call writes may not overlap what it reads, or what else it
-// writes, as its CTAs do both at once.
+// A device array of 32-bit words, or rows of them, `pitch` words apart (as wide or wider, where there
+// are several): what a call writes may not overlap what it reads, or what else it writes, as its CTAs
+// do both at once.
 struct Words {
     const char *name;
     const void *data;
-    int64_t n;
+    int64_t width, rows, pitch;
 };
+inline Words words(const char *name, const void *data, int64_t n) { return {name, data, n, 1, n}; }
+inline Words rows_of(const char *name, const void *data, int64_t rows, int64_t pitch, int64_t width)
+{
+    return {name, data, width, rows, rows > 1 ? pitch : width};
+}
+// Whether a word belongs to both. Rows of one table may lie between rows of the other.
 inline bool overlap(const Words &a, const Words &b)
 {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a.data), y = reinterpret_cast<uintptr_t>(b.data);
-    return a.n > 0 && b.n > 0 && x < y + 4 * static_cast<uintptr_t>(b.n) && y < x + 4 * static_cast<uintptr_t>(a.n);
+    if (a.rows > b.rows) return overlap(b, a);
+    if (a.width <= 0 || a.rows <= 0 || b.width <= 0) return false;
+    const int64_t pitch_a = 4 * a.pitch, pitch_b = 4 * b.pitch, wide_a = 4 * a.width, wide_b = 4 * b.width;
+    // first byte of a row of `a`, counted from the first of `b`
+    int64_t x = static_cast<int64_t>(reinterpret_cast<uintptr_t>(a.data) - reinterpret_cast<uintptr_t>(b.data));
+    if (x >= (b.rows - 1) * pitch_b + wide_b || x + (a.rows - 1) * pitch_a + wide_a <= 0) return false;
+    for (int64_t r = 0; r < a.rows; ++r, x += pitch_a) {
+        if (x + wide_a <= 0) continue;
+        const int64_t last = (x + wide_a - 1) / pitch_b;  // the last row of `b` that begins before this one's end
+        if ((last < b.rows ? last : b.rows - 1) * pitch_b + wide_b > x) return true;
+    }
+    return false;
 }
-// Words from a table's first entry to its last.
-inline int64_t extent_of(int64_t rows, int64_t row, int64_t width) { return rows > 0 ? (rows - 1) * row + width : 0; }
 // `out` against each of `n` others.
 inline int check_apart(const char *fn, const Words &out, const Words *others, int n)
 {

@@ -19,10 +19,10 @@ int check_rows(const char *fn, const char *what, int64_t rows, int64_t row, int6
     return UB_OK;
 }
 
-Words refs_of(const ub_pool_t &in) { return {"refs", in.refs, in.num_pages}; }
+Words refs_of(const ub_pool_t &in) { return words("refs", in.refs, in.num_pages); }
 Words table_of(const ub_pool_t &in)
 {
-    return {"page_table", in.page_table, extent_of(in.n_seqs, in.table_row, in.table_width)};
+    return rows_of("page_table", in.page_table, in.n_seqs, in.table_row, in.table_width);
 }
 
 int check_pool(const char *fn, ub_handle_t h, const ub_pool_t *in)
@@ -77,7 +77,7 @@ int rows_call(const char *fn, ub_handle_t h, PoolOp op, const ub_pool_t *in, con
 {
     if (int rc = check_pool(fn, h, in)) return rc;
     if (!begin || !end) return fail_call(UB_ERR_ARG, "%s: begin or end is null", fn);
-    const Words inputs[] = {{"begin", begin, in->n_seqs}, {"end", end, in->n_seqs}};
+    const Words inputs[] = {words("begin", begin, in->n_seqs), words("end", end, in->n_seqs)};
     if (int rc = check_apart(fn, refs_of(*in), inputs, 2)) return rc;
     if (int rc = check_apart(fn, table_of(*in), inputs, 2)) return rc;
     PoolParams p;
@@ -113,12 +113,12 @@ int ub_kv_fork(ub_handle_t h, const ub_pool_t *pool, const int32_t *kv_lens, con
     if (int rc = check_rows(fn, "new_table", n_children, new_row, pool->table_width)) return rc;
     const Words arrays[] = {table_of(*pool),
                             refs_of(*pool),
-                            {"kv_lens", kv_lens, pool->n_seqs},
-                            {"source", source, n_children},
-                            {"new_table", new_table, extent_of(n_children, new_row, pool->table_width)}};
+                            words("kv_lens", kv_lens, pool->n_seqs),
+                            words("source", source, n_children),
+                            rows_of("new_table", new_table, n_children, new_row, pool->table_width)};
     if (int rc = check_apart(fn, arrays[1], arrays + 2, 2)) return rc;  // (lengths and sources are read twice)
     if (int rc = check_apart(fn, arrays[4], arrays, 4)) return rc;
-    if (int rc = check_apart(fn, {"copies", copies, 2 * n_children}, arrays, 5)) return rc;
+    if (int rc = check_apart(fn, words("copies", copies, 2 * n_children), arrays, 5)) return rc;
     PoolParams p;
     memset(&p, 0, sizeof p);
     p.n = n_children;
@@ -142,9 +142,9 @@ int ub_kv_compact(ub_handle_t h, const ub_pool_t *pool, int32_t *refs_out, int32
     if (int rc = check_rows(fn, "table_out", pool->n_seqs, out_row, pool->table_width)) return rc;
     // refs_out and table_out may be refs and page_table, whole.
     const bool same_table = table_out == pool->page_table && (pool->n_seqs == 1 || out_row == pool->table_row);
-    const Words refs = refs_of(*pool), to_refs = {"refs_out", refs_out, pool->num_pages}, table = table_of(*pool);
-    const Words to_table = {"table_out", table_out, extent_of(pool->n_seqs, out_row, pool->table_width)};
-    const Words arrays[] = {refs, table, to_refs, to_table, {"moves", moves, 2 * n_moves}};
+    const Words refs = refs_of(*pool), to_refs = words("refs_out", refs_out, pool->num_pages), table = table_of(*pool);
+    const Words to_table = rows_of("table_out", table_out, pool->n_seqs, out_row, pool->table_width);
+    const Words arrays[] = {refs, table, to_refs, to_table, words("moves", moves, 2 * n_moves)};
     if (refs_out != pool->refs)
         if (int rc = check_apart(fn, to_refs, &refs, 1)) return rc;
     if (!same_table)
@@ -153,7 +153,7 @@ int ub_kv_compact(ub_handle_t h, const ub_pool_t *pool, int32_t *refs_out, int32
     if (int rc = check_apart(fn, to_table, &refs, 1)) return rc;
     if (int rc = check_apart(fn, to_table, &to_refs, 1)) return rc;
     if (int rc = check_apart(fn, arrays[4], arrays, 4)) return rc;
-    if (int rc = check_apart(fn, {"used", used, 1}, arrays, 5)) return rc;
+    if (int rc = check_apart(fn, words("used", used, 1), arrays, 5)) return rc;
     PoolParams p;
     memset(&p, 0, sizeof p);
     p.n = n_moves;
