@@ -141,8 +141,9 @@ struct Entries {
 __device__ __forceinline__ Entries take_range(const PoolParams &p, int s)
 {
     const int64_t b = p.begin[s], e = p.end[s], cap = static_cast<int64_t>(p.width) << p.page_shift;
+    if (e <= b) return Entries{0, 0};  // no rows, wherever they would be
     if (b < 0 || e > cap) report(p.status, UB_ERR_ARG);
-    if (e <= b || e <= 0 || b >= cap) return Entries{0, 0};
+    if (e <= 0 || b >= cap) return Entries{0, 0};
     return Entries{(b < 0 ? 0 : b) >> p.page_shift, ((e > cap ? cap : e) + (int64_t(1) << p.page_shift) - 1) >> p.page_shift};
 }
 
