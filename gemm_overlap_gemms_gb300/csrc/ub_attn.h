@@ -210,6 +210,7 @@ struct AcceptParams {
     int32_t *new_lens;
     int tokens;                   // entries of parents
     int kv_heads, head_dim;
+    int caches;                   // 2; 1: k_cache and v_cache are one
     int parts;                    // CTAs per sequence
     int pdl;
 };

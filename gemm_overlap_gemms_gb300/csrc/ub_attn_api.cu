@@ -543,6 +543,11 @@ int ub_kv_accept(ub_handle_t h, const ub_attn_t *in, const int32_t *parents, int
                             words("seq_starts", a.seq_starts, static_cast<int64_t>(a.n_seqs) + 1), words("parents", parents, n_tokens),
                             rows_of("page_table", a.page_table, a.n_seqs, a.table_row, a.table_width)};
     if (int rc = check_apart(fn, words("new_lens", new_lens, a.n_seqs), inputs, 5)) return rc;
+    // One cache for keys and values moves once: twice, in CTAs of their own, the one's rows would be
+    // loaded from where the other has stored.
+    const bool one = a.k_cache.data == a.v_cache.data;
+    if (one && (a.k_cache.page != a.v_cache.page || a.k_cache.head != a.v_cache.head || a.k_cache.row != a.v_cache.row))
+        return fail_call(UB_ERR_ARG, "%s: k_cache and v_cache are two views of one array", fn);
     if (static_cast<int64_t>(a.n_seqs) * ((2 * static_cast<int64_t>(a.kv_heads) * a.head_dim / 8 + 127) / 128) > INT32_MAX)
         return fail_call(UB_ERR_ARG, "%s: %d sequences of %d heads are too many", fn, a.n_seqs, a.kv_heads);
     DeviceScope g(handle_device(h));
@@ -559,6 +564,7 @@ int ub_kv_accept(ub_handle_t h, const ub_attn_t *in, const int32_t *parents, int
     p.leaves = leaves;
     p.new_lens = new_lens;
     p.tokens = static_cast<int>(n_tokens);
+    p.caches = one ? 1 : 2;
     p.pdl = c.pdl;
     bool timed = false;
     if (int rc = handle_prof_start(h, UB_OP_KV_ACCEPT, s, &timed)) return rc;

@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(ACCEPT_THREADS) ub_kv_accept_kernel(const __gr
     if (m == 0) return;
 
     const int col = part * ACCEPT_THREADS + tid;
-    if (col >= 2 * p.kv_heads * (D / 8)) return;
+    if (col >= p.caches * p.kv_heads * (D / 8)) return;
     const bool is_v = col >= p.kv_heads * (D / 8);
     const int c = is_v ? col - p.kv_heads * (D / 8) : col;
     const int64_t page_stride = is_v ? p.vc_page : p.kc_page, row_stride = is_v ? p.vc_row : p.kc_row;
@@ -527,7 +527,7 @@ cudaError_t launch_kv_copy(const PageCopyParams &p, cudaStream_t s)
 
 cudaError_t launch_kv_accept(AcceptParams p, cudaStream_t s)
 {
-    p.parts = (2 * p.kv_heads * p.head_dim / 8 + ACCEPT_THREADS - 1) / ACCEPT_THREADS;
+    p.parts = (p.caches * p.kv_heads * p.head_dim / 8 + ACCEPT_THREADS - 1) / ACCEPT_THREADS;
     return launch_ex(p.head_dim == 128 ? ub_kv_accept_kernel<128> : ub_kv_accept_kernel<64>, p, p.b.n_seqs * p.parts,
                      ACCEPT_THREADS, 0, 1, p.pdl != 0, s);
 }

@@ -502,6 +502,7 @@ int ub_attn_decode_window(ub_handle_t h, const ub_attn_t *a, int32_t window, int
  * are. It reads seq_starts, kv_lens, page_table and the cache's fields of ub_attn_t; `parents` has
  * n_tokens entries, whatever the active shape is now. new_lens must not overlap kv_lens (with a
  * cache for each layer, every layer's call takes the same lengths) nor any other array it reads.
+ * k_cache and v_cache are two arrays, or one and the same (the same strides, too: UB_ERR_ARG).
  *
  * Recorded in the sticky status (UB_ERR_ARG), besides what ub_kv_append lists: a parent outside
  * [-1, own place) (taken as -1), and in ub_kv_accept a leaf outside [-1, n_s), starts out of order
