@@ -318,8 +318,8 @@ struct Schedule {
 // Few rows over many keys (a call of fewer items than CTAs): items of more than `limit` key
 // tiles are cut into `pieces` pieces each, as even as the number of CTAs allows, which is one
 // piece or whole item for each: the pieces' CTAs then join their item together. With more
-// items than CTAs nothing is split, nor where no item has more than MIN_SPLIT key tiles: the
-// join takes about 6 us, a key tile 1.1 (four chunks of 16 tokens, 12 query and 4 key/value
+// items than CTAs nothing is split (windows: the last round may be, see plan_of), nor where no item
+// has more than MIN_SPLIT key tiles: the join takes about 6 us, a key tile 1.1 (four chunks of 16 tokens, 12 query and 4 key/value
 // heads of 128, split against whole: 1280 keys 21.2 and 18.2 us, 1536 keys 20.3 and 20.5, 2048
 // keys 21.9 and 25.1, 4096 keys 28.4 and 44.0).
 struct Plan {
@@ -346,8 +346,8 @@ __device__ Plan plan_of(const Schedule &sc, int units, int ctas, int slots, int 
     if (pl.total >= static_cast<uint32_t>(ctas)) {
         // Windows make items of one length, of which one more than fill the CTAs takes as long as
         // twice as many: the items of an incomplete last round are split where two CTAs or more can
-        // share each of them and they have more than MIN_SPLIT key tiles (of one or two rounds: of
-        // more rounds the last is a small part).
+        // share each of them and the longest of them reaches more than MIN_SPLIT key tiles, in sight or
+        // not (of one or two rounds: of more rounds the last is a small part).
         const uint32_t rounds = pl.total / ctas, left = pl.total - rounds * ctas;
         if (!WINDOW || rounds > 2u || left == 0u) return pl;
         uint32_t pieces = static_cast<uint32_t>(ctas) / left;

@@ -10,11 +10,16 @@
 // CTAs: each counts its eighth of the pool with ballots, the counts are exchanged through
 // distributed shared memory, and what passes from CTA to CTA otherwise (the list of free pages,
 // the moves) goes through the handle's workspace between two cluster barriers. No CTA waits for
-// one of another launch, and a call is one launch: it is bound by its latency (five dependent
-// trips to memory and two to four barriers).
+// one of another launch, and a call is one launch. On rows of up to some hundred entries it is bound
+// by its latency: five dependent trips to memory and two cluster barriers (compact: three). Beyond,
+// take and fork are bound by the walk along a row, which one warp does, 32 entries at a time and none
+// ahead (a CTA has 32 rows at least, so few rows leave most CTAs idle). One sequence, pages of 16
+// rows, between events that add about 5 us: 256 entries fork 15 and take 13 us, 1024 entries 29 and 23,
+// 8192 entries (131072 tokens) 177 and 124, where free, dealt over the GPU, takes 7 and compact, whose
+// entries all 8 CTAs share, 15. 16 sequences and 64 children of 8192 entries: 203, 169, 7 and 40.
 //
-// Copies are bound by HBM: a CTA moves 16 KB, four 16-byte vectors in flight per thread, eight CTAs
-// on an SM, and the GPU deals the CTAs. CTAs that run together have the same part of many pages:
+// Copies are bound by HBM: a CTA moves 16 KB, four 16-byte vectors in flight per thread, six CTAs
+// on an SM (40 registers a thread), and the GPU deals the CTAs. CTAs that run together have the same part of many pages:
 // children of one parent, wherever they stand in the list, then find its rows in L2. 508 copies of
 // the last pages of 64 parents, 512 KB each (267 MB written, 34 MB of sources): 55 us; page by page
 // 75, and on a grid of 8 CTAs per SM, whose last round is not full, 82. 206 MB of pages moved
@@ -417,6 +422,11 @@ __global__ void __launch_bounds__(COPY_THREADS) ub_kv_copy_kernel(const __grid_c
     }
 }
 
+// Bound by latency: 64 registers leave room for 8 CTAs on an SM, so that 256 sequences of 8 heads of 128
+// (2048 CTAs) come in two rounds; a thread looks up two page ids for every row before it loads it,
+// and the loads of some rows follow the stores of the last ones (14.5 us for 52 MB; the path, which one
+// lane walks in shared memory, has at most 34 drafts there).
+//
 // A CTA moves 128 of a sequence's 16-byte columns ([k, v][head][D / 8]), the rows of the path in
 // rising order. Draft a_d of the path goes to place d <= a_d: a thread loads some rows of its
 // column and then stores them, and never overwrites a row that it has yet to load, because the

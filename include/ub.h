@@ -552,9 +552,10 @@ int ub_kv_accept(ub_handle_t h, const ub_attn_t *a, const int32_t *parents, int6
  * table (cut), a source or a length out of range, a pair with one page outside the cache (skipped).
  *
  * An array that a call writes overlaps no other of its arrays (UB_ERR_ARG), but for the two pairs
- * named at ub_kv_compact. One kernel each, on `stream`; take, fork and compact use the handle's
- * workspace, so the calls of a handle are ordered as the attention's are. Host errors: UB_ERR_ARG,
- * UB_ERR_ZERO, UB_ERR_ALIGN, UB_ERR_CUDA.
+ * named at ub_kv_compact; rows of one table may lie between those of another. One kernel each, on
+ * `stream`; take, fork and compact use the handle's workspace, so the calls of a handle are ordered as
+ * the attention's are, and a pool has at most 65536 pages for every SM of the GPU (compact: 32768;
+ * UB_ERR_ARG). Host errors: UB_ERR_ARG, UB_ERR_ZERO, UB_ERR_ALIGN, UB_ERR_CUDA.
  */
 typedef struct {
     uint32_t size;       /* sizeof(ub_pool_t) */
